@@ -342,6 +342,164 @@ bl_status bl_signsgd_apply(const uint32_t* sign_words, int ranks, void* W, bl_dt
                            void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Training operators next to the BitLinear layer: what a decoder LM trained
+ * with BitLinear layers runs outside its ternary projections. The pages give
+ * no such operators ("bitnet-qat-train", Measured behavior, Training, trains
+ * a 4-layer transformer LM around the layer); they follow the definitions
+ * given at each call.
+ */
+
+/*
+ * X1 -- the LM head and its softmax cross-entropy, without keeping the logits:
+ *
+ *   z[m,v]  = sum_k h[m,k] * W[v,k]                       fp32 accumulate
+ *   lse[m]  = log sum_v exp(z[m,v])
+ *   loss[m] = lse[m] - z[m, targets[m]]
+ *
+ * h [M,K] bf16, W [V,K] bf16, targets [M] int64; loss [M], lse [M] float
+ * outputs. A target outside 0..V-1 marks a token that is left out (padding, a
+ * prompt): its loss is 0; its lse is written like any other's. One token's
+ * values never reach another's, so what a left-out token's row of h holds
+ * (infinities and NaN included) does not matter.
+ * workspace: at least bl_linear_xent_forward_workspace_size(M,V,K) bytes,
+ * 16-byte aligned, no initialisation, one call at a time per workspace: one
+ * (maximum, sum) pair per token and 256 vocabulary entries, never the logits.
+ * Limits: K a multiple of 8 up to 65536, M up to 131072, V up to 2^24.
+ * M == 0 is a no-op (the workspace size is then 0).
+ * Errors: BL_ERR_INVALID_ARG, BL_ERR_UNSUPPORTED_SHAPE, BL_ERR_ALIGNMENT,
+ *         BL_ERR_WORKSPACE, BL_ERR_ARCH, BL_ERR_CUDA; device timeouts via
+ *         bl_get_last_error.
+ */
+size_t bl_linear_xent_forward_workspace_size(int64_t M, int64_t V, int64_t K);
+bl_status bl_linear_xent_forward(const void* h, const void* W, const int64_t* targets,
+                                 int64_t M, int64_t V, int64_t K, float* loss, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * X2 -- the gradients of X1, given dloss [M] (the gradient of each token's
+ * loss; 1 / tokens for a mean):
+ *
+ *   dz[m,v] = dloss[m] * (exp(z[m,v] - lse[m]) - [v == targets[m]])
+ *   dH[m,k] = bf16_rn(sum_v dz[m,v] * W[v,k])
+ *   dW[v,k] = round(sum_m dz[m,v] * h[m,k] (+ dW[v,k] if accumulate_dW))
+ *
+ * The vocabulary is taken in pieces: each piece's logits are formed again and
+ * its dz kept, in bf16, only until its share of dH and dW has been added (at
+ * most 64 MiB of dz, or 256 columns; dW in fp32 keeps dz to 16 significant
+ * bits, as the sum of two bf16 numbers, and joins partial sums of 1024 tokens
+ * in fp32). Sums over pieces are kept in fp32 and always added in the same
+ * order: the same inputs give the same bits.
+ * lse is X1's output. dH [M,K] bf16 or NULL (skipped); dW [V,K] of dw_dtype
+ * (BL_BF16 or BL_F32) or NULL (skipped); accumulate_dW != 0 adds to what dW
+ * holds. A left-out token (X1) has dz = 0 whatever its h, lse and dloss hold:
+ * its row of dH is 0 and it adds nothing to dW. M == 0 writes dW = 0 (leaves
+ * it as it is with accumulate_dW).
+ * workspace: at least bl_linear_xent_backward_workspace_size(M,V,K,dw_dtype)
+ * bytes, otherwise as X1's; X1's workspace may be the same memory.
+ * Limits and errors: as X1, plus BL_ERR_DTYPE.
+ */
+size_t bl_linear_xent_backward_workspace_size(int64_t M, int64_t V, int64_t K, bl_dtype dw_dtype);
+bl_status bl_linear_xent_backward(const void* h, const void* W, const int64_t* targets,
+                                  const float* lse, const float* dloss,
+                                  int64_t M, int64_t V, int64_t K,
+                                  void* dH, void* dW, bl_dtype dw_dtype, int accumulate_dW,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * A1, A2 -- an activation kept in 8 bits until the backward. Each row of
+ * x [M,K] (x_dtype BL_BF16 or BL_F32) is cut into G = ceil(K / 128) groups of
+ * 128 values (the last may be shorter):
+ *
+ *   a           = max(max |x| of the group, 1e-30)
+ *   code        = rint_half_even(fp32(x * fp32(127 / a)))      in [-127, 127]
+ *   scale       = fp32(a / 127)
+ *   saved value = fp32(code * scale)
+ *
+ * codes [M,K] int8, scales [M,G] float. A group that holds an infinity or a
+ * NaN gets a NaN scale (its saved values are NaN: an overflow is not hidden).
+ * bl_act8_decode writes the saved values, rounded to x_dtype. K >= 1 is any
+ * size (multiples of 8 run the vectorised kernels). M == 0 is a no-op.
+ * Errors: BL_ERR_INVALID_ARG, BL_ERR_UNSUPPORTED_SHAPE, BL_ERR_DTYPE,
+ *         BL_ERR_ALIGNMENT, BL_ERR_ARCH, BL_ERR_CUDA.
+ */
+bl_status bl_act8_encode(const void* x, bl_dtype x_dtype, int64_t M, int64_t K,
+                         int8_t* codes, float* scales, void* stream);
+bl_status bl_act8_decode(const int8_t* codes, const float* scales, int64_t M, int64_t K,
+                         void* x, bl_dtype x_dtype, void* stream);
+
+/*
+ * N1 -- layer norm or RMS norm of the rows of x [M,K] (x_dtype BL_BF16 or
+ * BL_F32), sums in fp32:
+ *
+ *   mean[m] = sum_k x[m,k] / K                    (0 with rms != 0)
+ *   rstd[m] = 1 / sqrt(sum_k (x[m,k] - mean[m])^2 / K + eps)
+ *   y[m,k]  = round((x[m,k] - mean[m]) * rstd[m] * weight[k] + bias[k])
+ *
+ * weight, bias [K] of p_dtype (BL_BF16 or BL_F32), each NULL for ones and
+ * zeros; y [M,K] of x_dtype; mean, rstd [M] float, kept for N2 (mean is not
+ * touched with rms != 0 and may then be NULL). codes and scales, both or
+ * neither NULL, receive the 8-bit form of x (A1) for N2, in the same pass
+ * when K is a multiple of 8 and at most 32768.
+ * eps must be finite and >= 0. K >= 1 is any size; M == 0 is a no-op.
+ * Errors: as A1.
+ */
+bl_status bl_norm_forward(const void* x, bl_dtype x_dtype, const void* weight, const void* bias,
+                          bl_dtype p_dtype, int64_t M, int64_t K, float eps, int rms,
+                          void* y, float* mean, float* rstd, int8_t* codes, float* scales,
+                          void* stream);
+
+/*
+ * N2 -- the gradients of N1, with xhat[m,k] = (x[m,k] - mean[m]) * rstd[m]
+ * and g[m,k] = dy[m,k] * weight[k]:
+ *
+ *   dx[m,k]    = round(rstd[m] * (g[m,k] - c1[m] - xhat[m,k] * c2[m]))
+ *                c1 = sum_k g / K (0 with rms != 0), c2 = sum_k g * xhat / K
+ *   dweight[k] = round(sum_m dy[m,k] * xhat[m,k] (+ dweight[k] if accumulate))
+ *   dbias[k]   = round(sum_m dy[m,k] (+ dbias[k] if accumulate))
+ *
+ * x is the forward's input, or NULL with codes and scales: its 8-bit form,
+ * whose saved values are then used in its place. dy and dx [M,K] of x_dtype;
+ * dweight and dbias [K] of p_dtype; each of dx, dweight, dbias may be NULL
+ * (skipped). weight NULL stands for ones. The sums over the tokens are fp32
+ * and always added in the same order. M == 0 writes dweight = dbias = 0
+ * (leaves them as they are with accumulate). dx may be dy itself.
+ * workspace: at least bl_norm_backward_workspace_size(M,K) bytes, 16-byte
+ * aligned, no initialisation, one call at a time per workspace.
+ * Errors: as A1, plus BL_ERR_WORKSPACE.
+ */
+size_t bl_norm_backward_workspace_size(int64_t M, int64_t K);
+bl_status bl_norm_backward(const void* dy, const void* x, const int8_t* codes, const float* scales,
+                           bl_dtype x_dtype, const void* weight, bl_dtype p_dtype,
+                           const float* mean, const float* rstd, int64_t M, int64_t K, int rms,
+                           void* dx, void* dweight, void* dbias, int accumulate,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * U1 -- the SwiGLU gate, y[m,k] = round(silu(gate[m,k]) * up[m,k]) with
+ * silu(g) = g / (1 + exp(-g)); gate, up, y [M,K] of x_dtype (BL_BF16 or
+ * BL_F32). The four code and scale arrays, all or none NULL, receive the
+ * 8-bit forms of gate and up (A1) in the same pass: what U2 needs.
+ * Errors: as A1.
+ */
+bl_status bl_swiglu_forward(const void* gate, const void* up, bl_dtype x_dtype, int64_t M, int64_t K,
+                            void* y, int8_t* gate_codes, float* gate_scales,
+                            int8_t* up_codes, float* up_scales, void* stream);
+
+/*
+ * U2 -- the gradients of U1 from the 8-bit forms alone (g and u their saved
+ * values, s = 1 / (1 + exp(-g))):
+ *
+ *   dgate[m,k] = round(dy[m,k] * u * s * (1 + g * (1 - s)))
+ *   dup[m,k]   = round(dy[m,k] * g * s)
+ *
+ * dy, dgate, dup [M,K] of x_dtype; dgate or dup may be dy itself, not both.
+ * Errors: as A1.
+ */
+bl_status bl_swiglu_backward(const void* dy, const int8_t* gate_codes, const float* gate_scales,
+                             const int8_t* up_codes, const float* up_scales, bl_dtype x_dtype,
+                             int64_t M, int64_t K, void* dgate, void* dup, void* stream);
+
+/*
  * Synchronises the current device, then returns BL_OK or the first device
  * failure recorded since the last bl_reset_error (BL_ERR_TIMEOUT).
  */

@@ -52,6 +52,18 @@ SIGNATURES = {
     "bl_sign_vote": (_I32, [_VP, _I32, _I64, _I64, _VP, _VP]),
     "bl_signsgd_update": (_I32, [_VP, _I32, _I64, _I64, _VP, ctypes.c_float, _VP]),
     "bl_signsgd_apply": (_I32, [_VP, _I32, _VP, _I32, _I64, _I64, ctypes.c_float, _VP, _VP, _VP, _SZ, _VP]),
+    "bl_linear_xent_forward_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "bl_linear_xent_forward": (_I32, [_VP, _VP, _VP, _I64, _I64, _I64, _VP, _VP, _VP, _SZ, _VP]),
+    "bl_linear_xent_backward_workspace_size": (_SZ, [_I64, _I64, _I64, _I32]),
+    "bl_linear_xent_backward": (_I32, [_VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _VP, _VP, _I32, _I32, _VP, _SZ, _VP]),
+    "bl_act8_encode": (_I32, [_VP, _I32, _I64, _I64, _VP, _VP, _VP]),
+    "bl_act8_decode": (_I32, [_VP, _VP, _I64, _I64, _VP, _I32, _VP]),
+    "bl_norm_forward": (_I32, [_VP, _I32, _VP, _VP, _I32, _I64, _I64, ctypes.c_float, _I32, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "bl_norm_backward_workspace_size": (_SZ, [_I64, _I64]),
+    "bl_norm_backward": (_I32, [_VP, _VP, _VP, _VP, _I32, _VP, _I32, _VP, _VP, _I64, _I64, _I32, _VP, _VP, _VP, _I32, _VP,
+                                _SZ, _VP]),
+    "bl_swiglu_forward": (_I32, [_VP, _VP, _I32, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "bl_swiglu_backward": (_I32, [_VP, _VP, _VP, _VP, _VP, _I32, _I64, _I64, _VP, _VP, _VP]),
 }
 
 
@@ -326,6 +338,271 @@ def bl_get_last_error() -> int:
 
 def bl_reset_error() -> int:
     return load_library().bl_reset_error()
+
+
+# ----------------------------------------------------------------- training operators next to the layer
+
+def _dtype_code(t, name):
+    if t.dtype == torch.bfloat16:
+        return BL_BF16
+    if t.dtype == torch.float32:
+        return BL_F32
+    raise ValueError(f"{name} must be bf16 or f32")
+
+
+def _workspace_bytes(ws):
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def bl_linear_xent_forward_workspace_size(M: int, V: int, K: int) -> int:
+    return load_library().bl_linear_xent_forward_workspace_size(M, V, K)
+
+
+def bl_linear_xent_backward_workspace_size(M: int, V: int, K: int, dw_dtype=torch.bfloat16) -> int:
+    code = BL_F32 if dw_dtype == torch.float32 else BL_BF16
+    return load_library().bl_linear_xent_backward_workspace_size(M, V, K, code)
+
+
+def bl_linear_xent_forward(h, W, targets, loss, lse, workspace, stream=None):
+    """X1: loss [M], lse [M] f32 of the softmax cross-entropy of h [M,K] . W [V,K]^T
+    (bf16) at targets [M] int64; a target outside 0..V-1 leaves its token out."""
+    M, K = h.shape
+    V = W.shape[0]
+    _need(h, torch.bfloat16, (M, K), "h")
+    _need(W, torch.bfloat16, (V, K), "W")
+    _need(targets, torch.int64, (M,), "targets")
+    _need(loss, torch.float32, (M,), "loss")
+    _need(lse, torch.float32, (M,), "lse")
+    _on_current_device(h, W, targets, loss, lse, workspace)
+    _check(load_library().bl_linear_xent_forward(_ptr(h), _ptr(W), _ptr(targets), M, V, K, _ptr(loss), _ptr(lse),
+                                                 _ptr(workspace), _workspace_bytes(workspace), _stream(stream)),
+           "bl_linear_xent_forward")
+
+
+def bl_linear_xent_backward(h, W, targets, lse, dloss, dH=None, dW=None, workspace=None, accumulate_dW=False,
+                            stream=None):
+    """X2: dH [M,K] bf16 and dW [V,K] (bf16|f32) of X1 (each may be None), given
+    dloss [M] f32, the gradient of each token's loss, and X1's lse."""
+    M, K = h.shape
+    V = W.shape[0]
+    _need(h, torch.bfloat16, (M, K), "h")
+    _need(W, torch.bfloat16, (V, K), "W")
+    _need(targets, torch.int64, (M,), "targets")
+    _need(lse, torch.float32, (M,), "lse")
+    _need(dloss, torch.float32, (M,), "dloss")
+    dwdt = BL_BF16
+    if dH is not None:
+        _need(dH, torch.bfloat16, (M, K), "dH")
+    if dW is not None:
+        dwdt = _dtype_code(dW, "dW")
+        _need(dW, dW.dtype, (V, K), "dW")
+    _on_current_device(h, W, targets, lse, dloss, dH, dW, workspace)
+    _check(load_library().bl_linear_xent_backward(_ptr(h), _ptr(W), _ptr(targets), _ptr(lse), _ptr(dloss), M, V, K,
+                                                  _ptr(dH), _ptr(dW), dwdt, int(bool(accumulate_dW)),
+                                                  _ptr(workspace), _workspace_bytes(workspace), _stream(stream)),
+           "bl_linear_xent_backward")
+
+
+@dataclass
+class Act8:
+    """The 8-bit form of an activation [M,K]: codes [M,K] int8 and one scale per
+    128 values of a row, scales [M, ceil(K / 128)] f32."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    @staticmethod
+    def allocate(M, K, device="cuda"):
+        return Act8(codes=torch.empty((M, K), dtype=torch.int8, device=device),
+                    scales=torch.empty((M, -(-K // 128)), dtype=torch.float32, device=device))
+
+
+def _need_act8(a, M, K, name):
+    _need(a.codes, torch.int8, (M, K), f"{name}.codes")
+    _need(a.scales, torch.float32, (M, -(-K // 128)), f"{name}.scales")
+
+
+def bl_act8_encode(x, saved: Act8, stream=None):
+    """A1: saved <- the 8-bit form of x [M,K] (bf16|f32)."""
+    M, K = x.shape
+    dt = _dtype_code(x, "x")
+    _need(x, x.dtype, (M, K), "x")
+    _need_act8(saved, M, K, "saved")
+    _on_current_device(x, saved.codes, saved.scales)
+    _check(load_library().bl_act8_encode(_ptr(x), dt, M, K, _ptr(saved.codes), _ptr(saved.scales), _stream(stream)),
+           "bl_act8_encode")
+
+
+def bl_act8_decode(saved: Act8, x, stream=None):
+    """A2: x [M,K] (bf16|f32) <- the saved values."""
+    M, K = x.shape
+    dt = _dtype_code(x, "x")
+    _need(x, x.dtype, (M, K), "x")
+    _need_act8(saved, M, K, "saved")
+    _on_current_device(x, saved.codes, saved.scales)
+    _check(load_library().bl_act8_decode(_ptr(saved.codes), _ptr(saved.scales), M, K, _ptr(x), dt, _stream(stream)),
+           "bl_act8_decode")
+
+
+def bl_norm_forward(x, weight, bias, eps, y, mean, rstd, rms=False, saved8: Act8 | None = None, stream=None):
+    """N1: y [M,K] = layer norm (rms: RMS norm) of x [M,K] (bf16|f32) with weight,
+    bias [K] (bf16|f32, each may be None); mean (None with rms), rstd [M] f32;
+    saved8 receives the 8-bit form of x."""
+    M, K = x.shape
+    dt = _dtype_code(x, "x")
+    _need(x, x.dtype, (M, K), "x")
+    _need(y, x.dtype, (M, K), "y")
+    _need(rstd, torch.float32, (M,), "rstd")
+    if mean is not None:
+        _need(mean, torch.float32, (M,), "mean")
+    pdt = BL_F32
+    for t, name in ((bias, "bias"), (weight, "weight")):
+        if t is not None:
+            pdt = _dtype_code(t, name)
+            _need(t, t.dtype, (K,), name)
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise ValueError(f"weight and bias must have one dtype, got {weight.dtype} and {bias.dtype}")
+    codes = scales = None
+    if saved8 is not None:
+        _need_act8(saved8, M, K, "saved8")
+        codes, scales = saved8.codes, saved8.scales
+    _on_current_device(x, weight, bias, y, mean, rstd, codes, scales)
+    _check(load_library().bl_norm_forward(_ptr(x), dt, _ptr(weight), _ptr(bias), pdt, M, K, float(eps), int(bool(rms)),
+                                          _ptr(y), _ptr(mean), _ptr(rstd), _ptr(codes), _ptr(scales),
+                                          _stream(stream)), "bl_norm_forward")
+
+
+def bl_norm_backward_workspace_size(M: int, K: int) -> int:
+    return load_library().bl_norm_backward_workspace_size(M, K)
+
+
+def bl_norm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=None, workspace=None, rms=False,
+                     accumulate=False, stream=None):
+    """N2: dx [M,K], dweight, dbias [K] (each may be None) of N1. x: the forward's
+    input, or the Act8 that the forward saved."""
+    M, K = dy.shape
+    dt = _dtype_code(dy, "dy")
+    _need(dy, dy.dtype, (M, K), "dy")
+    codes = scales = None
+    if isinstance(x, Act8):
+        _need_act8(x, M, K, "x")
+        codes, scales, x = x.codes, x.scales, None
+    else:
+        _need(x, dy.dtype, (M, K), "x")
+    _need(rstd, torch.float32, (M,), "rstd")
+    if mean is not None:
+        _need(mean, torch.float32, (M,), "mean")
+    if dx is not None:
+        _need(dx, dy.dtype, (M, K), "dx")
+    params = [(t, name) for t, name in ((weight, "weight"), (dweight, "dweight"), (dbias, "dbias")) if t is not None]
+    for t, name in params:
+        _dtype_code(t, name)
+        _need(t, params[0][0].dtype, (K,), name)
+    pdt = _dtype_code(*params[0]) if params else BL_F32
+    _on_current_device(dy, x, codes, scales, weight, mean, rstd, dx, dweight, dbias, workspace)
+    _check(load_library().bl_norm_backward(_ptr(dy), _ptr(x), _ptr(codes), _ptr(scales), dt, _ptr(weight), pdt,
+                                           _ptr(mean), _ptr(rstd), M, K, int(bool(rms)), _ptr(dx), _ptr(dweight),
+                                           _ptr(dbias), int(bool(accumulate)), _ptr(workspace),
+                                           _workspace_bytes(workspace), _stream(stream)), "bl_norm_backward")
+
+
+def bl_swiglu_forward(gate, up, y, gate8: Act8 | None = None, up8: Act8 | None = None, stream=None):
+    """U1: y [M,K] = silu(gate) * up (bf16|f32); gate8, up8 (both or neither)
+    receive the 8-bit forms of gate and up."""
+    M, K = gate.shape
+    dt = _dtype_code(gate, "gate")
+    _need(gate, gate.dtype, (M, K), "gate")
+    _need(up, gate.dtype, (M, K), "up")
+    _need(y, gate.dtype, (M, K), "y")
+    if (gate8 is None) != (up8 is None):
+        raise ValueError("gate8 and up8 go together")
+    saved = [None] * 4
+    if gate8 is not None:
+        _need_act8(gate8, M, K, "gate8")
+        _need_act8(up8, M, K, "up8")
+        saved = [gate8.codes, gate8.scales, up8.codes, up8.scales]
+    _on_current_device(gate, up, y, *saved)
+    _check(load_library().bl_swiglu_forward(_ptr(gate), _ptr(up), dt, M, K, _ptr(y), *[_ptr(t) for t in saved],
+                                            _stream(stream)), "bl_swiglu_forward")
+
+
+def bl_swiglu_backward(dy, gate8: Act8, up8: Act8, dgate, dup, stream=None):
+    """U2: dgate, dup [M,K] of U1 from the 8-bit forms of gate and up."""
+    M, K = dy.shape
+    dt = _dtype_code(dy, "dy")
+    _need(dy, dy.dtype, (M, K), "dy")
+    _need_act8(gate8, M, K, "gate8")
+    _need_act8(up8, M, K, "up8")
+    _need(dgate, dy.dtype, (M, K), "dgate")
+    _need(dup, dy.dtype, (M, K), "dup")
+    _on_current_device(dy, gate8.codes, gate8.scales, up8.codes, up8.scales, dgate, dup)
+    _check(load_library().bl_swiglu_backward(_ptr(dy), _ptr(gate8.codes), _ptr(gate8.scales), _ptr(up8.codes),
+                                             _ptr(up8.scales), dt, M, K, _ptr(dgate), _ptr(dup), _stream(stream)),
+           "bl_swiglu_backward")
+
+
+@dataclass
+class XentBuffers:
+    """Device buffers of X1 and (backward) X2 (caller-owned, reused); one
+    workspace serves both calls, in either order on one stream."""
+    loss: torch.Tensor
+    lse: torch.Tensor
+    workspace: torch.Tensor
+    dH: torch.Tensor | None = None
+    dW: torch.Tensor | None = None
+
+    @staticmethod
+    def allocate(M, V, K, dw_dtype=torch.bfloat16, backward=True, device="cuda"):
+        ws = bl_linear_xent_forward_workspace_size(M, V, K)
+        if backward:
+            ws = max(ws, bl_linear_xent_backward_workspace_size(M, V, K, dw_dtype))
+        return XentBuffers(
+            loss=torch.empty(M, dtype=torch.float32, device=device),
+            lse=torch.empty(M, dtype=torch.float32, device=device),
+            workspace=torch.empty(max(ws, 16), dtype=torch.uint8, device=device),
+            dH=torch.empty((M, K), dtype=torch.bfloat16, device=device) if backward else None,
+            dW=torch.empty((V, K), dtype=dw_dtype, device=device) if backward else None,
+        )
+
+
+@dataclass
+class NormBuffers:
+    """Device buffers of N1 and N2 (caller-owned, reused)."""
+    y: torch.Tensor
+    mean: torch.Tensor | None
+    rstd: torch.Tensor
+    saved8: Act8 | None
+    dx: torch.Tensor
+    dweight: torch.Tensor
+    dbias: torch.Tensor | None
+    workspace: torch.Tensor
+
+    @staticmethod
+    def allocate(M, K, dtype=torch.bfloat16, p_dtype=torch.float32, rms=False, bias=False, saved8=False,
+                 device="cuda"):
+        def empty(shape, dt):
+            return torch.empty(shape, dtype=dt, device=device)
+        return NormBuffers(
+            y=empty((M, K), dtype), mean=None if rms else empty(M, torch.float32), rstd=empty(M, torch.float32),
+            saved8=Act8.allocate(M, K, device) if saved8 else None,
+            dx=empty((M, K), dtype), dweight=empty(K, p_dtype), dbias=empty(K, p_dtype) if bias else None,
+            workspace=empty(max(bl_norm_backward_workspace_size(M, K), 16), torch.uint8))
+
+
+@dataclass
+class SwigluBuffers:
+    """Device buffers of U1 and U2 (caller-owned, reused)."""
+    y: torch.Tensor
+    gate8: Act8
+    up8: Act8
+    dgate: torch.Tensor
+    dup: torch.Tensor
+
+    @staticmethod
+    def allocate(M, K, dtype=torch.bfloat16, device="cuda"):
+        def empty():
+            return torch.empty((M, K), dtype=dtype, device=device)
+        return SwigluBuffers(y=empty(), gate8=Act8.allocate(M, K, device), up8=Act8.allocate(M, K, device),
+                             dgate=empty(), dup=empty())
 
 
 # ----------------------------------------------------------------- one whole step

@@ -340,6 +340,205 @@ bl_status bl_signsgd_apply(const uint32_t* sign_words, int ranks, void* W, bl_dt
                      "bl_signsgd_apply");
 }
 
+// Shape limits of the head cross-entropy (its tile counts and tensor-map
+// coordinates fit in 32 bits within them).
+static bl_status check_xent(int64_t M, int64_t V, int64_t K) {
+  if (M < 0 || V < 1) return fail(BL_ERR_INVALID_ARG, "M=%lld, V=%lld", (long long)M, (long long)V);
+  if (K < 8 || K % 8 != 0 || K > 65536)
+    return fail(BL_ERR_UNSUPPORTED_SHAPE, "K=%lld must be a multiple of 8 from 8 to 65536", (long long)K);
+  if (M > 131072 || V > (int64_t(1) << 24))
+    return fail(BL_ERR_UNSUPPORTED_SHAPE, "M=%lld above 131072 or V=%lld above 2^24", (long long)M, (long long)V);
+  return BL_OK;
+}
+
+size_t bl_linear_xent_forward_workspace_size(int64_t M, int64_t V, int64_t K) {
+  g_msg[0] = 0;
+  if (M == 0 || check_xent(M, V, K) != BL_OK) return 0;
+  return bl::xent_forward_workspace_bytes(M, V, K);
+}
+
+size_t bl_linear_xent_backward_workspace_size(int64_t M, int64_t V, int64_t K, bl_dtype dw_dtype) {
+  g_msg[0] = 0;
+  if (M == 0 || check_xent(M, V, K) != BL_OK || (dw_dtype != BL_BF16 && dw_dtype != BL_F32)) return 0;
+  return bl::xent_backward_workspace_bytes(M, V, K, dw_dtype == BL_F32);
+}
+
+bl_status bl_linear_xent_forward(const void* h, const void* W, const int64_t* targets, int64_t M, int64_t V,
+                                 int64_t K, float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  g_msg[0] = 0;
+  if (bl_status s = check_xent(M, V, K)) return s;
+  if (M == 0) return BL_OK;
+  if (!h || !W || !targets || !loss || !lse) return fail(BL_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(h) || !aligned16(W) || !aligned16(targets) || !aligned16(loss) || !aligned16(lse))
+    return fail(BL_ERR_ALIGNMENT, "tensors must be 16-byte aligned");
+  const size_t need = bl_linear_xent_forward_workspace_size(M, V, K);
+  if (!workspace || workspace_bytes < need || !aligned16(workspace))
+    return fail(BL_ERR_WORKSPACE, "workspace needs %zu bytes, 16-byte aligned", need);
+  int* err = nullptr;
+  if (bl_status s = current_device(&err)) return s;
+  return cuda_status(bl::launch_xent_forward(h, W, targets, M, V, K, loss, lse, workspace, err,
+                                             static_cast<cudaStream_t>(stream)),
+                     "bl_linear_xent_forward launch");
+}
+
+bl_status bl_linear_xent_backward(const void* h, const void* W, const int64_t* targets, const float* lse,
+                                  const float* dloss, int64_t M, int64_t V, int64_t K, void* dH, void* dW,
+                                  bl_dtype dw_dtype, int accumulate_dW, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  g_msg[0] = 0;
+  if (bl_status s = check_xent(M, V, K)) return s;
+  if (dw_dtype != BL_BF16 && dw_dtype != BL_F32) return fail(BL_ERR_DTYPE, "dw_dtype %d", (int)dw_dtype);
+  if (!dH && !dW) return BL_OK;
+  if (M == 0 && (!dW || accumulate_dW)) return BL_OK;
+  if (M > 0 && (!h || !W || !targets || !lse || !dloss)) return fail(BL_ERR_INVALID_ARG, "null pointer");
+  if ((h && !aligned16(h)) || (W && !aligned16(W)) || (targets && !aligned16(targets)) || (lse && !aligned16(lse)) ||
+      (dloss && !aligned16(dloss)) || (dH && !aligned16(dH)) || (dW && !aligned16(dW)))
+    return fail(BL_ERR_ALIGNMENT, "tensors must be 16-byte aligned");
+  const size_t need = bl_linear_xent_backward_workspace_size(M, V, K, dw_dtype);
+  if (M > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+    return fail(BL_ERR_WORKSPACE, "workspace needs %zu bytes, 16-byte aligned", need);
+  int* err = nullptr;
+  if (bl_status s = current_device(&err)) return s;
+  return cuda_status(bl::launch_xent_backward(h, W, targets, lse, dloss, M, V, K, dH, dW, dw_dtype == BL_F32,
+                                              accumulate_dW != 0, workspace, err, static_cast<cudaStream_t>(stream)),
+                     "bl_linear_xent_backward launch");
+}
+
+// Shapes and type of the row operators (A1, A2, N1, N2, U1, U2).
+static bl_status check_rows(int64_t M, int64_t K, bl_dtype dtype) {
+  if (M < 0) return fail(BL_ERR_INVALID_ARG, "M=%lld must be >= 0", (long long)M);
+  if (K < 1 || K > (int64_t(1) << 30))
+    return fail(BL_ERR_UNSUPPORTED_SHAPE, "K=%lld must be from 1 to 2^30", (long long)K);
+  if (M > (int64_t(1) << 30)) return fail(BL_ERR_UNSUPPORTED_SHAPE, "M=%lld too large", (long long)M);
+  if (dtype != BL_BF16 && dtype != BL_F32) return fail(BL_ERR_DTYPE, "dtype %d", (int)dtype);
+  return BL_OK;
+}
+
+bl_status bl_act8_encode(const void* x, bl_dtype x_dtype, int64_t M, int64_t K, int8_t* codes, float* scales,
+                         void* stream) {
+  g_msg[0] = 0;
+  if (bl_status s = check_rows(M, K, x_dtype)) return s;
+  if (M == 0) return BL_OK;
+  if (!x || !codes || !scales) return fail(BL_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales))
+    return fail(BL_ERR_ALIGNMENT, "x, codes and scales must be 16-byte aligned");
+  int* err = nullptr;
+  if (bl_status s = current_device(&err)) return s;
+  return cuda_status(bl::launch_act8_encode(x, x_dtype == BL_F32, M, K, codes, scales,
+                                            static_cast<cudaStream_t>(stream)),
+                     "bl_act8_encode launch");
+}
+
+bl_status bl_act8_decode(const int8_t* codes, const float* scales, int64_t M, int64_t K, void* x, bl_dtype x_dtype,
+                         void* stream) {
+  g_msg[0] = 0;
+  if (bl_status s = check_rows(M, K, x_dtype)) return s;
+  if (M == 0) return BL_OK;
+  if (!x || !codes || !scales) return fail(BL_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales))
+    return fail(BL_ERR_ALIGNMENT, "x, codes and scales must be 16-byte aligned");
+  int* err = nullptr;
+  if (bl_status s = current_device(&err)) return s;
+  return cuda_status(bl::launch_act8_decode(codes, scales, M, K, x, x_dtype == BL_F32,
+                                            static_cast<cudaStream_t>(stream)),
+                     "bl_act8_decode launch");
+}
+
+bl_status bl_norm_forward(const void* x, bl_dtype x_dtype, const void* weight, const void* bias, bl_dtype p_dtype,
+                          int64_t M, int64_t K, float eps, int rms, void* y, float* mean, float* rstd, int8_t* codes,
+                          float* scales, void* stream) {
+  g_msg[0] = 0;
+  if (bl_status s = check_rows(M, K, x_dtype)) return s;
+  if (p_dtype != BL_BF16 && p_dtype != BL_F32) return fail(BL_ERR_DTYPE, "p_dtype %d", (int)p_dtype);
+  if (!(eps - eps == 0.0f) || eps < 0.0f) return fail(BL_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if ((codes == nullptr) != (scales == nullptr)) return fail(BL_ERR_INVALID_ARG, "codes and scales go together");
+  if (M == 0) return BL_OK;
+  if (!x || !y || !rstd || (!rms && !mean)) return fail(BL_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(x) || !aligned16(y) || !aligned16(rstd) || (mean && !aligned16(mean)) ||
+      (weight && !aligned16(weight)) || (bias && !aligned16(bias)) || (codes && !aligned16(codes)) ||
+      (scales && !aligned16(scales)))
+    return fail(BL_ERR_ALIGNMENT, "tensors must be 16-byte aligned");
+  int* err = nullptr;
+  if (bl_status s = current_device(&err)) return s;
+  return cuda_status(bl::launch_norm_forward(x, x_dtype == BL_F32, weight, bias, p_dtype == BL_F32, M, K, eps,
+                                             rms != 0, y, mean, rstd, codes, scales,
+                                             static_cast<cudaStream_t>(stream)),
+                     "bl_norm_forward launch");
+}
+
+size_t bl_norm_backward_workspace_size(int64_t M, int64_t K) {
+  g_msg[0] = 0;
+  if (M == 0 || check_rows(M, K, BL_BF16) != BL_OK) return 0;
+  return bl::norm_backward_workspace_bytes(M, K);
+}
+
+bl_status bl_norm_backward(const void* dy, const void* x, const int8_t* codes, const float* scales, bl_dtype x_dtype,
+                           const void* weight, bl_dtype p_dtype, const float* mean, const float* rstd, int64_t M,
+                           int64_t K, int rms, void* dx, void* dweight, void* dbias, int accumulate, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  g_msg[0] = 0;
+  if (bl_status s = check_rows(M, K, x_dtype)) return s;
+  if (p_dtype != BL_BF16 && p_dtype != BL_F32) return fail(BL_ERR_DTYPE, "p_dtype %d", (int)p_dtype);
+  if ((codes == nullptr) != (scales == nullptr)) return fail(BL_ERR_INVALID_ARG, "codes and scales go together");
+  if (x && codes) return fail(BL_ERR_INVALID_ARG, "x or its 8-bit form, not both");
+  if (M == 0 && ((!dweight && !dbias) || accumulate)) return BL_OK;
+  if (!dx && !dweight && !dbias) return BL_OK;
+  if (M > 0 && (!dy || (!x && !codes) || !rstd || (!rms && !mean))) return fail(BL_ERR_INVALID_ARG, "null pointer");
+  if ((dy && !aligned16(dy)) || (x && !aligned16(x)) || (codes && !aligned16(codes)) ||
+      (scales && !aligned16(scales)) || (weight && !aligned16(weight)) || (mean && !aligned16(mean)) ||
+      (rstd && !aligned16(rstd)) || (dx && !aligned16(dx)) || (dweight && !aligned16(dweight)) ||
+      (dbias && !aligned16(dbias)))
+    return fail(BL_ERR_ALIGNMENT, "tensors must be 16-byte aligned");
+  const size_t need = bl_norm_backward_workspace_size(M, K);
+  if (M > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+    return fail(BL_ERR_WORKSPACE, "workspace needs %zu bytes, 16-byte aligned", need);
+  int* err = nullptr;
+  if (bl_status s = current_device(&err)) return s;
+  return cuda_status(bl::launch_norm_backward(dy, x, codes, scales, x_dtype == BL_F32, weight, p_dtype == BL_F32,
+                                              mean, rstd, M, K, rms != 0, dx, dweight, dbias, accumulate != 0,
+                                              workspace, static_cast<cudaStream_t>(stream)),
+                     "bl_norm_backward launch");
+}
+
+bl_status bl_swiglu_forward(const void* gate, const void* up, bl_dtype x_dtype, int64_t M, int64_t K, void* y,
+                            int8_t* gate_codes, float* gate_scales, int8_t* up_codes, float* up_scales,
+                            void* stream) {
+  g_msg[0] = 0;
+  if (bl_status s = check_rows(M, K, x_dtype)) return s;
+  const int saved = (gate_codes != nullptr) + (gate_scales != nullptr) + (up_codes != nullptr) + (up_scales != nullptr);
+  if (saved != 0 && saved != 4) return fail(BL_ERR_INVALID_ARG, "the four code and scale arrays go together");
+  if (M == 0) return BL_OK;
+  if (!gate || !up || !y) return fail(BL_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(gate) || !aligned16(up) || !aligned16(y) ||
+      (saved && (!aligned16(gate_codes) || !aligned16(gate_scales) || !aligned16(up_codes) || !aligned16(up_scales))))
+    return fail(BL_ERR_ALIGNMENT, "tensors must be 16-byte aligned");
+  int* err = nullptr;
+  if (bl_status s = current_device(&err)) return s;
+  return cuda_status(bl::launch_swiglu_forward(gate, up, x_dtype == BL_F32, M, K, y, gate_codes, gate_scales, up_codes,
+                                               up_scales, static_cast<cudaStream_t>(stream)),
+                     "bl_swiglu_forward launch");
+}
+
+bl_status bl_swiglu_backward(const void* dy, const int8_t* gate_codes, const float* gate_scales,
+                             const int8_t* up_codes, const float* up_scales, bl_dtype x_dtype, int64_t M, int64_t K,
+                             void* dgate, void* dup, void* stream) {
+  g_msg[0] = 0;
+  if (bl_status s = check_rows(M, K, x_dtype)) return s;
+  if (M == 0) return BL_OK;
+  if (!dy || !gate_codes || !gate_scales || !up_codes || !up_scales || !dgate || !dup)
+    return fail(BL_ERR_INVALID_ARG, "null pointer");
+  if (dgate == dup) return fail(BL_ERR_INVALID_ARG, "dgate and dup are the same memory");
+  if (!aligned16(dy) || !aligned16(gate_codes) || !aligned16(gate_scales) || !aligned16(up_codes) ||
+      !aligned16(up_scales) || !aligned16(dgate) || !aligned16(dup))
+    return fail(BL_ERR_ALIGNMENT, "tensors must be 16-byte aligned");
+  int* err = nullptr;
+  if (bl_status s = current_device(&err)) return s;
+  return cuda_status(bl::launch_swiglu_backward(dy, gate_codes, gate_scales, up_codes, up_scales, x_dtype == BL_F32, M,
+                                                K, dgate, dup, static_cast<cudaStream_t>(stream)),
+                     "bl_swiglu_backward launch");
+}
+
 bl_status bl_selftest_timeout(void* stream) {
   g_msg[0] = 0;
   int* err = nullptr;

@@ -4,6 +4,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace bl {
@@ -109,11 +110,51 @@ cudaError_t launch_signsgd_update(void* W, int w_is_f32, int64_t N, int64_t K, c
 cudaError_t launch_signsgd_apply(const uint32_t* words, int ranks, void* W, int w_is_f32, int64_t N, int64_t K,
                                  float lr, uint8_t* packed, float* gamma, void* workspace, int* err, cudaStream_t s);
 
+// ---- Training operators next to the BitLinear layer
+// Head cross-entropy (k_xent.cu).
+size_t xent_forward_workspace_bytes(int64_t M, int64_t V, int64_t K);
+size_t xent_backward_workspace_bytes(int64_t M, int64_t V, int64_t K, int dw_is_f32);
+cudaError_t launch_xent_forward(const void* h, const void* W, const int64_t* targets, int64_t M, int64_t V, int64_t K,
+                                float* loss, float* lse, void* workspace, int* err, cudaStream_t s);
+cudaError_t launch_xent_backward(const void* h, const void* W, const int64_t* targets, const float* lse,
+                                 const float* dloss, int64_t M, int64_t V, int64_t K, void* dH, void* dW,
+                                 int dw_is_f32, int accumulate, void* workspace, int* err, cudaStream_t s);
+
+// Activations in 8 bits and the SwiGLU gate (k_act8.cu); the code arrays of
+// the SwiGLU forward may be null.
+cudaError_t launch_act8_encode(const void* x, int f32, int64_t M, int64_t K, int8_t* codes, float* scales,
+                               cudaStream_t s);
+cudaError_t launch_act8_decode(const int8_t* codes, const float* scales, int64_t M, int64_t K, void* x, int f32,
+                               cudaStream_t s);
+cudaError_t launch_swiglu_forward(const void* gate, const void* up, int f32, int64_t M, int64_t K, void* y,
+                                  int8_t* gate_codes, float* gate_scales, int8_t* up_codes, float* up_scales,
+                                  cudaStream_t s);
+cudaError_t launch_swiglu_backward(const void* dy, const int8_t* gate_codes, const float* gate_scales,
+                                   const int8_t* up_codes, const float* up_scales, int f32, int64_t M, int64_t K,
+                                   void* dgate, void* dup, cudaStream_t s);
+
+// Layer norm and RMS norm (k_norm.cu). The backward reads x, or (x null) its
+// 8-bit form.
+size_t norm_backward_workspace_bytes(int64_t M, int64_t K);
+cudaError_t launch_norm_forward(const void* x, int f32, const void* weight, const void* bias, int p_f32, int64_t M,
+                                int64_t K, float eps, int rms, void* y, float* mean, float* rstd, int8_t* codes,
+                                float* scales, cudaStream_t s);
+cudaError_t launch_norm_backward(const void* dy, const void* x, const int8_t* codes, const float* scales, int f32,
+                                 const void* weight, int p_f32, const float* mean, const float* rstd, int64_t M,
+                                 int64_t K, int rms, void* dx, void* dweight, void* dbias, int accumulate,
+                                 void* workspace, cudaStream_t s);
+
 // One warp waiting on an mbarrier that is never completed (bounded wait test).
 cudaError_t launch_selftest_timeout(int* err, cudaStream_t s);
 
 // Number of SMs of the current device (cached per device).
 int device_sm_count();
+
+// Tensor map of a row-major 2D array of bf16 (f32: fp32) elements with
+// 128-byte swizzled boxes of box_inner x box_outer elements; false (and a
+// launch detail) when the driver rejects it.
+bool make_swizzled_map(CUtensorMap* m, const void* base, bool f32, uint64_t inner, uint64_t outer, uint64_t row_bytes,
+                       uint32_t box_inner, uint32_t box_outer, const char* what);
 
 // Detail of the last host-side launch failure on this thread ("" if none).
 const char* launch_detail();

@@ -1,0 +1,768 @@
+// The LM head and its softmax cross-entropy over a large vocabulary, forward
+// and backward, without the logits in memory (X1, X2).
+//
+//   z = h W^T           lse = log sum_v exp z       loss = lse - z[target]
+//   dz = dloss (exp(z - lse) - [target])            dH = dz W      dW = dz^T h
+//
+// Three phases of one persistent CTA-pair GEMM template (bf16 operands, fp32
+// accumulators in TMEM, tcgen05.mma cta_group::2):
+//
+//                D rows x columns   A            B            reduction  epilogue
+//   Lse          tokens x vocab     h  K-major   W  K-major   K          max and sum of exp of the tile's columns, per token
+//   Dz           tokens x vocab     h  K-major   W  K-major   K          dz of a vocabulary piece, bf16 (two terms for fp32 dW)
+//   Grad: dH     tokens x K         dz K-major   W  MN-major  vocab      bf16, or fp32 partial sums over pieces and slices
+//   Grad: dW     vocab x K          dz MN-major  h  MN-major  tokens     bf16 or fp32
+//
+// The backward walks the vocabulary in pieces: Dz forms the piece's logits
+// again and leaves its dz in the workspace (64 MiB at most: about half of L2),
+// Grad multiplies it into dH and dW. Nothing of size tokens x vocabulary is
+// kept. That costs one product more than the three (z, dH, dW) the operator
+// cannot do without; keeping lse from the forward saves the second one.
+//
+// A pair tile is 256 x 256; every operand tile is 128 rows x 64 of the
+// reduction per CTA (two TMA boxes of 64 x 64, 128-byte swizzled: only the
+// coordinates and the descriptors differ between K-major and MN-major). With
+// 6 stages of 32 KB and two TMEM accumulators the tensor cores never wait for
+// an epilogue unless it takes longer than its tile's products. All bounds are
+// handled by TMA: rows and columns outside a tensor load as zeros and are not
+// stored.
+//
+// Roles (256 threads per CTA): warp 0 loads, warp 1 issues the MMAs (one lane
+// of the leader CTA), warps 4..7 are the epilogue (one per TMEM lane quadrant;
+// thread = row of D, so a token's softmax statistics stay in one thread).
+// Every wait is bounded: on expiry a CTA records a timeout in the device error
+// word, tells its peer, drains what it has in flight, frees TMEM and exits.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "bl_act8.cuh"
+#include "bl_device.cuh"
+#include "bl_internal.h"
+
+namespace bl {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarpLoad = 0, kWarpMma = 1, kWarpEpi0 = 4, kEpiWarps = 4;
+constexpr int kTile = 256;              // rows and columns of a pair tile
+constexpr int kBlockR = 64;             // reduction per stage
+constexpr int kBox = 8192;              // one 64 x 64 bf16 box
+constexpr int kStages = 6;
+constexpr int kStageBytes = 4 * kBox;   // A and B: two boxes each
+constexpr uint32_t kTmemCols = 512;     // two accumulators of 256 columns
+constexpr int kEpiBox = 4096;           // output box: 32 rows x 128 bytes
+constexpr int kEpiSlots = 2;            // per epilogue warp
+constexpr int kOffEpi = kStages * kStageBytes;
+constexpr int kOffBar = kOffEpi + kEpiWarps * kEpiSlots * kEpiBox;
+constexpr int kNumBars = 2 * kStages + 5;  // full, empty, tmem_full[2], tmem_empty[2], done
+constexpr int kOffMisc = kOffBar + kNumBars * 8;
+constexpr int kSmemBytes = kOffMisc + 64 + 1024 /*base alignment*/;
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+enum class Phase { Lse, Dz, Grad };
+
+struct XentParams {
+  int M, V, K;
+  int v0, vcount;        // this piece of the vocabulary
+  const int64_t* targets;
+  int* err;
+  int ntiles;
+  int tiles_m, tiles_k;  // tiles over tokens and over K
+  // Lse
+  float2* part;          // [vocab tile][M]: (max, sum exp(z - max))
+  float* tlogit;         // [M]
+  // Dz
+  const float* lse;
+  const float* dloss;
+  int split;             // dz also as its bf16 remainder
+  const uint4* h;        // rows of h, copied to hm with left-out rows cleared
+  uint4* hm;             // (first piece only, else null)
+  // Grad
+  int ntiles_h;          // tiles of dH (all slices); the rest are dW's
+  int slices;            // the reduction of dH is split over this many partial sums
+  int rows_pad;          // rows between the slices' partial sums
+  int h_f32;             // dH goes to the fp32 partial sums (else straight to bf16)
+  int h_add;             // ... and is added to them (later pieces)
+  int t0, tcount;        // tokens of this launch's share of dW
+  int w_f32, w_add;      // dW is fp32; dW adds to its contents
+  void* dW;              // for the bf16 sums that read dW back
+};
+
+struct Tile {
+  int cls;         // Grad: 0 dH, 1 dW
+  int a0, b0;      // first A row and B row of the pair tile
+  int kb0, nkb;    // k-blocks
+  int slice;
+};
+
+template <Phase P>
+__device__ __forceinline__ Tile decode(const XentParams& p, int u) {
+  Tile t{};
+  if constexpr (P != Phase::Grad) {
+    // tokens fastest: the pairs at work share few tiles of W, and h stays in L2
+    t.a0 = (u % p.tiles_m) * kTile;
+    t.b0 = (u / p.tiles_m) * kTile;
+    t.nkb = (p.K + kBlockR - 1) / kBlockR;
+  } else if (u < p.ntiles_h) {
+    const int per = p.tiles_m * p.tiles_k;
+    t.slice = u / per;
+    u -= t.slice * per;
+    t.a0 = (u / p.tiles_k) * kTile;
+    t.b0 = (u % p.tiles_k) * kTile;
+    const int nkb = (p.vcount + kBlockR - 1) / kBlockR;
+    t.kb0 = static_cast<int>(static_cast<int64_t>(nkb) * t.slice / p.slices);
+    t.nkb = static_cast<int>(static_cast<int64_t>(nkb) * (t.slice + 1) / p.slices) - t.kb0;
+  } else {
+    u -= p.ntiles_h;
+    t.cls = 1;
+    t.a0 = (u / p.tiles_k) * kTile;
+    t.b0 = (u % p.tiles_k) * kTile;
+    t.nkb = (p.tcount + kBlockR - 1) / kBlockR;
+    if (p.split) t.nkb *= 2;  // the remainders first, while the sums are small
+  }
+  return t;
+}
+
+// Instruction descriptors and descriptor steps (16-byte units per 16 of the
+// reduction): K-major 32 bytes along the row, MN-major 16 rows.
+__host__ __device__ constexpr uint32_t idesc(int a_mn, int b_mn) { return make_idesc(1 /*f32*/, 1 /*bf16*/, a_mn, b_mn, kTile, kTile); }
+
+__device__ __forceinline__ void mma_stage(uint32_t d_tmem, uint32_t sa, uint32_t sb, bool a_mn, bool b_mn, uint32_t id,
+                                          int kb) {
+  const uint64_t ad = smem_desc_sw128(sa, a_mn ? kBox : 16, 1024);
+  const uint64_t bd = smem_desc_sw128(sb, b_mn ? kBox : 16, 1024);
+  const uint64_t as = a_mn ? 128 : 2, bs = b_mn ? 128 : 2;
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) mma_f16_pair(d_tmem, ad + kk * as, bd + kk * bs, id, (kb | kk) != 0);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// 16-byte chunk j of row `lane` of a 32 x 128 byte box, 128-byte swizzled.
+__device__ __forceinline__ uint32_t box_chunk(uint32_t box, int lane, int j) {
+  return box + static_cast<uint32_t>(lane) * 128u + (static_cast<uint32_t>(j ^ (lane & 7)) << 4);
+}
+
+// The epilogue warp's output staging: kEpiSlots boxes used in turn.
+struct Stager {
+  uint32_t base;
+  uint32_t seq;
+  int lane;
+  // A box whose last store has been read. kOpen: boxes taken before this one
+  // whose stores are still to be issued.
+  template <int kOpen = 0>
+  __device__ __forceinline__ uint32_t next() {
+    static_assert(kOpen < kEpiSlots, "slots");
+    if (lane == 0) bulk_wait_group_read<kEpiSlots - 1 - kOpen>();
+    __syncwarp();
+    return base + (seq++ % kEpiSlots) * kEpiBox;
+  }
+  // `live`: the box has rows inside the tensor.
+  __device__ __forceinline__ void store(const CUtensorMap* map, uint32_t box, int x, int y, bool add, bool live) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && live) {
+      if (add) tma_add_2d(map, box, x, y);
+      else tma_store_2d(map, box, x, y);
+      bulk_commit_group();
+    }
+  }
+};
+
+// ---- Lse: running maximum and sum over the tile's columns of one token.
+struct LseState {
+  float m, s;
+  __device__ __forceinline__ void chunk(uint32_t (&r)[32], int valid) {
+    if (valid < 32) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) r[j] = j < valid ? r[j] : 0xFF800000u;  // -inf
+    }
+    float c = __uint_as_float(r[0]);
+#pragma unroll
+    for (int j = 1; j < 32; ++j) c = fmaxf(c, __uint_as_float(r[j]));
+    const float n = fmaxf(m, c);
+    // an empty maximum (all -inf) leaves exp(-inf - 0) = 0
+    const float nl = n == __uint_as_float(0xFF800000u) ? 0.0f : n * kLog2e;
+    float a0 = 0.0f, a1 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      a0 += ex2(fmaf(__uint_as_float(r[j]), kLog2e, -nl));
+      a1 += ex2(fmaf(__uint_as_float(r[j + 1]), kLog2e, -nl));
+    }
+    s = fmaf(s, ex2(fmaf(m, kLog2e, -nl)), a0 + a1);
+    m = n;
+  }
+};
+
+template <Phase P>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    xent_kernel(const __grid_constant__ CUtensorMap map_h, const __grid_constant__ CUtensorMap map_w,
+                const __grid_constant__ CUtensorMap map_dz, const __grid_constant__ CUtensorMap map_dz_lo,
+                const __grid_constant__ CUtensorMap out0, const __grid_constant__ CUtensorMap out1,
+                const __grid_constant__ XentParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  uint64_t* empty = full + kStages;
+  uint64_t* tmem_full = full + 2 * kStages;
+  uint64_t* tmem_empty = tmem_full + 2;
+  uint64_t* done_bar = tmem_full + 4;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
+  int* issued_parity = reinterpret_cast<int*>(smem + kOffMisc + 8);  // [kStages]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = static_cast<int>(blockIdx.x >> 1), npairs = static_cast<int>(gridDim.x >> 1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      issued_parity[s] = -1;
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tmem_full[b], 1);
+      mbar_init(&tmem_empty[b], 2 * kEpiWarps);
+    }
+    mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc_pair(tmem_holder, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  pdl_wait_primary();
+  pdl_launch_dependents();
+
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (mbar_wait(bar, parity, abort_flag, p.err)) return true;
+    st_cluster_u32(map_to_rank(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u), 1u);
+    return false;
+  };
+  auto lead = [&](uint64_t* bar) -> uint32_t { return map_to_rank(smem_u32(bar), 0); };
+
+  if (warp == kWarpLoad) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int u = pair; ok && u < p.ntiles; u += npairs) {
+        const Tile t = decode<P>(p, u);
+        const int a0 = t.a0 + static_cast<int>(rank) * 128, b0 = t.b0 + static_cast<int>(rank) * 128;
+        const int half = t.nkb >> 1;
+        for (int kb = 0; kb < t.nkb; ++kb) {
+          if (!wait(&empty[stage], phase ^ 1)) {
+            ok = false;
+            break;
+          }
+          issued_parity[stage] = static_cast<int>(phase);
+          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
+          const uint32_t bar = lead(&full[stage]);
+          uint8_t* sa = smem + stage * kStageBytes;
+          uint8_t* sb = sa + 2 * kBox;
+          if constexpr (P != Phase::Grad) {
+            const int k0 = kb * kBlockR;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              tma_load_2d_pair(&map_h, bar, sa + j * kBox, k0, a0 + 64 * j);
+              tma_load_2d_pair(&map_w, bar, sb + j * kBox, k0, p.v0 + b0 + 64 * j);
+            }
+          } else if (t.cls == 0) {
+            const int v = (t.kb0 + kb) * kBlockR;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              tma_load_2d_pair(&map_dz, bar, sa + j * kBox, v, a0 + 64 * j);
+              tma_load_2d_pair(&map_w, bar, sb + j * kBox, b0 + 64 * j, p.v0 + v);
+            }
+          } else {
+            const bool lo = p.split && kb < half;
+            const int m = p.t0 + (p.split && !lo ? kb - half : kb) * kBlockR;
+            const CUtensorMap* md = lo ? &map_dz_lo : &map_dz;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              tma_load_2d_pair(md, bar, sa + j * kBox, a0 + 64 * j, m);
+              tma_load_2d_pair(&map_h, bar, sb + j * kBox, b0 + 64 * j, m);
+            }
+          }
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (leader && (!ok || *abort_flag)) {
+        // let every copy already issued land before the pair exits
+        const unsigned long long deadline = globaltimer_ns() + kWaitLimitNs;
+        for (int s = 0; s < kStages; ++s)
+          if (issued_parity[s] >= 0) mbar_drain_until(&full[s], static_cast<uint32_t>(issued_parity[s]), deadline);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kWarpMma) {
+    if (leader && lane == 0) {
+      const uint32_t s0 = smem_u32(smem);
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, buf_phase = 0;
+      bool ok = true;
+      for (int u = pair; ok && u < p.ntiles; u += npairs) {
+        const Tile t = decode<P>(p, u);
+        if (t.nkb == 0) continue;
+        if (!wait(&tmem_empty[buf], buf_phase ^ 1)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * kTile);
+        for (int kb = 0; kb < t.nkb; ++kb) {
+          if (!wait(&full[stage], phase)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = s0 + stage * kStageBytes, sb = sa + 2 * kBox;
+          if constexpr (P != Phase::Grad) mma_stage(d_tmem, sa, sb, false, false, idesc(0, 0), kb);
+          else if (t.cls == 0) mma_stage(d_tmem, sa, sb, false, true, idesc(0, 1), kb);
+          else mma_stage(d_tmem, sa, sb, true, true, idesc(1, 1), kb);
+          mma_commit_pair(&empty[stage], 0x3);
+          if (kb == t.nkb - 1) mma_commit_pair(&tmem_full[buf], 0x3);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (++buf == 2) {
+          buf = 0;
+          buf_phase ^= 1;
+        }
+      }
+      mma_commit_pair(done_bar, 0x3);
+    }
+    if (lane == 0) mbar_drain(done_bar, 0);
+    __syncwarp();
+  } else if (warp >= kWarpEpi0) {
+    const int q = warp & 3;
+    if constexpr (P == Phase::Dz) {
+      if (p.hm) {
+        // h with the left-out rows cleared, for dW: done here, where the first
+        // tile's products are still to come
+        const int per_row = p.K / 8;
+        const int64_t n = static_cast<int64_t>(p.M) * per_row;
+        const int64_t T = static_cast<int64_t>(gridDim.x) * (kEpiWarps * 32);
+        for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kEpiWarps * 32) + (threadIdx.x - kWarpEpi0 * 32); i < n; i += T) {
+          const int64_t t = __ldg(p.targets + i / per_row);
+          p.hm[i] = t >= 0 && t < p.V ? __ldg(p.h + i) : make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+    }
+    Stager st{smem_u32(smem + kOffEpi + (warp - kWarpEpi0) * kEpiSlots * kEpiBox), 0u, lane};
+    int buf = 0;
+    uint32_t buf_phase = 0;
+    for (int u = pair; u < p.ntiles; u += npairs) {
+      const Tile t = decode<P>(p, u);
+      if (t.nkb == 0) continue;
+      const int row0 = t.a0 + static_cast<int>(rank) * 128 + q * 32;  // first D row of the warp
+      const int row = row0 + lane;
+      // the thread's token
+      int tgt = -1;
+      float nlse = 0.0f, g = 0.0f;
+      uint32_t keep = 0u;
+      LseState ls{__uint_as_float(0xFF800000u), 0.0f};
+      if constexpr (P != Phase::Grad) {
+        if (row < p.M) {
+          const int64_t tt = __ldg(p.targets + row);
+          if (tt >= 0 && tt < p.V) {
+            tgt = static_cast<int>(tt) - (p.v0 + t.b0);
+            keep = 0xFFFFFFFFu;
+            if constexpr (P == Phase::Dz) {
+              nlse = -__ldg(p.lse + row) * kLog2e;
+              g = __ldg(p.dloss + row);
+            }
+          }
+        }
+      }
+      if (!wait(&tmem_full[buf], buf_phase)) break;
+      tc_fence_after();
+      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kTile;
+      uint32_t box = 0, box_lo = 0;
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(tbase + 32 * c, r);
+        tmem_ld_wait();
+        if (c == 7) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(lead(&tmem_empty[buf]));
+        }
+        const int col = t.b0 + 32 * c;  // first column: of the piece (Lse, Dz) or of K (Grad)
+        if constexpr (P == Phase::Lse) {
+          if (static_cast<unsigned>(tgt - 32 * c) < 32u) {
+            float z = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) z = j == tgt - 32 * c ? __uint_as_float(r[j]) : z;
+            p.tlogit[row] = z;
+          }
+          if (p.v0 + col < p.V) ls.chunk(r, p.V - (p.v0 + col));
+        } else if constexpr (P == Phase::Dz) {
+          if (col >= p.vcount) continue;
+          const bool here = static_cast<unsigned>(tgt - 32 * c) < 32u;
+          float d[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) d[j] = ex2(fmaf(__uint_as_float(r[j]), kLog2e, nlse));
+          if (here) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) d[j] = j == tgt - 32 * c ? d[j] - 1.0f : d[j];
+          }
+          // dz to bf16: the type the products take (as the dY of the layer's
+          // own backward); with `split` its remainder too, 16 bits in all
+          uint32_t hi[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            d[2 * j] *= g;
+            d[2 * j + 1] *= g;
+            hi[j] = pack_bf16x2(d[2 * j + 1], d[2 * j]);
+          }
+          if ((c & 1) == 0) box = st.next();
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            st_shared_v4(box_chunk(box, lane, (c & 1) * 4 + j), hi[4 * j] & keep, hi[4 * j + 1] & keep,
+                         hi[4 * j + 2] & keep, hi[4 * j + 3] & keep);
+          const bool last = (c & 1) || col + 32 >= p.vcount;
+          if (last) st.store(&out0, box, col & ~63, row0, false, row0 < p.M);
+          if (p.split) {
+            if ((c & 1) == 0) box_lo = st.next<1>();
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              hi[j] = pack_bf16x2(d[2 * j + 1] - bf16_hi(hi[j]), d[2 * j] - bf16_lo(hi[j]));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              st_shared_v4(box_chunk(box_lo, lane, (c & 1) * 4 + j), hi[4 * j] & keep, hi[4 * j + 1] & keep,
+                           hi[4 * j + 2] & keep, hi[4 * j + 3] & keep);
+            if (last) st.store(&out1, box_lo, col & ~63, row0, false, row0 < p.M);
+          }
+        } else {
+          if (col >= p.K) continue;
+          const bool live = row0 < (t.cls == 0 ? p.M : p.vcount);
+          const bool f32 = t.cls == 0 ? p.h_f32 != 0 : p.w_f32 != 0;
+          if (f32) {
+            box = st.next();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) st_shared_v4(box_chunk(box, lane, j), r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+            if (t.cls == 0) st.store(&out0, box, col, t.slice * p.rows_pad + row0, p.h_add != 0, live);
+            else st.store(&out1, box, col, p.v0 + row0, p.w_add != 0, live);
+          } else {
+            if (t.cls == 1 && p.w_add && row < p.vcount) {
+              // one rounding: the bf16 contents are added to the fp32 sum
+              const uint4* old = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dW) +
+                                                                static_cast<int64_t>(p.v0 + row) * p.K + col);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if (col + 8 * j < p.K) {
+                  const uint4 o = old[j];
+                  const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    r[8 * j + 2 * i] = __float_as_uint(__uint_as_float(r[8 * j + 2 * i]) + bf16_lo(w[i]));
+                    r[8 * j + 2 * i + 1] = __float_as_uint(__uint_as_float(r[8 * j + 2 * i + 1]) + bf16_hi(w[i]));
+                  }
+                }
+              }
+            }
+            if ((c & 1) == 0) box = st.next();
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              st_shared_v4(box_chunk(box, lane, (c & 1) * 4 + j),
+                           pack_bf16x2(__uint_as_float(r[8 * j + 1]), __uint_as_float(r[8 * j])),
+                           pack_bf16x2(__uint_as_float(r[8 * j + 3]), __uint_as_float(r[8 * j + 2])),
+                           pack_bf16x2(__uint_as_float(r[8 * j + 5]), __uint_as_float(r[8 * j + 4])),
+                           pack_bf16x2(__uint_as_float(r[8 * j + 7]), __uint_as_float(r[8 * j + 6])));
+            if ((c & 1) || col + 32 >= p.K) {
+              if (t.cls == 0) st.store(&out0, box, col & ~63, row0, false, live);
+              else st.store(&out1, box, col & ~63, p.v0 + row0, false, live);
+            }
+          }
+        }
+      }
+      if constexpr (P == Phase::Lse) {
+        if (row < p.M) p.part[static_cast<int64_t>(t.b0 / kTile) * p.M + row] = make_float2(ls.m, ls.s);
+      }
+      if (++buf == 2) {
+        buf = 0;
+        buf_phase ^= 1;
+      }
+    }
+    if (lane == 0) bulk_wait_group_all();
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  cluster_sync_all();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+// lse and loss from the vocabulary tiles' (max, sum): 32 tokens per block, the
+// tiles spread over 32 threads of each token, joined in a fixed order.
+__global__ void __launch_bounds__(1024) xent_join_kernel(const float2* __restrict__ part, int tiles, int M, int V,
+                                                         const float* __restrict__ tlogit,
+                                                         const int64_t* __restrict__ targets, float* loss, float* lse) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  __shared__ float2 sh[32][33];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int m = static_cast<int>(blockIdx.x) * 32 + x;
+  const float ninf = __uint_as_float(0xFF800000u);
+  auto join = [&](float2 a, float2 b) {
+    const float n = fmaxf(a.x, b.x);
+    const float nl = n == ninf ? 0.0f : n * kLog2e;
+    return make_float2(n, a.y * ex2(fmaf(a.x, kLog2e, -nl)) + b.y * ex2(fmaf(b.x, kLog2e, -nl)));
+  };
+  float2 a = make_float2(ninf, 0.0f);
+  if (m < M) {
+#pragma unroll 4
+    for (int t = y; t < tiles; t += 32) a = join(a, part[static_cast<int64_t>(t) * M + m]);
+  }
+  sh[y][x] = a;
+  __syncthreads();
+  // warp y joins token y's 32 partial pairs
+  a = sh[x][y];
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    const float2 b = make_float2(__shfl_xor_sync(0xffffffffu, a.x, s), __shfl_xor_sync(0xffffffffu, a.y, s));
+    a = join(a, b);
+  }
+  const int mm = static_cast<int>(blockIdx.x) * 32 + y;
+  if (x == 0 && mm < M) {
+    const float l = a.x + logf(a.y);
+    const int64_t t = targets[mm];
+    lse[mm] = l;
+    loss[mm] = t >= 0 && t < V ? l - tlogit[mm] : 0.0f;
+  }
+}
+
+// dH from the fp32 partial sums of its slices, added in order.
+__global__ void __launch_bounds__(256) xent_dh_kernel(const float4* __restrict__ acc, int64_t slice_vecs, int slices,
+                                                      int64_t nvecs, uint2* __restrict__ dH) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int64_t T = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < nvecs; i += T) {
+    float4 v = acc[i];
+    for (int s = 1; s < slices; ++s) {
+      const float4 w = acc[s * slice_vecs + i];
+      v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+    }
+    dH[i] = make_uint2(pack_bf16x2(v.y, v.x), pack_bf16x2(v.w, v.z));
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+template <Phase P>
+cudaError_t launch_phase(const CUtensorMap (&maps)[6], const XentParams& p, cudaStream_t s) {
+  static int pairs_of[64] = {};  // pairs resident at once, by device
+  int dev = 0;
+  cudaGetDevice(&dev);
+  int pairs = dev >= 0 && dev < 64 ? pairs_of[dev] : 0;
+  if (!pairs) {
+    if (cudaError_t e = cudaFuncSetAttribute(xent_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        e != cudaSuccess)
+      return e;
+    pairs = device_sm_count() / 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, xent_kernel<P>, &cfg) == cudaSuccess && clusters > 0 && clusters < pairs)
+      pairs = clusters;
+    cudaGetLastError();
+    if (dev >= 0 && dev < 64) pairs_of[dev] = pairs;
+  }
+  if (p.ntiles == 0) return cudaSuccess;
+  const int n = p.ntiles < pairs ? p.ntiles : pairs;
+  return launch_pdl(xent_kernel<P>, dim3(2 * n), dim3(kThreads), kSmemBytes, s, maps[0], maps[1], maps[2], maps[3],
+                    maps[4], maps[5], p);
+}
+
+int tiles_of(int64_t n) { return static_cast<int>((n + kTile - 1) / kTile); }
+size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
+
+// Where the backward's parts lie in the workspace, and how it cuts the work.
+struct Plan {
+  int64_t piece;   // vocabulary columns per piece (a multiple of 256)
+  int pieces, slices;
+  int64_t rows_pad;
+  bool sums;       // dH goes through fp32 partial sums
+  size_t off_lo, off_h, off_sum, bytes;
+};
+
+constexpr int64_t kPieceBytes = int64_t(64) << 20;
+constexpr int kF32Tokens = 1024;  // tokens per partial sum of an fp32 dW
+
+Plan make_plan(int64_t M, int64_t V, int64_t K, bool f32) {
+  Plan q{};
+  const int64_t per_col = M * (f32 ? 4 : 2);
+  int64_t most = kPieceBytes / per_col / kTile * kTile;
+  if (most < kTile) most = kTile;
+  const int64_t all = (V + kTile - 1) / kTile * kTile;
+  q.pieces = static_cast<int>((all + most - 1) / most);
+  q.piece = ((V + q.pieces - 1) / q.pieces + kTile - 1) / kTile * kTile;
+  q.pieces = static_cast<int>((V + q.piece - 1) / q.piece);
+  q.rows_pad = (M + kTile - 1) / kTile * kTile;
+  // few tiles of dH: its reduction over the piece is cut into slices, so that
+  // they occupy the SMs next to dW's tiles
+  const int64_t tiles = static_cast<int64_t>(tiles_of(M)) * tiles_of(K);
+  const int64_t nkb = (V < q.piece ? V : q.piece) / kBlockR;
+  int64_t slices = 74 / tiles;
+  if (slices > 8) slices = 8;
+  if (slices > nkb) slices = nkb;
+  q.slices = slices < 1 ? 1 : static_cast<int>(slices);
+  q.sums = q.pieces > 1 || q.slices > 1;
+  size_t off = align256(static_cast<size_t>(M) * q.piece * 2);
+  q.off_lo = off;
+  if (f32) off += align256(static_cast<size_t>(M) * q.piece * 2);
+  q.off_h = off;
+  off += align256(static_cast<size_t>(M) * K * 2);
+  q.off_sum = off;
+  if (q.sums) off += static_cast<size_t>(q.slices) * q.rows_pad * K * 4;
+  q.bytes = off;
+  return q;
+}
+
+}  // namespace
+
+size_t xent_forward_workspace_bytes(int64_t M, int64_t V, int64_t K) {
+  return align256(static_cast<size_t>(tiles_of(V)) * M * 8) + align256(static_cast<size_t>(M) * 4);
+}
+
+size_t xent_backward_workspace_bytes(int64_t M, int64_t V, int64_t K, int dw_is_f32) {
+  return make_plan(M, V, K, dw_is_f32 != 0).bytes;
+}
+
+cudaError_t launch_xent_forward(const void* h, const void* W, const int64_t* targets, int64_t M, int64_t V, int64_t K,
+                                float* loss, float* lse, void* workspace, int* err, cudaStream_t s) {
+  CUtensorMap maps[6] = {};
+  if (!make_swizzled_map(&maps[0], h, false, K, M, K * 2, 64, 64, "h") ||
+      !make_swizzled_map(&maps[1], W, false, K, V, K * 2, 64, 64, "W"))
+    return cudaErrorInvalidValue;
+  XentParams p{};
+  p.M = static_cast<int>(M);
+  p.V = static_cast<int>(V);
+  p.K = static_cast<int>(K);
+  p.vcount = p.V;
+  p.targets = targets;
+  p.err = err;
+  p.tiles_m = tiles_of(M);
+  p.tiles_k = tiles_of(K);
+  const int tiles_v = tiles_of(V);
+  p.ntiles = p.tiles_m * tiles_v;
+  p.part = static_cast<float2*>(workspace);
+  p.tlogit = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256(static_cast<size_t>(tiles_v) * M * 8));
+  if (cudaError_t e = launch_phase<Phase::Lse>(maps, p, s); e != cudaSuccess) return e;
+  return launch_pdl(xent_join_kernel, dim3(static_cast<unsigned>((M + 31) / 32)), dim3(1024), 0, s,
+                    static_cast<const float2*>(p.part), tiles_v, p.M, p.V, static_cast<const float*>(p.tlogit), targets,
+                    loss, lse);
+}
+
+cudaError_t launch_xent_backward(const void* h, const void* W, const int64_t* targets, const float* lse,
+                                 const float* dloss, int64_t M, int64_t V, int64_t K, void* dH, void* dW,
+                                 int dw_is_f32, int accumulate, void* workspace, int* err, cudaStream_t s) {
+  if (M == 0) {
+    if (dW && !accumulate) return cudaMemsetAsync(dW, 0, static_cast<size_t>(V) * K * (dw_is_f32 ? 4 : 2), s);
+    return cudaSuccess;
+  }
+  const bool f32 = dW && dw_is_f32;
+  const Plan q = make_plan(M, V, K, dw_is_f32 != 0);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  void* dz = ws;
+  void* lo = ws + q.off_lo;
+  void* hm = ws + q.off_h;
+  float* sum = reinterpret_cast<float*>(ws + q.off_sum);
+
+  XentParams p{};
+  p.M = static_cast<int>(M);
+  p.V = static_cast<int>(V);
+  p.K = static_cast<int>(K);
+  p.targets = targets;
+  p.err = err;
+  p.tiles_m = tiles_of(M);
+  p.tiles_k = tiles_of(K);
+  p.lse = lse;
+  p.dloss = dloss;
+  p.split = f32;
+  p.h = static_cast<const uint4*>(h);
+  p.slices = q.slices;
+  p.rows_pad = static_cast<int>(q.rows_pad);
+  p.h_f32 = q.sums;
+  p.w_f32 = f32;
+  p.dW = dW;
+
+  CUtensorMap zm[6] = {}, gm[6] = {};  // maps of Dz and of Grad
+  if (!make_swizzled_map(&zm[0], h, false, K, M, K * 2, 64, 64, "h") ||
+      !make_swizzled_map(&zm[1], W, false, K, V, K * 2, 64, 64, "W") ||
+      !make_swizzled_map(&gm[0], hm, false, K, M, K * 2, 64, 64, "h (dW)"))
+    return cudaErrorInvalidValue;
+  gm[1] = zm[1];
+  if (dH && !(q.sums ? make_swizzled_map(&gm[4], sum, true, K, static_cast<uint64_t>(q.slices) * q.rows_pad, K * 4, 32, 32,
+                                         "sums of dH")
+                     : make_swizzled_map(&gm[4], dH, false, K, M, K * 2, 64, 32, "dH")))
+    return cudaErrorInvalidValue;
+  if (dW && !make_swizzled_map(&gm[5], dW, f32, K, V, K * (f32 ? 4 : 2), f32 ? 32 : 64, 32, "dW"))
+    return cudaErrorInvalidValue;
+
+  for (int i = 0; i < q.pieces; ++i) {
+    p.v0 = static_cast<int>(i * q.piece);
+    p.vcount = static_cast<int>(V - p.v0 < q.piece ? V - p.v0 : q.piece);
+    // dz of this piece: rows of `piece` elements, of which vcount are used
+    // (the products read zeros beyond them)
+    if (!make_swizzled_map(&gm[2], dz, false, p.vcount, M, q.piece * 2, 64, 64, "dz") ||
+        !make_swizzled_map(&zm[4], dz, false, p.vcount, M, q.piece * 2, 64, 32, "dz (store)"))
+      return cudaErrorInvalidValue;
+    if (f32 && (!make_swizzled_map(&gm[3], lo, false, p.vcount, M, q.piece * 2, 64, 64, "dz remainder") ||
+                !make_swizzled_map(&zm[5], lo, false, p.vcount, M, q.piece * 2, 64, 32, "dz remainder (store)")))
+      return cudaErrorInvalidValue;
+    p.hm = i == 0 && dW ? static_cast<uint4*>(hm) : nullptr;
+    p.ntiles = p.tiles_m * tiles_of(p.vcount);
+    if (cudaError_t e = launch_phase<Phase::Dz>(zm, p, s); e != cudaSuccess) return e;
+    // an fp32 dW joins partial sums of 1024 tokens, one launch each (the
+    // launches order the additions)
+    const int step = f32 ? kF32Tokens : p.M;
+    for (int t0 = 0; t0 < p.M; t0 += step) {
+      p.t0 = t0;
+      p.tcount = p.M - t0 < step ? p.M - t0 : step;
+      p.ntiles_h = dH && t0 == 0 ? p.slices * p.tiles_m * p.tiles_k : 0;
+      p.h_add = i > 0;
+      p.w_add = accumulate || t0 > 0;
+      p.ntiles = p.ntiles_h + (dW ? tiles_of(p.vcount) * p.tiles_k : 0);
+      if (cudaError_t e = launch_phase<Phase::Grad>(gm, p, s); e != cudaSuccess) return e;
+      if (!dW) break;
+    }
+  }
+  if (!dH || !q.sums) return cudaSuccess;
+  const int64_t nvecs = M * K / 4;
+  const int64_t want = (nvecs + 255) / 256, cap = static_cast<int64_t>(8) * device_sm_count();
+  return launch_pdl(xent_dh_kernel, dim3(static_cast<unsigned>(want < cap ? want : cap)), dim3(256), 0, s,
+                    reinterpret_cast<const float4*>(sum), q.rows_pad * K / 4, q.slices, nvecs, static_cast<uint2*>(dH));
+}
+
+}  // namespace bl
