@@ -411,8 +411,9 @@ bl_status bl_linear_xent_backward(const void* h, const void* W, const int64_t* t
  * 128 values (the last may be shorter):
  *
  *   a           = max(max |x| of the group, 1e-30)
- *   code        = rint_half_even(fp32(x * fp32(127 / a)))      in [-127, 127]
- *   scale       = fp32(a / 127)
+ *   inv         = fp32(fp32(1 / a) * 127)
+ *   code        = rint_half_even(fp32(x * inv))                in [-127, 127]
+ *   scale       = fp32(a * fp32(1 / 127))
  *   saved value = fp32(code * scale)
  *
  * codes [M,K] int8, scales [M,G] float. A group that holds an infinity or a

@@ -350,8 +350,42 @@ def _dtype_code(t, name):
     raise ValueError(f"{name} must be bf16 or f32")
 
 
-def _workspace_bytes(ws):
-    return 0 if ws is None else ws.numel() * ws.element_size()
+def _device(t, name):
+    """The current CUDA device, for a call whose first tensor is t."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return torch.cuda.current_device()
+
+
+def _pointers(cur, specs):
+    """Addresses of the tensors of specs, (tensor or None, dtype, shape, name)
+    each, after the checks of _need and _on_current_device in one pass."""
+    out = []
+    for t, dtype, shape, name in specs:
+        if t is None:
+            out.append(None)
+            continue
+        if t.dtype is not dtype or t.shape != shape or t.device.index != cur or not t.is_contiguous():
+            _need(t, dtype, shape, name)
+            _on_current_device(t)
+        out.append(t.data_ptr())
+    return out
+
+
+def _scratch(cur, workspace):
+    """(address, bytes) of a workspace (None: none)."""
+    if workspace is None:
+        return None, 0
+    if workspace.device.index != cur:
+        _on_current_device(workspace)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _stream_of(stream, cur):
+    # the address alone: no Stream object per call
+    return torch._C._cuda_getCurrentRawStream(cur) if stream is None else _stream(stream)
 
 
 def bl_linear_xent_forward_workspace_size(M: int, V: int, K: int) -> int:
@@ -368,14 +402,12 @@ def bl_linear_xent_forward(h, W, targets, loss, lse, workspace, stream=None):
     (bf16) at targets [M] int64; a target outside 0..V-1 leaves its token out."""
     M, K = h.shape
     V = W.shape[0]
-    _need(h, torch.bfloat16, (M, K), "h")
-    _need(W, torch.bfloat16, (V, K), "W")
-    _need(targets, torch.int64, (M,), "targets")
-    _need(loss, torch.float32, (M,), "loss")
-    _need(lse, torch.float32, (M,), "lse")
-    _on_current_device(h, W, targets, loss, lse, workspace)
-    _check(load_library().bl_linear_xent_forward(_ptr(h), _ptr(W), _ptr(targets), M, V, K, _ptr(loss), _ptr(lse),
-                                                 _ptr(workspace), _workspace_bytes(workspace), _stream(stream)),
+    cur = _device(h, "h")
+    p = _pointers(cur, ((h, torch.bfloat16, (M, K), "h"), (W, torch.bfloat16, (V, K), "W"),
+                        (targets, torch.int64, (M,), "targets"), (loss, torch.float32, (M,), "loss"),
+                        (lse, torch.float32, (M,), "lse")))
+    ws, n = _scratch(cur, workspace)
+    _check(load_library().bl_linear_xent_forward(p[0], p[1], p[2], M, V, K, p[3], p[4], ws, n, _stream_of(stream, cur)),
            "bl_linear_xent_forward")
 
 
@@ -385,22 +417,15 @@ def bl_linear_xent_backward(h, W, targets, lse, dloss, dH=None, dW=None, workspa
     dloss [M] f32, the gradient of each token's loss, and X1's lse."""
     M, K = h.shape
     V = W.shape[0]
-    _need(h, torch.bfloat16, (M, K), "h")
-    _need(W, torch.bfloat16, (V, K), "W")
-    _need(targets, torch.int64, (M,), "targets")
-    _need(lse, torch.float32, (M,), "lse")
-    _need(dloss, torch.float32, (M,), "dloss")
-    dwdt = BL_BF16
-    if dH is not None:
-        _need(dH, torch.bfloat16, (M, K), "dH")
-    if dW is not None:
-        dwdt = _dtype_code(dW, "dW")
-        _need(dW, dW.dtype, (V, K), "dW")
-    _on_current_device(h, W, targets, lse, dloss, dH, dW, workspace)
-    _check(load_library().bl_linear_xent_backward(_ptr(h), _ptr(W), _ptr(targets), _ptr(lse), _ptr(dloss), M, V, K,
-                                                  _ptr(dH), _ptr(dW), dwdt, int(bool(accumulate_dW)),
-                                                  _ptr(workspace), _workspace_bytes(workspace), _stream(stream)),
-           "bl_linear_xent_backward")
+    cur = _device(h, "h")
+    dwdt = BL_BF16 if dW is None else _dtype_code(dW, "dW")
+    p = _pointers(cur, ((h, torch.bfloat16, (M, K), "h"), (W, torch.bfloat16, (V, K), "W"),
+                        (targets, torch.int64, (M,), "targets"), (lse, torch.float32, (M,), "lse"),
+                        (dloss, torch.float32, (M,), "dloss"), (dH, torch.bfloat16, (M, K), "dH"),
+                        (dW, None if dW is None else dW.dtype, (V, K), "dW")))
+    ws, n = _scratch(cur, workspace)
+    _check(load_library().bl_linear_xent_backward(*p[:5], M, V, K, p[5], p[6], dwdt, 1 if accumulate_dW else 0, ws, n,
+                                                  _stream_of(stream, cur)), "bl_linear_xent_backward")
 
 
 @dataclass
@@ -416,31 +441,29 @@ class Act8:
                     scales=torch.empty((M, -(-K // 128)), dtype=torch.float32, device=device))
 
 
-def _need_act8(a, M, K, name):
-    _need(a.codes, torch.int8, (M, K), f"{name}.codes")
-    _need(a.scales, torch.float32, (M, -(-K // 128)), f"{name}.scales")
+def _act8_specs(a, M, K, name):
+    if a is None:
+        return (None,) * 4, (None,) * 4
+    return ((a.codes, torch.int8, (M, K), f"{name}.codes"),
+            (a.scales, torch.float32, (M, -(-K // 128)), f"{name}.scales"))
 
 
 def bl_act8_encode(x, saved: Act8, stream=None):
     """A1: saved <- the 8-bit form of x [M,K] (bf16|f32)."""
     M, K = x.shape
+    cur = _device(x, "x")
     dt = _dtype_code(x, "x")
-    _need(x, x.dtype, (M, K), "x")
-    _need_act8(saved, M, K, "saved")
-    _on_current_device(x, saved.codes, saved.scales)
-    _check(load_library().bl_act8_encode(_ptr(x), dt, M, K, _ptr(saved.codes), _ptr(saved.scales), _stream(stream)),
-           "bl_act8_encode")
+    p = _pointers(cur, ((x, x.dtype, (M, K), "x"), *_act8_specs(saved, M, K, "saved")))
+    _check(load_library().bl_act8_encode(p[0], dt, M, K, p[1], p[2], _stream_of(stream, cur)), "bl_act8_encode")
 
 
 def bl_act8_decode(saved: Act8, x, stream=None):
     """A2: x [M,K] (bf16|f32) <- the saved values."""
     M, K = x.shape
+    cur = _device(x, "x")
     dt = _dtype_code(x, "x")
-    _need(x, x.dtype, (M, K), "x")
-    _need_act8(saved, M, K, "saved")
-    _on_current_device(x, saved.codes, saved.scales)
-    _check(load_library().bl_act8_decode(_ptr(saved.codes), _ptr(saved.scales), M, K, _ptr(x), dt, _stream(stream)),
-           "bl_act8_decode")
+    p = _pointers(cur, (*_act8_specs(saved, M, K, "saved"), (x, x.dtype, (M, K), "x")))
+    _check(load_library().bl_act8_decode(p[0], p[1], M, K, p[2], dt, _stream_of(stream, cur)), "bl_act8_decode")
 
 
 def bl_norm_forward(x, weight, bias, eps, y, mean, rstd, rms=False, saved8: Act8 | None = None, stream=None):
@@ -448,27 +471,15 @@ def bl_norm_forward(x, weight, bias, eps, y, mean, rstd, rms=False, saved8: Act8
     bias [K] (bf16|f32, each may be None); mean (None with rms), rstd [M] f32;
     saved8 receives the 8-bit form of x."""
     M, K = x.shape
+    cur = _device(x, "x")
     dt = _dtype_code(x, "x")
-    _need(x, x.dtype, (M, K), "x")
-    _need(y, x.dtype, (M, K), "y")
-    _need(rstd, torch.float32, (M,), "rstd")
-    if mean is not None:
-        _need(mean, torch.float32, (M,), "mean")
-    pdt = BL_F32
-    for t, name in ((bias, "bias"), (weight, "weight")):
-        if t is not None:
-            pdt = _dtype_code(t, name)
-            _need(t, t.dtype, (K,), name)
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        raise ValueError(f"weight and bias must have one dtype, got {weight.dtype} and {bias.dtype}")
-    codes = scales = None
-    if saved8 is not None:
-        _need_act8(saved8, M, K, "saved8")
-        codes, scales = saved8.codes, saved8.scales
-    _on_current_device(x, weight, bias, y, mean, rstd, codes, scales)
-    _check(load_library().bl_norm_forward(_ptr(x), dt, _ptr(weight), _ptr(bias), pdt, M, K, float(eps), int(bool(rms)),
-                                          _ptr(y), _ptr(mean), _ptr(rstd), _ptr(codes), _ptr(scales),
-                                          _stream(stream)), "bl_norm_forward")
+    param = weight if weight is not None else bias
+    pdt, ptype = (BL_F32, None) if param is None else (_dtype_code(param, "weight or bias"), param.dtype)
+    p = _pointers(cur, ((x, x.dtype, (M, K), "x"), (weight, ptype, (K,), "weight"), (bias, ptype, (K,), "bias"),
+                        (y, x.dtype, (M, K), "y"), (mean, torch.float32, (M,), "mean"),
+                        (rstd, torch.float32, (M,), "rstd"), *_act8_specs(saved8, M, K, "saved8")))
+    _check(load_library().bl_norm_forward(p[0], dt, p[1], p[2], pdt, M, K, eps, 1 if rms else 0, *p[3:8],
+                                          _stream_of(stream, cur)), "bl_norm_forward")
 
 
 def bl_norm_backward_workspace_size(M: int, K: int) -> int:
@@ -480,63 +491,46 @@ def bl_norm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=Non
     """N2: dx [M,K], dweight, dbias [K] (each may be None) of N1. x: the forward's
     input, or the Act8 that the forward saved."""
     M, K = dy.shape
+    cur = _device(dy, "dy")
     dt = _dtype_code(dy, "dy")
-    _need(dy, dy.dtype, (M, K), "dy")
-    codes = scales = None
+    saved8 = None
     if isinstance(x, Act8):
-        _need_act8(x, M, K, "x")
-        codes, scales, x = x.codes, x.scales, None
-    else:
-        _need(x, dy.dtype, (M, K), "x")
-    _need(rstd, torch.float32, (M,), "rstd")
-    if mean is not None:
-        _need(mean, torch.float32, (M,), "mean")
-    if dx is not None:
-        _need(dx, dy.dtype, (M, K), "dx")
-    params = [(t, name) for t, name in ((weight, "weight"), (dweight, "dweight"), (dbias, "dbias")) if t is not None]
-    for t, name in params:
-        _dtype_code(t, name)
-        _need(t, params[0][0].dtype, (K,), name)
-    pdt = _dtype_code(*params[0]) if params else BL_F32
-    _on_current_device(dy, x, codes, scales, weight, mean, rstd, dx, dweight, dbias, workspace)
-    _check(load_library().bl_norm_backward(_ptr(dy), _ptr(x), _ptr(codes), _ptr(scales), dt, _ptr(weight), pdt,
-                                           _ptr(mean), _ptr(rstd), M, K, int(bool(rms)), _ptr(dx), _ptr(dweight),
-                                           _ptr(dbias), int(bool(accumulate)), _ptr(workspace),
-                                           _workspace_bytes(workspace), _stream(stream)), "bl_norm_backward")
+        saved8, x = x, None
+    param = weight if weight is not None else dweight if dweight is not None else dbias
+    pdt, ptype = (BL_F32, None) if param is None else (_dtype_code(param, "weight, dweight or dbias"), param.dtype)
+    p = _pointers(cur, ((dy, dy.dtype, (M, K), "dy"), (x, dy.dtype, (M, K), "x"), *_act8_specs(saved8, M, K, "x"),
+                        (weight, ptype, (K,), "weight"), (mean, torch.float32, (M,), "mean"),
+                        (rstd, torch.float32, (M,), "rstd"), (dx, dy.dtype, (M, K), "dx"),
+                        (dweight, ptype, (K,), "dweight"), (dbias, ptype, (K,), "dbias")))
+    ws, n = _scratch(cur, workspace)
+    _check(load_library().bl_norm_backward(*p[:4], dt, p[4], pdt, p[5], p[6], M, K, 1 if rms else 0, *p[7:10],
+                                           1 if accumulate else 0, ws, n, _stream_of(stream, cur)),
+           "bl_norm_backward")
 
 
 def bl_swiglu_forward(gate, up, y, gate8: Act8 | None = None, up8: Act8 | None = None, stream=None):
     """U1: y [M,K] = silu(gate) * up (bf16|f32); gate8, up8 (both or neither)
     receive the 8-bit forms of gate and up."""
     M, K = gate.shape
+    cur = _device(gate, "gate")
     dt = _dtype_code(gate, "gate")
-    _need(gate, gate.dtype, (M, K), "gate")
-    _need(up, gate.dtype, (M, K), "up")
-    _need(y, gate.dtype, (M, K), "y")
     if (gate8 is None) != (up8 is None):
         raise ValueError("gate8 and up8 go together")
-    saved = [None] * 4
-    if gate8 is not None:
-        _need_act8(gate8, M, K, "gate8")
-        _need_act8(up8, M, K, "up8")
-        saved = [gate8.codes, gate8.scales, up8.codes, up8.scales]
-    _on_current_device(gate, up, y, *saved)
-    _check(load_library().bl_swiglu_forward(_ptr(gate), _ptr(up), dt, M, K, _ptr(y), *[_ptr(t) for t in saved],
-                                            _stream(stream)), "bl_swiglu_forward")
+    p = _pointers(cur, ((gate, gate.dtype, (M, K), "gate"), (up, gate.dtype, (M, K), "up"), (y, gate.dtype, (M, K), "y"),
+                        *_act8_specs(gate8, M, K, "gate8"), *_act8_specs(up8, M, K, "up8")))
+    _check(load_library().bl_swiglu_forward(p[0], p[1], dt, M, K, *p[2:7], _stream_of(stream, cur)),
+           "bl_swiglu_forward")
 
 
 def bl_swiglu_backward(dy, gate8: Act8, up8: Act8, dgate, dup, stream=None):
     """U2: dgate, dup [M,K] of U1 from the 8-bit forms of gate and up."""
     M, K = dy.shape
+    cur = _device(dy, "dy")
     dt = _dtype_code(dy, "dy")
-    _need(dy, dy.dtype, (M, K), "dy")
-    _need_act8(gate8, M, K, "gate8")
-    _need_act8(up8, M, K, "up8")
-    _need(dgate, dy.dtype, (M, K), "dgate")
-    _need(dup, dy.dtype, (M, K), "dup")
-    _on_current_device(dy, gate8.codes, gate8.scales, up8.codes, up8.scales, dgate, dup)
-    _check(load_library().bl_swiglu_backward(_ptr(dy), _ptr(gate8.codes), _ptr(gate8.scales), _ptr(up8.codes),
-                                             _ptr(up8.scales), dt, M, K, _ptr(dgate), _ptr(dup), _stream(stream)),
+    p = _pointers(cur, ((dy, dy.dtype, (M, K), "dy"), *_act8_specs(gate8, M, K, "gate8"),
+                        *_act8_specs(up8, M, K, "up8"), (dgate, dy.dtype, (M, K), "dgate"),
+                        (dup, dy.dtype, (M, K), "dup")))
+    _check(load_library().bl_swiglu_backward(*p[:5], dt, M, K, p[5], p[6], _stream_of(stream, cur)),
            "bl_swiglu_backward")
 
 

@@ -1,8 +1,12 @@
 // The 8-bit form of an activation, shared by the kernels that write or read it:
 // groups of 128 values of a row,
 //
-//   a = max(absmax, 1e-30);  code = rint(fp32(x * fp32(127 / a)));
-//   scale = fp32(a / 127);   saved value = fp32(code * scale)
+//   a = max(absmax, 1e-30);        inv = fp32(fp32(1 / a) * 127)
+//   code = rint(fp32(x * inv));    scale = fp32(a * fp32(1 / 127))
+//   saved value = fp32(code * scale)
+//
+// (one reciprocal and two products per group instead of two divisions; three
+// half steps of fp32 cannot lift |x * inv| to 127.5, so codes end at 127).
 //
 // Two thread layouts. Vector (K % 8 == 0): 16 lanes hold 8 consecutive values
 // each, one 16-byte load (two for fp32) and one 8-byte code access per lane,
@@ -96,7 +100,7 @@ struct Act8Scale {
 __device__ __forceinline__ Act8Scale act8_scale(uint32_t absmax_bits) {
   if (absmax_bits >= 0x7F800000u) return {0.0f, __uint_as_float(0x7FC00000u)};
   const float a = fmaxf(__uint_as_float(absmax_bits), kAct8Floor);
-  return {__fdiv_rn(127.0f, a), __fdiv_rn(a, 127.0f)};
+  return {__fmul_rn(__frcp_rn(a), 127.0f), __fmul_rn(a, 1.0f / 127.0f)};
 }
 
 // The code in the low byte: |x * inv| rounds to at most 127, so adding

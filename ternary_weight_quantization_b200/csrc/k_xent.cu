@@ -59,7 +59,7 @@ constexpr int kOffEpi = kStages * kStageBytes;
 constexpr int kOffBar = kOffEpi + kEpiWarps * kEpiSlots * kEpiBox;
 constexpr int kNumBars = 2 * kStages + 5;  // full, empty, tmem_full[2], tmem_empty[2], done
 constexpr int kOffMisc = kOffBar + kNumBars * 8;
-constexpr int kSmemBytes = kOffMisc + 64 + 1024 /*base alignment*/;
+constexpr int kSmemBytes = kOffMisc + 64 /*TMEM base, abort flag, issued parities, epilogue maxima*/ + 1024 /*base alignment*/;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -75,10 +75,13 @@ struct XentParams {
   int tiles_m, tiles_k;  // tiles over tokens and over K
   // Lse
   float2* part;          // [vocab tile][M]: (max, sum exp(z - max))
-  float* tlogit;         // [M]
+  float2* tlogit;        // [M]: the target's logit, as the tile has it and as an fp32 dot product
+  const uint4* W;        // rows of W
   // Dz
   const float* lse;
   const float* dloss;
+  float* scale;          // max |dloss| of the tokens that count
+  int find_scale;        // first piece: form it; later ones read it
   int split;             // dz also as its bf16 remainder
   const uint4* h;        // rows of h, copied to hm with left-out rows cleared
   uint4* hm;             // (first piece only, else null)
@@ -356,21 +359,100 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) mbar_drain(done_bar, 0);
     __syncwarp();
-  } else if (warp >= kWarpEpi0) {
-    const int q = warp & 3;
+  } else if (warp < kWarpEpi0) {
+    // The loss is a difference with the target's logit, which the tensor
+    // core's sum leaves up to K / 16 steps of fp32 low: these two warps form
+    // it again as an fp32 dot product while the tiles run, and the join puts
+    // it in the place of the tile's.
+    if constexpr (P == Phase::Lse) {
+      const int per_row = p.K / 8;
+      for (int m = static_cast<int>(blockIdx.x) * 2 + warp - 2; m < p.M; m += 2 * static_cast<int>(gridDim.x)) {
+        const int64_t t = __ldg(p.targets + m);
+        if (t < 0 || t >= p.V) continue;
+        const uint4* a = p.h + static_cast<int64_t>(m) * per_row;
+        const uint4* b = p.W + t * per_row;
+        float z0 = 0.0f, z1 = 0.0f;
+#pragma unroll 4
+        for (int i = lane; i < per_row; i += 32) {
+          const uint4 x = __ldg(a + i), y = __ldg(b + i);
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            z0 = fmaf(bf16_lo(xs[j]), bf16_lo(ys[j]), z0);
+            z1 = fmaf(bf16_hi(xs[j]), bf16_hi(ys[j]), z1);
+          }
+        }
+        float z = z0 + z1;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        if (lane == 0) p.tlogit[m].y = z;
+      }
+    }
     if constexpr (P == Phase::Dz) {
       if (p.hm) {
-        // h with the left-out rows cleared, for dW: done here, where the first
-        // tile's products are still to come
-        const int per_row = p.K / 8;
-        const int64_t n = static_cast<int64_t>(p.M) * per_row;
-        const int64_t T = static_cast<int64_t>(gridDim.x) * (kEpiWarps * 32);
-        for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kEpiWarps * 32) + (threadIdx.x - kWarpEpi0 * 32); i < n; i += T) {
-          const int64_t t = __ldg(p.targets + i / per_row);
-          p.hm[i] = t >= 0 && t < p.V ? __ldg(p.h + i) : make_uint4(0u, 0u, 0u, 0u);
+        // h with the left-out rows cleared, for dW (0 * NaN would be NaN)
+        const int64_t n = static_cast<int64_t>(p.M) * (p.K / 8);
+        const int64_t T = static_cast<int64_t>(gridDim.x) * 64;
+        const uint32_t per_row = static_cast<uint32_t>(p.K / 8);
+        const bool narrow = n <= 0xFFFFFFFFll;
+        constexpr int kU = 8;
+        for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * 64 + (threadIdx.x - 64); i0 < n; i0 += kU * T) {
+          uint4 v[kU];
+          int64_t t[kU];
+#pragma unroll
+          for (int u = 0; u < kU; ++u) {
+            const int64_t i = i0 + u * T;
+            if (i < n) {
+              v[u] = __ldg(p.h + i);
+              t[u] = __ldg(p.targets + (narrow ? static_cast<int64_t>(static_cast<uint32_t>(i) / per_row) : i / per_row));
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < kU; ++u) {
+            const int64_t i = i0 + u * T;
+            if (i < n) p.hm[i] = t[u] >= 0 && t[u] < p.V ? v[u] : make_uint4(0u, 0u, 0u, 0u);
+          }
         }
       }
     }
+  } else {
+    const int q = warp & 3;
+    float scale = 1.0f;
+    if constexpr (P == Phase::Dz) {
+      // dz is kept relative to the largest |dloss|: its target term -dloss
+      // would otherwise round the same way for every token of a mean
+      // (dloss = 1 / tokens), an error of up to 2^-8 of the whole gradient.
+      // The products' epilogues put the factor back in fp32.
+      if (p.find_scale) {
+        const int e = threadIdx.x - kWarpEpi0 * 32;
+        constexpr int kU = 8;  // tokens in flight per thread
+        float top = 0.0f;
+        for (int m0 = e; m0 < p.M; m0 += kU * kEpiWarps * 32) {
+          int64_t t[kU];
+          float a[kU];
+#pragma unroll
+          for (int i = 0; i < kU; ++i) {
+            const int m = m0 + i * kEpiWarps * 32;
+            t[i] = m < p.M ? __ldg(p.targets + m) : -1;
+            a[i] = m < p.M ? fabsf(__ldg(p.dloss + m)) : 0.0f;
+          }
+#pragma unroll
+          for (int i = 0; i < kU; ++i)
+            if (t[i] >= 0 && t[i] < p.V && a[i] < __uint_as_float(0x7F800000u)) top = fmaxf(top, a[i]);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        float* tops = reinterpret_cast<float*>(smem + kOffMisc + 32);
+        if (lane == 0) tops[warp - kWarpEpi0] = top;
+        asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
+        top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+        scale = top > 0.0f ? top : 1.0f;
+        if (blockIdx.x == 0 && e == 0) *p.scale = scale;
+      } else {
+        scale = *p.scale;
+      }
+    }
+    if constexpr (P == Phase::Grad) scale = __ldg(p.scale);
     Stager st{smem_u32(smem + kOffEpi + (warp - kWarpEpi0) * kEpiSlots * kEpiBox), 0u, lane};
     int buf = 0;
     uint32_t buf_phase = 0;
@@ -392,7 +474,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             keep = 0xFFFFFFFFu;
             if constexpr (P == Phase::Dz) {
               nlse = -__ldg(p.lse + row) * kLog2e;
-              g = __ldg(p.dloss + row);
+              g = __fdiv_rn(__ldg(p.dloss + row), scale);
             }
           }
         }
@@ -417,7 +499,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             float z = 0.0f;
 #pragma unroll
             for (int j = 0; j < 32; ++j) z = j == tgt - 32 * c ? __uint_as_float(r[j]) : z;
-            p.tlogit[row] = z;
+            p.tlogit[row].x = z;
           }
           if (p.v0 + col < p.V) ls.chunk(r, p.V - (p.v0 + col));
         } else if constexpr (P == Phase::Dz) {
@@ -459,6 +541,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         } else {
           if (col >= p.K) continue;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * scale);
           const bool live = row0 < (t.cls == 0 ? p.M : p.vcount);
           const bool f32 = t.cls == 0 ? p.h_f32 != 0 : p.w_f32 != 0;
           if (f32) {
@@ -523,7 +607,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // lse and loss from the vocabulary tiles' (max, sum): 32 tokens per block, the
 // tiles spread over 32 threads of each token, joined in a fixed order.
 __global__ void __launch_bounds__(1024) xent_join_kernel(const float2* __restrict__ part, int tiles, int M, int V,
-                                                         const float* __restrict__ tlogit,
+                                                         const float2* __restrict__ tlogit,
                                                          const int64_t* __restrict__ targets, float* loss, float* lse) {
   pdl_wait_primary();
   pdl_launch_dependents();
@@ -552,10 +636,19 @@ __global__ void __launch_bounds__(1024) xent_join_kernel(const float2* __restric
   }
   const int mm = static_cast<int>(blockIdx.x) * 32 + y;
   if (x == 0 && mm < M) {
-    const float l = a.x + logf(a.y);
+    float l = a.x + logf(a.y);
     const int64_t t = targets[mm];
+    float nll = 0.0f;
+    if (t >= 0 && t < V) {
+      // the fp32 target logit in the place of the tile's, in lse too: a token
+      // whose target holds nearly all of the sum keeps a loss near 0
+      const float2 tl = tlogit[mm];
+      const float d = __expf(tl.y - l) - __expf(tl.x - l);
+      if (d > -0.5f) l += log1pf(d);
+      nll = l - tl.y;
+    }
     lse[mm] = l;
-    loss[mm] = t >= 0 && t < V ? l - tlogit[mm] : 0.0f;
+    loss[mm] = nll;
   }
 }
 
@@ -613,7 +706,7 @@ struct Plan {
   int pieces, slices;
   int64_t rows_pad;
   bool sums;       // dH goes through fp32 partial sums
-  size_t off_lo, off_h, off_sum, bytes;
+  size_t off_lo, off_h, off_scale, off_sum, bytes;
 };
 
 constexpr int64_t kPieceBytes = int64_t(64) << 20;
@@ -643,6 +736,8 @@ Plan make_plan(int64_t M, int64_t V, int64_t K, bool f32) {
   if (f32) off += align256(static_cast<size_t>(M) * q.piece * 2);
   q.off_h = off;
   off += align256(static_cast<size_t>(M) * K * 2);
+  q.off_scale = off;
+  off += 256;
   q.off_sum = off;
   if (q.sums) off += static_cast<size_t>(q.slices) * q.rows_pad * K * 4;
   q.bytes = off;
@@ -652,7 +747,7 @@ Plan make_plan(int64_t M, int64_t V, int64_t K, bool f32) {
 }  // namespace
 
 size_t xent_forward_workspace_bytes(int64_t M, int64_t V, int64_t K) {
-  return align256(static_cast<size_t>(tiles_of(V)) * M * 8) + align256(static_cast<size_t>(M) * 4);
+  return align256(static_cast<size_t>(tiles_of(V)) * M * 8) + align256(static_cast<size_t>(M) * 8);
 }
 
 size_t xent_backward_workspace_bytes(int64_t M, int64_t V, int64_t K, int dw_is_f32) {
@@ -676,11 +771,13 @@ cudaError_t launch_xent_forward(const void* h, const void* W, const int64_t* tar
   p.tiles_k = tiles_of(K);
   const int tiles_v = tiles_of(V);
   p.ntiles = p.tiles_m * tiles_v;
+  p.h = static_cast<const uint4*>(h);
+  p.W = static_cast<const uint4*>(W);
   p.part = static_cast<float2*>(workspace);
-  p.tlogit = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256(static_cast<size_t>(tiles_v) * M * 8));
+  p.tlogit = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + align256(static_cast<size_t>(tiles_v) * M * 8));
   if (cudaError_t e = launch_phase<Phase::Lse>(maps, p, s); e != cudaSuccess) return e;
   return launch_pdl(xent_join_kernel, dim3(static_cast<unsigned>((M + 31) / 32)), dim3(1024), 0, s,
-                    static_cast<const float2*>(p.part), tiles_v, p.M, p.V, static_cast<const float*>(p.tlogit), targets,
+                    static_cast<const float2*>(p.part), tiles_v, p.M, p.V, static_cast<const float2*>(p.tlogit), targets,
                     loss, lse);
 }
 
@@ -711,6 +808,7 @@ cudaError_t launch_xent_backward(const void* h, const void* W, const int64_t* ta
   p.dloss = dloss;
   p.split = f32;
   p.h = static_cast<const uint4*>(h);
+  p.scale = reinterpret_cast<float*>(ws + q.off_scale);
   p.slices = q.slices;
   p.rows_pad = static_cast<int>(q.rows_pad);
   p.h_f32 = q.sums;
@@ -742,6 +840,7 @@ cudaError_t launch_xent_backward(const void* h, const void* W, const int64_t* ta
                 !make_swizzled_map(&zm[5], lo, false, p.vcount, M, q.piece * 2, 64, 32, "dz remainder (store)")))
       return cudaErrorInvalidValue;
     p.hm = i == 0 && dW ? static_cast<uint4*>(hm) : nullptr;
+    p.find_scale = i == 0;
     p.ntiles = p.tiles_m * tiles_of(p.vcount);
     if (cudaError_t e = launch_phase<Phase::Dz>(zm, p, s); e != cudaSuccess) return e;
     // an fp32 dW joins partial sums of 1024 tokens, one launch each (the
