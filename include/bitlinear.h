@@ -363,7 +363,7 @@ bl_status bl_signsgd_apply(const uint32_t* sign_words, int ranks, void* W, bl_dt
  * (infinities and NaN included) does not matter.
  * workspace: at least bl_linear_xent_forward_workspace_size(M,V,K) bytes,
  * 16-byte aligned, no initialisation, one call at a time per workspace: one
- * (maximum, sum) pair per token and 256 vocabulary entries, never the logits.
+ * (maximum, sum) pair per token and 128 vocabulary entries, never the logits.
  * Limits: K a multiple of 8 up to 65536, M up to 131072, V up to 2^24.
  * M == 0 is a no-op (the workspace size is then 0).
  * Errors: BL_ERR_INVALID_ARG, BL_ERR_UNSUPPORTED_SHAPE, BL_ERR_ALIGNMENT,
@@ -440,7 +440,7 @@ bl_status bl_act8_decode(const int8_t* codes, const float* scales, int64_t M, in
  * zeros; y [M,K] of x_dtype; mean, rstd [M] float, kept for N2 (mean is not
  * touched with rms != 0 and may then be NULL). codes and scales, both or
  * neither NULL, receive the 8-bit form of x (A1) for N2, in the same pass
- * when K is a multiple of 8 and at most 32768.
+ * when K is a multiple of 8 and at most 16384.
  * eps must be finite and >= 0. K >= 1 is any size; M == 0 is a no-op.
  * Errors: as A1.
  */

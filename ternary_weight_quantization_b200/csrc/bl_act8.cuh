@@ -8,6 +8,10 @@
 // (one reciprocal and two products per group instead of two divisions; three
 // half steps of fp32 cannot lift |x * inv| to 127.5, so codes end at 127).
 //
+// The arithmetic on 8 consecutive values runs on pairs (packed fp32x2
+// instructions, each half rounded like the scalar one): these kernels are
+// bound by the instructions they issue as much as by HBM.
+//
 // Two thread layouts. Vector (K % 8 == 0): 16 lanes hold 8 consecutive values
 // each, one 16-byte load (two for fp32) and one 8-byte code access per lane,
 // two groups to a warp. Scalar (any K: rows start at any element): 32 lanes
@@ -40,7 +44,52 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float hi, float lo) {
   return r;
 }
 
-// 8 consecutive values at a 16-byte aligned address.
+// ---- pairs of fp32 values
+using f32x2 = uint64_t;
+
+__device__ __forceinline__ f32x2 pair2(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ f32x2 both2(float v) { return pair2(v, v); }
+__device__ __forceinline__ void split2(f32x2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float sum2(f32x2 v) {
+  float lo, hi;
+  split2(v, lo, hi);
+  return lo + hi;
+}
+
+// Maxima that keep a NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// 8 consecutive values at a 16-byte aligned address, as loaded.
 template <typename T>
 struct Raw8;
 template <>
@@ -48,9 +97,15 @@ struct Raw8<__nv_bfloat16> {
   uint4 a;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void clear() { a = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    v[0] = bf16_lo(a.x), v[1] = bf16_hi(a.x), v[2] = bf16_lo(a.y), v[3] = bf16_hi(a.y);
-    v[4] = bf16_lo(a.z), v[5] = bf16_hi(a.z), v[6] = bf16_lo(a.w), v[7] = bf16_hi(a.w);
+  __device__ __forceinline__ void get(f32x2 (&v)[4]) const {
+    v[0] = pair2(bf16_lo(a.x), bf16_hi(a.x)), v[1] = pair2(bf16_lo(a.y), bf16_hi(a.y));
+    v[2] = pair2(bf16_lo(a.z), bf16_hi(a.z)), v[3] = pair2(bf16_lo(a.w), bf16_hi(a.w));
+  }
+  // The largest |x|; a NaN if there is one.
+  __device__ __forceinline__ float absmax() const {
+    const uint32_t m = max_nan_bf16x2(max_nan_bf16x2(a.x & 0x7FFF7FFFu, a.y & 0x7FFF7FFFu),
+                                      max_nan_bf16x2(a.z & 0x7FFF7FFFu, a.w & 0x7FFF7FFFu));
+    return max_nan(bf16_lo(m), bf16_hi(m));
   }
 };
 template <>
@@ -61,18 +116,29 @@ struct Raw8<float> {
     b = reinterpret_cast<const float4*>(p)[1];
   }
   __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  __device__ __forceinline__ void get(f32x2 (&v)[4]) const {
+    v[0] = pair2(a.x, a.y), v[1] = pair2(a.z, a.w), v[2] = pair2(b.x, b.y), v[3] = pair2(b.z, b.w);
+  }
+  __device__ __forceinline__ float absmax() const {
+    return max_nan(max_nan(max_nan(fabsf(a.x), fabsf(a.y)), max_nan(fabsf(a.z), fabsf(a.w))),
+                   max_nan(max_nan(fabsf(b.x), fabsf(b.y)), max_nan(fabsf(b.z), fabsf(b.w))));
   }
 };
 
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[1], v[0]), pack_bf16x2(v[3], v[2]),
-                                            pack_bf16x2(v[5], v[4]), pack_bf16x2(v[7], v[6]));
+__device__ __forceinline__ uint32_t pack_bf16x2(f32x2 v) {
+  float lo, hi;
+  split2(v, lo, hi);
+  return pack_bf16x2(hi, lo);
 }
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const f32x2 (&v)[4]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0]), pack_bf16x2(v[1]), pack_bf16x2(v[2]), pack_bf16x2(v[3]));
+}
+__device__ __forceinline__ void store8(float* p, const f32x2 (&v)[4]) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split2(v[i], f[2 * i], f[2 * i + 1]);
+  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
@@ -80,16 +146,11 @@ __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162flo
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// Absmax of the group over its W lanes (every lane gets it), as bits: for
-// non-negative fp32 the order of the bits is the order of the values, with
-// infinity and NaN above all finite ones.
-template <bool kVec>
-__device__ __forceinline__ uint32_t act8_absmax_bits(const float (&v)[Act8Lane<kVec>::N]) {
-  uint32_t m = 0;
+// The group's absmax from its kLanes lanes' own (every lane gets it).
+template <int kLanes>
+__device__ __forceinline__ float act8_absmax(float m) {
 #pragma unroll
-  for (int i = 0; i < Act8Lane<kVec>::N; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-#pragma unroll
-  for (int s = Act8Lane<kVec>::W / 2; s > 0; s >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
+  for (int s = kLanes / 2; s > 0; s >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, s));
   return m;
 }
 
@@ -97,36 +158,48 @@ struct Act8Scale {
   float inv, scale;
 };
 
-__device__ __forceinline__ Act8Scale act8_scale(uint32_t absmax_bits) {
-  if (absmax_bits >= 0x7F800000u) return {0.0f, __uint_as_float(0x7FC00000u)};
-  const float a = fmaxf(__uint_as_float(absmax_bits), kAct8Floor);
+__device__ __forceinline__ Act8Scale act8_scale(float absmax) {
+  // infinity and NaN have the bits above all finite values'
+  if (__float_as_uint(absmax) >= 0x7F800000u) return {0.0f, __uint_as_float(0x7FC00000u)};
+  const float a = fmaxf(absmax, kAct8Floor);
   return {__fmul_rn(__frcp_rn(a), 127.0f), __fmul_rn(a, 1.0f / 127.0f)};
 }
 
 // The code in the low byte: |x * inv| rounds to at most 127, so adding
 // 1.5 * 2^23 rounds the product to an integer (half to even) in the low bits
-// of the sum. inv = 0 marks a group without finite codes: 0.
+// of the sum. (In a group that holds an infinity or a NaN inv is 0; its codes
+// do not matter, as its scale is NaN.)
 __device__ __forceinline__ uint32_t act8_code(float x, float inv) {
-  const uint32_t t = __float_as_uint(__fadd_rn(__fmul_rn(x, inv), 12582912.0f));
-  return inv == 0.0f ? 0u : t;
+  return __float_as_uint(__fadd_rn(__fmul_rn(x, inv), 12582912.0f));
 }
 
-__device__ __forceinline__ uint2 act8_codes8(const float (&v)[8], float inv) {
-  uint32_t t[8];
+__device__ __forceinline__ uint2 act8_codes8(const f32x2 (&v)[4], float inv) {
+  const f32x2 inv2 = both2(inv);
+  uint32_t t[4];  // two codes each
 #pragma unroll
-  for (int i = 0; i < 8; ++i) t[i] = act8_code(v[i], inv);
-  return make_uint2(__byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410),
-                    __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410));
+  for (int i = 0; i < 4; ++i) {
+    // the product is rounded before the addition: a packed addition after the
+    // packed product was measured to come out as one fused operation (codes
+    // at ties differ), the scalar ones do not
+    float lo, hi;
+    split2(mul2(v[i], inv2), lo, hi);
+    t[i] = __byte_perm(__float_as_uint(__fadd_rn(lo, 12582912.0f)), __float_as_uint(__fadd_rn(hi, 12582912.0f)), 0x0040);
+  }
+  return make_uint2(__byte_perm(t[0], t[1], 0x5410), __byte_perm(t[2], t[3], 0x5410));
 }
 
 // Saved values of 8 codes. fp32(code) through the 2^23 shifter: the bits
 // 0x4B0000uu are 2^23 + u with u = code + 128.
-__device__ __forceinline__ void act8_values8(const uint2& c, float scale, float (&v)[8]) {
+__device__ __forceinline__ void act8_values8(const uint2& c, float scale, f32x2 (&v)[4]) {
   const uint32_t w[2] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u};
+  const f32x2 shift2 = both2(-8388736.0f), scale2 = both2(scale);
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    v[i] = __fmul_rn(__fsub_rn(__uint_as_float(__byte_perm(w[i >> 2], 0x4B000000u, 0x7440u | (i & 3))), 8388736.0f),
-                     scale);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t b = 2 * (i & 1);
+    const uint32_t lo = __byte_perm(w[i >> 1], 0x4B000000u, 0x7440u | b);
+    const uint32_t hi = __byte_perm(w[i >> 1], 0x4B000000u, 0x7440u | (b + 1));
+    v[i] = mul2(add2((static_cast<uint64_t>(hi) << 32) | lo, shift2), scale2);
+  }
 }
 
 __device__ __forceinline__ float act8_value(int8_t code, float scale) {

@@ -11,13 +11,13 @@
 // All four are streams bound by HBM: per value (bf16) A1 moves 3 bytes, A2 3,
 // U1 8 (6 without the 8-bit forms) and U2 8. A unit of work is one group of
 // 128 values (half a warp of 8-value lanes where K % 8 == 0, else a warp, see
-// bl_act8.cuh). Each thread takes kU units spaced one grid apart, so that
-// every load of a warp is contiguous and all of a thread's loads are in
-// flight before it computes.
+// bl_act8.cuh). A block takes consecutive units, kU per thread, and issues all
+// of a thread's loads before it computes.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "bl_act8.cuh"
 #include "bl_device.cuh"
@@ -28,22 +28,43 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// One lane's share of a unit: `off` is the element offset of the lane's first
-// value, n how many of its values exist (vector: 0 or 8; scalar: values l,
-// l + 32, ... below the group's length).
+// A unit: its first element and its length.
 struct Unit {
   int64_t off;
-  int len;  // values of the group
+  int len;  // values of the group (0: no unit)
 };
 
-__device__ __forceinline__ Unit unit_at(int64_t u, int groups, int K, bool narrow) {
-  const int64_t row = narrow ? static_cast<int64_t>(static_cast<uint32_t>(u) / static_cast<uint32_t>(groups)) : u / groups;
-  const int g = static_cast<int>(u - row * groups);
-  const int left = K - g * kAct8Group;
-  return {row * K + static_cast<int64_t>(g) * kAct8Group, left < kAct8Group ? left : kAct8Group};
-}
+// The units of a block: kPer consecutive ones. With whole groups only
+// (K % 128 == 0) unit u starts at element 128 u; else each row before it
+// takes `pad` = 128 G - K off. The row of a unit is found once per block by a
+// division and from there by a product: for n < 2^22, floor((n + 1/2) (1 / G))
+// in fp32 is floor(n / G) (the product is off by less than 1 / (2 G)).
+struct Units {
+  int64_t first, count, row0;
+  int g0, groups, pad, last;
+  float inv;
+  __device__ __forceinline__ Units(int64_t f, int64_t n, int g, int K) : first(f), count(n), groups(g) {
+    pad = g * kAct8Group - K;
+    last = kAct8Group - pad;
+    if (pad) {
+      row0 = n <= 0xFFFFFFFFll ? static_cast<int64_t>(static_cast<uint32_t>(f) / static_cast<uint32_t>(g)) : f / g;
+      g0 = static_cast<int>(f - row0 * g);
+      inv = 1.0f / static_cast<float>(g);
+    }
+  }
+  __device__ __forceinline__ Unit at(int i) const {
+    const int64_t u = first + i;
+    if (u >= count) return {0, 0};
+    if (!pad) return {u * kAct8Group, kAct8Group};
+    // more groups than 2^21 to a row: the block's units cross one row end at most
+    const int n = g0 + i;
+    const int q = groups > (1 << 21) ? (n >= groups) : static_cast<int>((static_cast<float>(n) + 0.5f) * inv);
+    return {u * kAct8Group - (row0 + q) * pad, n - q * groups == groups - 1 ? last : kAct8Group};
+  }
+};
 
-// A lane's values of a unit, as loaded.
+// A lane's values of a unit, as loaded; n() of them come in `Val`s (pairs in
+// the vector layout, single values in the scalar one).
 template <typename T, bool kVec>
 struct Loaded;
 template <typename T>
@@ -53,7 +74,8 @@ struct Loaded<T, true> {
     if (l * 8 < u.len) r.load(p + u.off + l * 8);
     else r.clear();
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const { r.get(v); }
+  __device__ __forceinline__ void get(f32x2 (&v)[4]) const { r.get(v); }
+  __device__ __forceinline__ float absmax() const { return act8_absmax<16>(r.absmax()); }
 };
 template <typename T>
 struct Loaded<T, false> {
@@ -66,6 +88,9 @@ struct Loaded<T, false> {
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = r[j];
   }
+  __device__ __forceinline__ float absmax() const {
+    return act8_absmax<32>(max_nan(max_nan(fabsf(r[0]), fabsf(r[1])), max_nan(fabsf(r[2]), fabsf(r[3]))));
+  }
 };
 
 template <bool kVec>
@@ -76,7 +101,7 @@ struct LoadedCodes<true> {
   __device__ __forceinline__ void load(const int8_t* p, const Unit& u, int l) {
     c = l * 8 < u.len ? *reinterpret_cast<const uint2*>(p + u.off + l * 8) : make_uint2(0u, 0u);
   }
-  __device__ __forceinline__ void get(float scale, float (&v)[8]) const { act8_values8(c, scale, v); }
+  __device__ __forceinline__ void get(float scale, f32x2 (&v)[4]) const { act8_values8(c, scale, v); }
 };
 template <>
 struct LoadedCodes<false> {
@@ -92,7 +117,7 @@ struct LoadedCodes<false> {
 };
 
 template <typename T>
-__device__ __forceinline__ void store_values(T* p, const Unit& u, int l, const float (&v)[8]) {
+__device__ __forceinline__ void store_values(T* p, const Unit& u, int l, const f32x2 (&v)[4]) {
   if (l * 8 < u.len) store8(p + u.off + l * 8, v);
 }
 template <typename T>
@@ -102,22 +127,18 @@ __device__ __forceinline__ void store_values(T* p, const Unit& u, int l, const f
     if (l + 32 * j < u.len) store1(p + u.off + l + 32 * j, v[j]);
 }
 
-// Codes and scale of one unit (every lane of the warp takes part).
-__device__ __forceinline__ void encode_unit(const float (&v)[8], bool live, const Unit& u, int64_t idx, int l,
+// Codes and scale of one unit.
+__device__ __forceinline__ void store_codes(const f32x2 (&v)[4], const Act8Scale& s, const Unit& u, int64_t idx, int l,
                                             int8_t* codes, float* scales) {
-  const Act8Scale s = act8_scale(act8_absmax_bits<true>(v));
-  if (!live) return;
   if (l * 8 < u.len) *reinterpret_cast<uint2*>(codes + u.off + l * 8) = act8_codes8(v, s.inv);
-  if (l == 0) scales[idx] = s.scale;
+  if (l == 0 && u.len > 0) scales[idx] = s.scale;
 }
-__device__ __forceinline__ void encode_unit(const float (&v)[4], bool live, const Unit& u, int64_t idx, int l,
+__device__ __forceinline__ void store_codes(const float (&v)[4], const Act8Scale& s, const Unit& u, int64_t idx, int l,
                                             int8_t* codes, float* scales) {
-  const Act8Scale s = act8_scale(act8_absmax_bits<false>(v));
-  if (!live) return;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     if (l + 32 * j < u.len) codes[u.off + l + 32 * j] = static_cast<int8_t>(act8_code(v[j], s.inv) & 0xFFu);
-  if (l == 0) scales[idx] = s.scale;
+  if (l == 0 && u.len > 0) scales[idx] = s.scale;
 }
 
 // 1 / (1 + exp(-g)). For bf16 results the hardware's approximations (a few
@@ -125,8 +146,41 @@ __device__ __forceinline__ void encode_unit(const float (&v)[4], bool live, cons
 // the rounded division.
 template <typename T>
 __device__ __forceinline__ float sigmoid(float g) {
-  if constexpr (sizeof(T) == 2) return __fdividef(1.0f, 1.0f + __expf(-g));
-  else return __fdiv_rn(1.0f, 1.0f + expf(-g));
+  if constexpr (sizeof(T) == 2) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+  } else {
+    return __fdiv_rn(1.0f, 1.0f + expf(-g));
+  }
+}
+
+// y = silu(g) u; and dg = d u s (1 + g (1 - s)), du = d g s.
+template <typename T>
+__device__ __forceinline__ void gate_forward(float g, float u, float& y) {
+  y = g * sigmoid<T>(g) * u;
+}
+template <typename T>
+__device__ __forceinline__ void gate_forward(f32x2 g, f32x2 u, f32x2& y) {
+  float a, b;
+  split2(g, a, b);
+  y = mul2(mul2(g, pair2(sigmoid<T>(a), sigmoid<T>(b))), u);
+}
+template <typename T>
+__device__ __forceinline__ void gate_backward(float d, float g, float u, float& dg, float& du) {
+  const float s = sigmoid<T>(g), ds = d * s;
+  dg = ds * u * fmaf(g, 1.0f - s, 1.0f);
+  du = ds * g;
+}
+template <typename T>
+__device__ __forceinline__ void gate_backward(f32x2 d, f32x2 g, f32x2 u, f32x2& dg, f32x2& du) {
+  float a, b;
+  split2(g, a, b);
+  const f32x2 one = both2(1.0f);
+  const f32x2 s = pair2(sigmoid<T>(a), sigmoid<T>(b)), ds = mul2(d, s);
+  dg = mul2(mul2(ds, u), fma2(g, fma2(s, both2(-1.0f), one), one));
+  du = mul2(ds, g);
 }
 
 struct Act8Args {
@@ -148,34 +202,29 @@ template <What what, typename T, bool kVec, int kU>
 __global__ void __launch_bounds__(kThreads) act8_kernel(const Act8Args p) {
   pdl_wait_primary();
   pdl_launch_dependents();
-  constexpr int W = Act8Lane<kVec>::W, N = Act8Lane<kVec>::N;
-  const int l = threadIdx.x % W;
-  const int64_t T0 = static_cast<int64_t>(gridDim.x) * (kThreads / W);
-  const bool narrow = p.units <= 0xFFFFFFFFll;
+  constexpr int W = Act8Lane<kVec>::W, kRow = kThreads / W;  // units that the block takes at once
+  constexpr int N = 4;  // pairs or single values per lane
+  using Val = std::conditional_t<kVec, f32x2, float>;
+  const int l = threadIdx.x % W, h = threadIdx.x / W;
   const T* a = static_cast<const T*>(p.a);
   const T* b = static_cast<const T*>(p.b);
-  // the loop runs on the whole warp's first unit, so that every lane of the
-  // warp takes part in its shuffles
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kThreads / W) + threadIdx.x / W;
-  for (int64_t base = first - threadIdx.x % 32 / W; base < p.units; base += kU * T0) {
-    const int64_t u0 = base + threadIdx.x % 32 / W;
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * (kRow * kU); first < p.units;
+       first += static_cast<int64_t>(gridDim.x) * (kRow * kU)) {
+    const Units all(first, p.units, p.groups, p.K);
+    const int64_t u0 = first + h;
+    constexpr int T0 = kRow;
     Unit u[kU];
-    bool live[kU];
 #pragma unroll
-    for (int i = 0; i < kU; ++i) {
-      const int64_t idx = u0 + i * T0;
-      live[i] = idx < p.units;
-      u[i] = live[i] ? unit_at(idx, p.groups, p.K, narrow) : Unit{0, 0};
-    }
+    for (int i = 0; i < kU; ++i) u[i] = all.at(h + i * kRow);
     if constexpr (what == What::Encode) {
       Loaded<T, kVec> x[kU];
 #pragma unroll
       for (int i = 0; i < kU; ++i) x[i].load(a, u[i], l);
 #pragma unroll
       for (int i = 0; i < kU; ++i) {
-        float v[N];
+        Val v[N];
         x[i].get(v);
-        encode_unit(v, live[i], u[i], u0 + i * T0, l, p.c0, p.s0);
+        store_codes(v, act8_scale(x[i].absmax()), u[i], u0 + i * T0, l, p.c0, p.s0);
       }
     } else if constexpr (what == What::Decode) {
       LoadedCodes<kVec> c[kU];
@@ -183,11 +232,11 @@ __global__ void __launch_bounds__(kThreads) act8_kernel(const Act8Args p) {
 #pragma unroll
       for (int i = 0; i < kU; ++i) {
         c[i].load(p.c0, u[i], l);
-        s[i] = live[i] ? __ldg(p.s0 + u0 + i * T0) : 0.0f;
+        s[i] = u[i].len ? __ldg(p.s0 + u0 + i * T0) : 0.0f;
       }
 #pragma unroll
       for (int i = 0; i < kU; ++i) {
-        float v[N];
+        Val v[N];
         c[i].get(s[i], v);
         store_values(static_cast<T*>(p.o0), u[i], l, v);
       }
@@ -200,15 +249,15 @@ __global__ void __launch_bounds__(kThreads) act8_kernel(const Act8Args p) {
       }
 #pragma unroll
       for (int i = 0; i < kU; ++i) {
-        float gv[N], uv[N], y[N];
+        Val gv[N], uv[N], y[N];
         g[i].get(gv);
         q[i].get(uv);
 #pragma unroll
-        for (int j = 0; j < N; ++j) y[j] = gv[j] * sigmoid<T>(gv[j]) * uv[j];
+        for (int j = 0; j < N; ++j) gate_forward<T>(gv[j], uv[j], y[j]);
         store_values(static_cast<T*>(p.o0), u[i], l, y);
         if constexpr (what == What::FwdSave) {
-          encode_unit(gv, live[i], u[i], u0 + i * T0, l, p.c0, p.s0);
-          encode_unit(uv, live[i], u[i], u0 + i * T0, l, p.c1, p.s1);
+          store_codes(gv, act8_scale(g[i].absmax()), u[i], u0 + i * T0, l, p.c0, p.s0);
+          store_codes(uv, act8_scale(q[i].absmax()), u[i], u0 + i * T0, l, p.c1, p.s1);
         }
       }
     } else {
@@ -220,22 +269,17 @@ __global__ void __launch_bounds__(kThreads) act8_kernel(const Act8Args p) {
         d[i].load(a, u[i], l);
         cg[i].load(p.c0, u[i], l);
         cu[i].load(p.c1, u[i], l);
-        sg[i] = live[i] ? __ldg(p.s0 + u0 + i * T0) : 0.0f;
-        su[i] = live[i] ? __ldg(p.s1 + u0 + i * T0) : 0.0f;
+        sg[i] = u[i].len ? __ldg(p.s0 + u0 + i * T0) : 0.0f;
+        su[i] = u[i].len ? __ldg(p.s1 + u0 + i * T0) : 0.0f;
       }
 #pragma unroll
       for (int i = 0; i < kU; ++i) {
-        float dv[N], gv[N], uv[N], dg[N], du[N];
+        Val dv[N], gv[N], uv[N], dg[N], du[N];
         d[i].get(dv);
         cg[i].get(sg[i], gv);
         cu[i].get(su[i], uv);
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const float s = sigmoid<T>(gv[j]);
-          const float ds = dv[j] * s;
-          dg[j] = ds * uv[j] * fmaf(gv[j], 1.0f - s, 1.0f);
-          du[j] = ds * gv[j];
-        }
+        for (int j = 0; j < N; ++j) gate_backward<T>(dv[j], gv[j], uv[j], dg[j], du[j]);
         store_values(static_cast<T*>(p.o0), u[i], l, dg);
         store_values(static_cast<T*>(p.o1), u[i], l, du);
       }

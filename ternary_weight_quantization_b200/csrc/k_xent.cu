@@ -45,36 +45,48 @@
 namespace bl {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarpLoad = 0, kWarpMma = 1, kWarpEpi0 = 4, kEpiWarps = 4;
+enum class Phase { Lse, Dz, Grad };
+
+constexpr int kWarpLoad = 0, kWarpMma = 1, kWarpEpi0 = 4;
 constexpr int kTile = 256;              // rows and columns of a pair tile
 constexpr int kBlockR = 64;             // reduction per stage
 constexpr int kBox = 8192;              // one 64 x 64 bf16 box
-constexpr int kStages = 6;
 constexpr int kStageBytes = 4 * kBox;   // A and B: two boxes each
 constexpr uint32_t kTmemCols = 512;     // two accumulators of 256 columns
 constexpr int kEpiBox = 4096;           // output box: 32 rows x 128 bytes
-constexpr int kEpiSlots = 2;            // per epilogue warp
-constexpr int kOffEpi = kStages * kStageBytes;
-constexpr int kOffBar = kOffEpi + kEpiWarps * kEpiSlots * kEpiBox;
-constexpr int kNumBars = 2 * kStages + 5;  // full, empty, tmem_full[2], tmem_empty[2], done
-constexpr int kOffMisc = kOffBar + kNumBars * 8;
-constexpr int kSmemBytes = kOffMisc + 64 /*TMEM base, abort flag, issued parities, epilogue maxima*/ + 1024 /*base alignment*/;
-static_assert(kSmemBytes <= 232448, "shared memory budget");
+
+// Stages, epilogue warps and output boxes per epilogue warp of each phase.
+template <Phase P>
+struct Geo {
+  static constexpr int kStages = P == Phase::Lse ? 7 : P == Phase::Dz ? 5 : 6;
+  static constexpr int kEpiWarps = P == Phase::Grad ? 4 : 8;
+  static constexpr int kSlots = P == Phase::Lse ? 0 : 2;
+  static constexpr int kParts = kEpiWarps / 4;        // warps that share a TMEM lane quadrant
+  static constexpr int kChunks = 8 / kParts;          // 32-column chunks of each
+  static constexpr int kThreads = 32 * (kWarpEpi0 + kEpiWarps);
+  static constexpr int kOffEpi = kStages * kStageBytes;
+  static constexpr int kOffBar = kOffEpi + kEpiWarps * kSlots * kEpiBox;
+  static constexpr int kNumBars = 2 * kStages + 5;    // full, empty, tmem_full[2], tmem_empty[2], done
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  // TMEM base, abort flag, issued parities; epilogue maxima at 64
+  static constexpr int kSmemBytes = kOffMisc + 128 + 1024 /*base alignment*/;
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+};
 
 constexpr float kLog2e = 1.4426950408889634f;
-
-enum class Phase { Lse, Dz, Grad };
 
 struct XentParams {
   int M, V, K;
   int v0, vcount;        // this piece of the vocabulary
   const int64_t* targets;
   int* err;
-  int ntiles;
+  // The pairs' tiles: `ntiles_a` tiles taken round robin, then `ntiles_b`
+  // cheaper ones, of which the pairs without a last tile of the first kind
+  // (from `split_pair` on) take `more` each, before the others continue.
+  int ntiles_a, ntiles_b, split_pair, more;
   int tiles_m, tiles_k;  // tiles over tokens and over K
   // Lse
-  float2* part;          // [vocab tile][M]: (max, sum exp(z - max))
+  float2* part;          // [2 per vocab tile][M]: (max, sum exp(z - max)) of 128 columns
   float2* tlogit;        // [M]: the target's logit, as the tile has it and as an fp32 dot product
   const uint4* W;        // rows of W
   // Dz
@@ -87,6 +99,8 @@ struct XentParams {
   uint4* hm;             // (first piece only, else null)
   // Grad
   int ntiles_h;          // tiles of dH (all slices); the rest are dW's
+  int dw_first;          // dW's tiles are the costlier ones
+  int cost_a, cost_b;    // k-blocks of a tile of either kind
   int slices;            // the reduction of dH is split over this many partial sums
   int rows_pad;          // rows between the slices' partial sums
   int h_f32;             // dH goes to the fp32 partial sums (else straight to bf16)
@@ -103,6 +117,23 @@ struct Tile {
   int slice;
 };
 
+// The pair's i-th tile (false: none left).
+__device__ __forceinline__ bool next_tile(const XentParams& p, int pair, int npairs, int i, int& u) {
+  u = i * npairs + pair;
+  if (u < p.ntiles_a) return true;
+  const int own = pair < p.ntiles_a ? (p.ntiles_a - 1 - pair) / npairs + 1 : 0;
+  const int j = i - own;  // its j-th tile of the second kind
+  if (pair >= p.split_pair) {
+    u = j * (npairs - p.split_pair) + pair - p.split_pair;
+    if (j >= p.more) return false;
+  } else {
+    u = p.more * (npairs - p.split_pair) + j * p.split_pair + pair;
+  }
+  if (u >= p.ntiles_b) return false;
+  u += p.ntiles_a;
+  return true;
+}
+
 template <Phase P>
 __device__ __forceinline__ Tile decode(const XentParams& p, int u) {
   Tile t{};
@@ -111,7 +142,11 @@ __device__ __forceinline__ Tile decode(const XentParams& p, int u) {
     t.a0 = (u % p.tiles_m) * kTile;
     t.b0 = (u / p.tiles_m) * kTile;
     t.nkb = (p.K + kBlockR - 1) / kBlockR;
-  } else if (u < p.ntiles_h) {
+    return t;
+  }
+  // dH's tiles come first unless dW's are the costlier ones
+  if (p.dw_first) u = u < p.ntiles_a ? u + p.ntiles_h : u - p.ntiles_a;
+  if (u < p.ntiles_h) {
     const int per = p.tiles_m * p.tiles_k;
     t.slice = u / per;
     u -= t.slice * per;
@@ -159,7 +194,8 @@ __device__ __forceinline__ uint32_t box_chunk(uint32_t box, int lane, int j) {
   return box + static_cast<uint32_t>(lane) * 128u + (static_cast<uint32_t>(j ^ (lane & 7)) << 4);
 }
 
-// The epilogue warp's output staging: kEpiSlots boxes used in turn.
+// An epilogue warp's output staging: kSlots boxes used in turn.
+template <int kSlots>
 struct Stager {
   uint32_t base;
   uint32_t seq;
@@ -168,10 +204,10 @@ struct Stager {
   // whose stores are still to be issued.
   template <int kOpen = 0>
   __device__ __forceinline__ uint32_t next() {
-    static_assert(kOpen < kEpiSlots, "slots");
-    if (lane == 0) bulk_wait_group_read<kEpiSlots - 1 - kOpen>();
+    static_assert(kOpen < kSlots, "slots");
+    if (lane == 0) bulk_wait_group_read<kSlots - 1 - kOpen>();
     __syncwarp();
-    return base + (seq++ % kEpiSlots) * kEpiBox;
+    return base + (seq++ % kSlots) * kEpiBox;
   }
   // `live`: the box has rows inside the tensor.
   __device__ __forceinline__ void store(const CUtensorMap* map, uint32_t box, int x, int y, bool add, bool live) {
@@ -211,21 +247,23 @@ struct LseState {
 };
 
 template <Phase P>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
     xent_kernel(const __grid_constant__ CUtensorMap map_h, const __grid_constant__ CUtensorMap map_w,
                 const __grid_constant__ CUtensorMap map_dz, const __grid_constant__ CUtensorMap map_dz_lo,
                 const __grid_constant__ CUtensorMap out0, const __grid_constant__ CUtensorMap out1,
                 const __grid_constant__ XentParams p) {
+  using G = Geo<P>;
+  constexpr int kStages = G::kStages, kEpiWarps = G::kEpiWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::kOffBar);
   uint64_t* empty = full + kStages;
   uint64_t* tmem_full = full + 2 * kStages;
   uint64_t* tmem_empty = tmem_full + 2;
   uint64_t* done_bar = tmem_full + 4;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + kOffMisc);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
-  int* issued_parity = reinterpret_cast<int*>(smem + kOffMisc + 8);  // [kStages]
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + G::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + G::kOffMisc + 4);
+  int* issued_parity = reinterpret_cast<int*>(smem + G::kOffMisc + 8);  // [kStages]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -269,7 +307,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int u = pair; ok && u < p.ntiles; u += npairs) {
+      int u;
+      for (int i = 0; ok && next_tile(p, pair, npairs, i, u); ++i) {
         const Tile t = decode<P>(p, u);
         const int a0 = t.a0 + static_cast<int>(rank) * 128, b0 = t.b0 + static_cast<int>(rank) * 128;
         const int half = t.nkb >> 1;
@@ -327,7 +366,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int stage = 0, buf = 0;
       uint32_t phase = 0, buf_phase = 0;
       bool ok = true;
-      for (int u = pair; ok && u < p.ntiles; u += npairs) {
+      int u;
+      for (int i = 0; ok && next_tile(p, pair, npairs, i, u); ++i) {
         const Tile t = decode<P>(p, u);
         if (t.nkb == 0) continue;
         if (!wait(&tmem_empty[buf], buf_phase ^ 1)) break;
@@ -416,7 +456,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    const int q = warp & 3;
+    const int q = warp & 3, part = (warp - kWarpEpi0) >> 2;
     float scale = 1.0f;
     if constexpr (P == Phase::Dz) {
       // dz is kept relative to the largest |dloss|: its target term -dloss
@@ -442,10 +482,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        float* tops = reinterpret_cast<float*>(smem + kOffMisc + 32);
+        float* tops = reinterpret_cast<float*>(smem + G::kOffMisc + 64);
         if (lane == 0) tops[warp - kWarpEpi0] = top;
         asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
-        top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+#pragma unroll
+        for (int w = 0; w < kEpiWarps; ++w) top = fmaxf(top, tops[w]);
         scale = top > 0.0f ? top : 1.0f;
         if (blockIdx.x == 0 && e == 0) *p.scale = scale;
       } else {
@@ -453,10 +494,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
     if constexpr (P == Phase::Grad) scale = __ldg(p.scale);
-    Stager st{smem_u32(smem + kOffEpi + (warp - kWarpEpi0) * kEpiSlots * kEpiBox), 0u, lane};
+    Stager<G::kSlots> st{smem_u32(smem + G::kOffEpi + (warp - kWarpEpi0) * G::kSlots * kEpiBox), 0u, lane};
     int buf = 0;
     uint32_t buf_phase = 0;
-    for (int u = pair; u < p.ntiles; u += npairs) {
+    int u;
+    for (int i = 0; next_tile(p, pair, npairs, i, u); ++i) {
       const Tile t = decode<P>(p, u);
       if (t.nkb == 0) continue;
       const int row0 = t.a0 + static_cast<int>(rank) * 128 + q * 32;  // first D row of the warp
@@ -484,11 +526,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kTile;
       uint32_t box = 0, box_lo = 0;
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
+      for (int c = part * G::kChunks; c < (part + 1) * G::kChunks; ++c) {
         uint32_t r[32];
         tmem_ld_32x32b_x32(tbase + 32 * c, r);
         tmem_ld_wait();
-        if (c == 7) {
+        if (c == (part + 1) * G::kChunks - 1) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(lead(&tmem_empty[buf]));
@@ -529,7 +571,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const bool last = (c & 1) || col + 32 >= p.vcount;
           if (last) st.store(&out0, box, col & ~63, row0, false, row0 < p.M);
           if (p.split) {
-            if ((c & 1) == 0) box_lo = st.next<1>();
+            if ((c & 1) == 0) box_lo = st.template next<1>();
 #pragma unroll
             for (int j = 0; j < 16; ++j)
               hi[j] = pack_bf16x2(d[2 * j + 1] - bf16_hi(hi[j]), d[2 * j] - bf16_lo(hi[j]));
@@ -585,7 +627,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if constexpr (P == Phase::Lse) {
-        if (row < p.M) p.part[static_cast<int64_t>(t.b0 / kTile) * p.M + row] = make_float2(ls.m, ls.s);
+        if (row < p.M) p.part[static_cast<int64_t>(t.b0 / 128 + part) * p.M + row] = make_float2(ls.m, ls.s);
       }
       if (++buf == 2) {
         buf = 0;
@@ -670,31 +712,47 @@ __global__ void __launch_bounds__(256) xent_dh_kernel(const float4* __restrict__
 
 // ---------------------------------------------------------------- host side
 
+// Spreads the second kind of tiles so that the pairs end together: the least
+// end time at which they all fit. With ntiles_a = qP + e, the first e pairs
+// are busy with q + 1 of the first kind, the others with q.
+void share_tiles(XentParams& p, int npairs) {
+  p.split_pair = p.ntiles_a % npairs;
+  p.more = 0;
+  if (p.ntiles_b == 0) return;
+  const int64_t ahead = p.cost_a / p.cost_b;  // tiles of the second kind in one of the first
+  const int64_t e = p.split_pair, f = npairs - e;
+  int64_t more = p.ntiles_b / npairs;
+  while (f * more + (more > ahead ? e * (more - ahead) : 0) < p.ntiles_b) ++more;
+  p.more = static_cast<int>(more);
+}
+
 template <Phase P>
-cudaError_t launch_phase(const CUtensorMap (&maps)[6], const XentParams& p, cudaStream_t s) {
+cudaError_t launch_phase(const CUtensorMap (&maps)[6], XentParams& p, cudaStream_t s) {
   static int pairs_of[64] = {};  // pairs resident at once, by device
   int dev = 0;
   cudaGetDevice(&dev);
   int pairs = dev >= 0 && dev < 64 ? pairs_of[dev] : 0;
   if (!pairs) {
-    if (cudaError_t e = cudaFuncSetAttribute(xent_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (cudaError_t e = cudaFuncSetAttribute(xent_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<P>::kSmemBytes);
         e != cudaSuccess)
       return e;
     pairs = device_sm_count() / 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(2 * pairs);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.blockDim = dim3(Geo<P>::kThreads);
+    cfg.dynamicSmemBytes = Geo<P>::kSmemBytes;
     int clusters = 0;
     if (cudaOccupancyMaxActiveClusters(&clusters, xent_kernel<P>, &cfg) == cudaSuccess && clusters > 0 && clusters < pairs)
       pairs = clusters;
     cudaGetLastError();
     if (dev >= 0 && dev < 64) pairs_of[dev] = pairs;
   }
-  if (p.ntiles == 0) return cudaSuccess;
-  const int n = p.ntiles < pairs ? p.ntiles : pairs;
-  return launch_pdl(xent_kernel<P>, dim3(2 * n), dim3(kThreads), kSmemBytes, s, maps[0], maps[1], maps[2], maps[3],
-                    maps[4], maps[5], p);
+  const int ntiles = p.ntiles_a + p.ntiles_b;
+  if (ntiles == 0) return cudaSuccess;
+  const int n = ntiles < pairs ? ntiles : pairs;
+  share_tiles(p, n);
+  return launch_pdl(xent_kernel<P>, dim3(2 * n), dim3(Geo<P>::kThreads), Geo<P>::kSmemBytes, s, maps[0], maps[1],
+                    maps[2], maps[3], maps[4], maps[5], p);
 }
 
 int tiles_of(int64_t n) { return static_cast<int>((n + kTile - 1) / kTile); }
@@ -747,7 +805,7 @@ Plan make_plan(int64_t M, int64_t V, int64_t K, bool f32) {
 }  // namespace
 
 size_t xent_forward_workspace_bytes(int64_t M, int64_t V, int64_t K) {
-  return align256(static_cast<size_t>(tiles_of(V)) * M * 8) + align256(static_cast<size_t>(M) * 8);
+  return align256(static_cast<size_t>(tiles_of(V)) * M * 16) + align256(static_cast<size_t>(M) * 8);
 }
 
 size_t xent_backward_workspace_bytes(int64_t M, int64_t V, int64_t K, int dw_is_f32) {
@@ -770,14 +828,14 @@ cudaError_t launch_xent_forward(const void* h, const void* W, const int64_t* tar
   p.tiles_m = tiles_of(M);
   p.tiles_k = tiles_of(K);
   const int tiles_v = tiles_of(V);
-  p.ntiles = p.tiles_m * tiles_v;
+  p.ntiles_a = p.tiles_m * tiles_v;
   p.h = static_cast<const uint4*>(h);
   p.W = static_cast<const uint4*>(W);
   p.part = static_cast<float2*>(workspace);
-  p.tlogit = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + align256(static_cast<size_t>(tiles_v) * M * 8));
+  p.tlogit = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + align256(static_cast<size_t>(tiles_v) * M * 16));
   if (cudaError_t e = launch_phase<Phase::Lse>(maps, p, s); e != cudaSuccess) return e;
   return launch_pdl(xent_join_kernel, dim3(static_cast<unsigned>((M + 31) / 32)), dim3(1024), 0, s,
-                    static_cast<const float2*>(p.part), tiles_v, p.M, p.V, static_cast<const float2*>(p.tlogit), targets,
+                    static_cast<const float2*>(p.part), 2 * tiles_v, p.M, p.V, static_cast<const float2*>(p.tlogit), targets,
                     loss, lse);
 }
 
@@ -841,7 +899,8 @@ cudaError_t launch_xent_backward(const void* h, const void* W, const int64_t* ta
       return cudaErrorInvalidValue;
     p.hm = i == 0 && dW ? static_cast<uint4*>(hm) : nullptr;
     p.find_scale = i == 0;
-    p.ntiles = p.tiles_m * tiles_of(p.vcount);
+    p.ntiles_a = p.tiles_m * tiles_of(p.vcount);
+    p.ntiles_b = 0;
     if (cudaError_t e = launch_phase<Phase::Dz>(zm, p, s); e != cudaSuccess) return e;
     // an fp32 dW joins partial sums of 1024 tokens, one launch each (the
     // launches order the additions)
@@ -852,7 +911,15 @@ cudaError_t launch_xent_backward(const void* h, const void* W, const int64_t* ta
       p.ntiles_h = dH && t0 == 0 ? p.slices * p.tiles_m * p.tiles_k : 0;
       p.h_add = i > 0;
       p.w_add = accumulate || t0 > 0;
-      p.ntiles = p.ntiles_h + (dW ? tiles_of(p.vcount) * p.tiles_k : 0);
+      const int ntiles_w = dW ? tiles_of(p.vcount) * p.tiles_k : 0;
+      const int cost_h = (p.vcount + kBlockR - 1) / kBlockR / p.slices;
+      const int cost_w = (p.tcount + kBlockR - 1) / kBlockR * (p.split ? 2 : 1);
+      p.dw_first = cost_w > cost_h || p.ntiles_h == 0;
+      p.ntiles_a = p.dw_first ? ntiles_w : p.ntiles_h;
+      p.ntiles_b = p.dw_first ? p.ntiles_h : ntiles_w;
+      // a tile also costs its epilogue, about 4 k-blocks
+      p.cost_a = (p.dw_first ? cost_w : cost_h) + 4;
+      p.cost_b = (p.dw_first ? cost_h : cost_w) + 4;
       if (cudaError_t e = launch_phase<Phase::Grad>(gm, p, s); e != cudaSuccess) return e;
       if (!dW) break;
     }

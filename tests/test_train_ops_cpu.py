@@ -87,9 +87,9 @@ def test_empty_work_is_ok_without_gpu():
 
 
 def test_workspace_sizes():
-    # forward: a (maximum, sum) pair per token and 256 vocabulary entries, and
+    # forward: a (maximum, sum) pair per token and 128 vocabulary entries, and
     # the target's logit per token (twice)
-    assert bl.bl_linear_xent_forward_workspace_size(2048, 8192, 512) == 32 * 2048 * 8 + 2048 * 8
+    assert bl.bl_linear_xent_forward_workspace_size(2048, 8192, 512) == 64 * 2048 * 8 + 2048 * 8
     assert bl.bl_linear_xent_forward_workspace_size(1, 257, 8) == 256 + 256
     assert bl.bl_linear_xent_forward_workspace_size(0, 8192, 512) == 0
     assert bl.bl_linear_xent_forward_workspace_size(4, 8192, 60) == 0
