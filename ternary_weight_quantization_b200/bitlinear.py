@@ -1,5 +1,9 @@
 """Thin Python binding of libbitlinear.so (argument marshalling only).
 
+The training operators next to the layer go through the extension module
+_binding (csrc/binding.cpp), which makes the same checks and the call in one
+step; where it finds an argument that does not fit, the checks here say which.
+
 Each function has the name of the C entry point it calls, takes torch CUDA
 tensors, checks dtype / shape / contiguity, passes raw device pointers and
 the current CUDA stream, and raises :class:`BitLinearError` on any status
@@ -74,6 +78,7 @@ class BitLinearError(RuntimeError):
 
 
 _LIB = None
+_QUICK = None
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -90,6 +95,19 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         fn.argtypes = args
     _LIB = lib
     return lib
+
+
+def _quick():
+    """The extension module (raises if absent)."""
+    global _QUICK
+    if _QUICK is None:
+        load_library()
+        if not os.path.exists(os.path.join(_PKG, "_binding.so")):
+            raise RuntimeError(f"{_PKG}/_binding.so is missing: build it with "
+                               "`python -m ternary_weight_quantization_b200.build`")
+        from . import _binding
+        _QUICK = _binding
+    return _QUICK
 
 
 def _check(status: int, where: str):
@@ -400,6 +418,9 @@ def bl_linear_xent_backward_workspace_size(M: int, V: int, K: int, dw_dtype=torc
 def bl_linear_xent_forward(h, W, targets, loss, lse, workspace, stream=None):
     """X1: loss [M], lse [M] f32 of the softmax cross-entropy of h [M,K] . W [V,K]^T
     (bf16) at targets [M] int64; a target outside 0..V-1 leaves its token out."""
+    status = _quick().xent_forward(h, W, targets, loss, lse, workspace, stream)
+    if status is not None:
+        return _check(status, "bl_linear_xent_forward")
     M, K = h.shape
     V = W.shape[0]
     cur = _device(h, "h")
@@ -415,6 +436,9 @@ def bl_linear_xent_backward(h, W, targets, lse, dloss, dH=None, dW=None, workspa
                             stream=None):
     """X2: dH [M,K] bf16 and dW [V,K] (bf16|f32) of X1 (each may be None), given
     dloss [M] f32, the gradient of each token's loss, and X1's lse."""
+    status = _quick().xent_backward(h, W, targets, lse, dloss, dH, dW, workspace, accumulate_dW, stream)
+    if status is not None:
+        return _check(status, "bl_linear_xent_backward")
     M, K = h.shape
     V = W.shape[0]
     cur = _device(h, "h")
@@ -450,6 +474,9 @@ def _act8_specs(a, M, K, name):
 
 def bl_act8_encode(x, saved: Act8, stream=None):
     """A1: saved <- the 8-bit form of x [M,K] (bf16|f32)."""
+    status = _quick().act8_encode(x, saved.codes, saved.scales, stream)
+    if status is not None:
+        return _check(status, "bl_act8_encode")
     M, K = x.shape
     cur = _device(x, "x")
     dt = _dtype_code(x, "x")
@@ -459,6 +486,9 @@ def bl_act8_encode(x, saved: Act8, stream=None):
 
 def bl_act8_decode(saved: Act8, x, stream=None):
     """A2: x [M,K] (bf16|f32) <- the saved values."""
+    status = _quick().act8_decode(saved.codes, saved.scales, x, stream)
+    if status is not None:
+        return _check(status, "bl_act8_decode")
     M, K = x.shape
     cur = _device(x, "x")
     dt = _dtype_code(x, "x")
@@ -470,6 +500,10 @@ def bl_norm_forward(x, weight, bias, eps, y, mean, rstd, rms=False, saved8: Act8
     """N1: y [M,K] = layer norm (rms: RMS norm) of x [M,K] (bf16|f32) with weight,
     bias [K] (bf16|f32, each may be None); mean (None with rms), rstd [M] f32;
     saved8 receives the 8-bit form of x."""
+    codes, scales = (None, None) if saved8 is None else (saved8.codes, saved8.scales)
+    status = _quick().norm_forward(x, weight, bias, eps, y, mean, rstd, rms, codes, scales, stream)
+    if status is not None:
+        return _check(status, "bl_norm_forward")
     M, K = x.shape
     cur = _device(x, "x")
     dt = _dtype_code(x, "x")
@@ -490,12 +524,15 @@ def bl_norm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=Non
                      accumulate=False, stream=None):
     """N2: dx [M,K], dweight, dbias [K] (each may be None) of N1. x: the forward's
     input, or the Act8 that the forward saved."""
+    saved8, x = (x, None) if isinstance(x, Act8) else (None, x)
+    codes, scales = (None, None) if saved8 is None else (saved8.codes, saved8.scales)
+    status = _quick().norm_backward(dy, x, codes, scales, weight, mean, rstd, dx, dweight, dbias, workspace, rms,
+                                    accumulate, stream)
+    if status is not None:
+        return _check(status, "bl_norm_backward")
     M, K = dy.shape
     cur = _device(dy, "dy")
     dt = _dtype_code(dy, "dy")
-    saved8 = None
-    if isinstance(x, Act8):
-        saved8, x = x, None
     param = weight if weight is not None else dweight if dweight is not None else dbias
     pdt, ptype = (BL_F32, None) if param is None else (_dtype_code(param, "weight, dweight or dbias"), param.dtype)
     p = _pointers(cur, ((dy, dy.dtype, (M, K), "dy"), (x, dy.dtype, (M, K), "x"), *_act8_specs(saved8, M, K, "x"),
@@ -511,11 +548,15 @@ def bl_norm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=Non
 def bl_swiglu_forward(gate, up, y, gate8: Act8 | None = None, up8: Act8 | None = None, stream=None):
     """U1: y [M,K] = silu(gate) * up (bf16|f32); gate8, up8 (both or neither)
     receive the 8-bit forms of gate and up."""
+    if (gate8 is None) != (up8 is None):
+        raise ValueError("gate8 and up8 go together")
+    saved = (None,) * 4 if gate8 is None else (gate8.codes, gate8.scales, up8.codes, up8.scales)
+    status = _quick().swiglu_forward(gate, up, y, *saved, stream)
+    if status is not None:
+        return _check(status, "bl_swiglu_forward")
     M, K = gate.shape
     cur = _device(gate, "gate")
     dt = _dtype_code(gate, "gate")
-    if (gate8 is None) != (up8 is None):
-        raise ValueError("gate8 and up8 go together")
     p = _pointers(cur, ((gate, gate.dtype, (M, K), "gate"), (up, gate.dtype, (M, K), "up"), (y, gate.dtype, (M, K), "y"),
                         *_act8_specs(gate8, M, K, "gate8"), *_act8_specs(up8, M, K, "up8")))
     _check(load_library().bl_swiglu_forward(p[0], p[1], dt, M, K, *p[2:7], _stream_of(stream, cur)),
@@ -524,6 +565,9 @@ def bl_swiglu_forward(gate, up, y, gate8: Act8 | None = None, up8: Act8 | None =
 
 def bl_swiglu_backward(dy, gate8: Act8, up8: Act8, dgate, dup, stream=None):
     """U2: dgate, dup [M,K] of U1 from the 8-bit forms of gate and up."""
+    status = _quick().swiglu_backward(dy, gate8.codes, gate8.scales, up8.codes, up8.scales, dgate, dup, stream)
+    if status is not None:
+        return _check(status, "bl_swiglu_backward")
     M, K = dy.shape
     cur = _device(dy, "dy")
     dt = _dtype_code(dy, "dy")

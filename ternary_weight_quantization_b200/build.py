@@ -1,4 +1,6 @@
-"""Build libbitlinear.so (sm_100a) in-tree with nvcc.
+"""Build libbitlinear.so (sm_100a) in-tree with nvcc, and the binding's
+extension module _binding.so (csrc/binding.cpp, host code) with the host
+compiler against the installed torch.
 
 Usage: python -m ternary_weight_quantization_b200.build [--verbose]
 
@@ -16,12 +18,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbitlinear.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -46,7 +51,34 @@ def _newest_input_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def build_binding(force: bool = False) -> str:
+    """_binding.so: links libbitlinear.so (found beside it) and torch."""
+    inputs = (BINDING_SRC, os.path.join(ROOT, "include", "bitlinear.h"), os.path.abspath(__file__))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, inputs)):
+        return BINDING
+    import torch
+    from torch.utils import cpp_extension
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-I{p}" for p in cpp_extension.include_paths()], f"-I{sysconfig.get_paths()['include']}", f"-I{cuda}",
+           BINDING_SRC, "-o", BINDING + ".tmp", f"-L{PKG}", "-l:libbitlinear.so", f"-L{lib}", "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{r.stderr}")
+    os.replace(BINDING + ".tmp", BINDING)
+    return BINDING
+
+
 def build(verbose: bool = False, force: bool = False) -> str:
+    lib = build_library(verbose=verbose, force=force)
+    build_binding(force=force)
+    return lib
+
+
+def build_library(verbose: bool = False, force: bool = False) -> str:
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_input_mtime():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
