@@ -909,7 +909,8 @@ def run_signsgd(args, rank, world, local_rank):
 def run_lm(args, rank, world, local_rank):
     """Decoder-LM mode: the 4-layer LM of workloads/lm.py trained through the
     library (every projection a BitLinear call; the rest plain PyTorch in
-    fp64, the precision the LM oracle keeps it in) for
+    fp64, the precision the LM oracle keeps it in; with --lm-ops library the
+    norms, the gating and the head's loss are the library's too, in fp32) for
     its 50 steps on each rank (independent replicas). Reports tokens per
     second (batch x sequence per step over the mean device time of a step,
     the first step excluded) and the largest |loss - oracle loss| over the
@@ -920,7 +921,9 @@ def run_lm(args, rank, world, local_rank):
     dev = torch.device("cuda", local_rank)
     torch.cuda.set_device(dev)
     cfg = LM_CONFIG
-    losses, ms = train_lm(lm_init(cfg, seed=0), lm_batches(cfg, seed=0), cfg, dev, timing=True)
+    library = args.lm_ops == "library"
+    how = {"dtype": torch.float32, "library_ops": True, "saved8": True} if library else {}
+    losses, ms = train_lm(lm_init(cfg, seed=0), lm_batches(cfg, seed=0), cfg, dev, timing=True, **how)
     job_ms = job_time_ms(ms, world, dev)
     worst = None
     gold_path = os.path.join(ROOT, "tests", "golden", "lm_oracle_losses.json")
@@ -933,7 +936,8 @@ def run_lm(args, rank, world, local_rank):
     tokens = cfg.batch * cfg.seq
     return {"metric": "bitlinear_lm_train_tokens_per_s", "value": round(tokens * world / (job_ms * 1e-3), 1),
             "unit": "tokens/s", "n_gpus": world, "steps": cfg.steps, "warmup": 1, "ms_per_step": round(job_ms, 4),
-            "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "int8/bf16 BitLinear, fp64 rest",
+            "higher_is_better": True, "scaling": "weak", "vs_baseline": None,
+            "dtype": "int8/bf16 BitLinear, " + ("bf16 head, 8-bit saved activations, fp32 rest" if library else "fp64 rest"),
             "data": "synthetic",
             "config": {"workload": "4-layer decoder LM", "layers": cfg.layers, "d": cfg.d, "heads": cfg.heads,
                        "ffn": cfg.ffn, "vocab": cfg.vocab, "seq": cfg.seq, "batch": cfg.batch, "lr": cfg.lr},
@@ -995,6 +999,9 @@ def main():
                     help="layer-stack mode (prints its own line instead of the single-layer one)")
     ap.add_argument("--lm", action="store_true",
                     help="decoder-LM training mode (prints its own line)")
+    ap.add_argument("--lm-ops", choices=["torch", "library"], default="torch",
+                    help="the decoder LM's norms, gating and head loss: plain PyTorch in fp64, or the library's "
+                         "operators (fp32, activations kept in 8 bits)")
     ap.add_argument("--signsgd", action="store_true",
                     help="sign-gradient data-parallel step mode (prints its own line)")
     ap.add_argument("--few-tokens", default=None,

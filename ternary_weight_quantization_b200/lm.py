@@ -24,6 +24,15 @@ and its output gradient to bf16 (one rounding, straight from ``dtype``), the
 master to fp32; y and dX come back in bf16 and dW in fp32. The embedding is a
 one-hot product, so its gradient is a plain matrix product (the same sums on
 every run) rather than an atomic scatter.
+
+With ``library_ops`` (dtype fp32) the library also runs what lies between the
+projections: the norms (``bl_norm_forward`` / ``bl_norm_backward``, whose
+inputs are kept in 8 bits with ``saved8``), the SwiGLU gating
+(``bl_swiglu_forward`` / ``bl_swiglu_backward``: gate and up are kept in 8 bits
+for the backward, not in fp32) and the LM head with the cross-entropy
+(``bl_linear_xent_forward`` / ``bl_linear_xent_backward``: no logits). The head
+then takes the last norm's output and its weights in bf16, and a target outside
+the vocabulary leaves its token out of the mean.
 """
 
 from __future__ import annotations
@@ -34,7 +43,8 @@ import torch
 
 from . import bitlinear as b
 
-__all__ = ["BitLinearFunction", "to_bf16_rn", "lm_loss", "adamw_step", "train_lm"]
+__all__ = ["BitLinearFunction", "RMSNormFunction", "SwigluFunction", "HeadLossFunction", "to_bf16_rn", "lm_loss",
+           "adamw_step", "train_lm"]
 
 _BF16_MIN_NORMAL = 2.0 ** -126
 
@@ -96,12 +106,104 @@ class BitLinearFunction(torch.autograd.Function):
         return dX.to(ctx.out_dtype), dW.to(ctx.w_dtype)
 
 
+class RMSNormFunction(torch.autograd.Function):
+    """y [M, K] = RMS norm of x [M, K] with gain weight [K]; x is kept for the
+    backward as it is, or (saved8) in 8 bits."""
+
+    @staticmethod
+    def forward(ctx, x, weight, eps, saved8):
+        M, K = x.shape
+        x, weight = x.contiguous(), weight.contiguous()
+        y = torch.empty_like(x)
+        rstd = torch.empty(M, dtype=torch.float32, device=x.device)
+        keep = b.Act8.allocate(M, K, x.device) if saved8 else None
+        b.bl_norm_forward(x, weight, None, eps, y, None, rstd, rms=True, saved8=keep)
+        ctx.saved8 = saved8
+        ctx.save_for_backward(weight, rstd, *((keep.codes, keep.scales) if saved8 else (x,)))
+        return y
+
+    @staticmethod
+    def backward(ctx, gy):
+        weight, rstd, *kept = ctx.saved_tensors
+        x = b.Act8(*kept) if ctx.saved8 else kept[0]
+        gy = gy.contiguous()
+        dx, dweight = torch.empty_like(gy), torch.empty_like(weight)
+        ws = torch.empty(max(b.bl_norm_backward_workspace_size(*gy.shape), 16), dtype=torch.uint8, device=gy.device)
+        b.bl_norm_backward(gy, x, weight, None, rstd, dx, dweight, None, ws, rms=True)
+        return dx, dweight, None, None
+
+
+class SwigluFunction(torch.autograd.Function):
+    """y [M, K] = silu(gate) * up in bf16 (the type the BitLinear calls around
+    it give and take), returned in the dtype of gate; gate and up are kept for
+    the backward in 8 bits."""
+
+    @staticmethod
+    def forward(ctx, gate, up):
+        g, u = gate.to(torch.bfloat16).contiguous(), up.to(torch.bfloat16).contiguous()
+        y = torch.empty_like(g)
+        g8, u8 = b.Act8.allocate(*g.shape, g.device), b.Act8.allocate(*g.shape, g.device)
+        b.bl_swiglu_forward(g, u, y, g8, u8)
+        ctx.save_for_backward(g8.codes, g8.scales, u8.codes, u8.scales)
+        return y.to(gate.dtype)
+
+    @staticmethod
+    def backward(ctx, gy):
+        gc, gs, uc, us = ctx.saved_tensors
+        dy = gy.to(torch.bfloat16).contiguous()
+        dgate, dup = torch.empty_like(dy), torch.empty_like(dy)
+        b.bl_swiglu_backward(dy, b.Act8(gc, gs), b.Act8(uc, us), dgate, dup)
+        return dgate.to(gy.dtype), dup.to(gy.dtype)
+
+
+class HeadLossFunction(torch.autograd.Function):
+    """Mean cross-entropy of h [M, K] . head [V, K]^T at targets [M] over the
+    tokens whose target lies in the vocabulary (0 if there is none)."""
+
+    @staticmethod
+    def forward(ctx, h, head, targets):
+        (M, K), V = h.shape, head.shape[0]
+        hb, wb = h.to(torch.bfloat16).contiguous(), head.to(torch.bfloat16).contiguous()
+        targets = targets.contiguous()
+        buf = b.XentBuffers.allocate(M, V, K, backward=False, device=h.device)
+        b.bl_linear_xent_forward(hb, wb, targets, buf.loss, buf.lse, buf.workspace)
+        share = ((targets >= 0) & (targets < V)).sum().clamp(min=1).to(torch.float32).reciprocal()
+        ctx.save_for_backward(hb, wb, targets, buf.lse, share)
+        ctx.dtypes = h.dtype, head.dtype
+        return (buf.loss.sum() * share).to(h.dtype)
+
+    @staticmethod
+    def backward(ctx, g):
+        h, head, targets, lse, share = ctx.saved_tensors
+        (M, K), V = h.shape, head.shape[0]
+        dloss = (g.to(torch.float32) * share).expand(M).contiguous()
+        dH = torch.empty_like(h) if ctx.needs_input_grad[0] else None
+        dW = torch.empty((V, K), dtype=torch.float32, device=h.device) if ctx.needs_input_grad[1] else None
+        ws = torch.empty(max(b.bl_linear_xent_backward_workspace_size(M, V, K, torch.float32), 16), dtype=torch.uint8,
+                         device=h.device)
+        b.bl_linear_xent_backward(h, head, targets, lse, dloss, dH, dW, ws)
+        return (None if dH is None else dH.to(ctx.dtypes[0])), (None if dW is None else dW.to(ctx.dtypes[1])), None
+
+
 def _rmsnorm(x, g, eps):
     return x / torch.sqrt(torch.mean(x * x, dim=-1, keepdim=True) + eps) * g
 
 
-def lm_loss(params: dict, ids: torch.Tensor, cfg) -> torch.Tensor:
-    """Mean next-token cross-entropy of ids [B, S + 1] (parameters of one float dtype)."""
+def lm_loss(params: dict, ids: torch.Tensor, cfg, library_ops: bool = False, saved8: bool = False) -> torch.Tensor:
+    """Mean next-token cross-entropy of ids [B, S + 1] (parameters of one float
+    dtype; fp32 with library_ops: the norms, the gating and the head's loss by
+    the library, the norms' inputs kept in 8 bits with saved8)."""
+    if library_ops and params["embed"].dtype != torch.float32:
+        raise ValueError(f"library_ops takes fp32 parameters, got {params['embed'].dtype}")
+
+    def norm(x, g):
+        if library_ops:
+            return RMSNormFunction.apply(x.reshape(-1, d), g, cfg.norm_eps, saved8)
+        return _rmsnorm(x, g, cfg.norm_eps).reshape(-1, d)
+
+    def gated(gate, up):
+        return SwigluFunction.apply(gate, up) if library_ops else torch.nn.functional.silu(gate) * up
+
     B, S1 = ids.shape
     S, d, H = S1 - 1, cfg.d, cfg.heads
     dh = d // H
@@ -114,16 +216,18 @@ def lm_loss(params: dict, ids: torch.Tensor, cfg) -> torch.Tensor:
     for i in range(cfg.layers):
         def p(n):
             return params[f"layer{i}.{n}"]
-        a = _rmsnorm(h, p("attn_norm"), cfg.norm_eps).reshape(B * S, d)
+        a = norm(h, p("attn_norm"))
         q, k, v = (bl(a, p(n)).reshape(B, S, H, dh).transpose(1, 2) for n in ("q", "k", "v"))
         scores = (q @ k.transpose(-1, -2)) / math.sqrt(dh)
         scores = scores.masked_fill(~causal, float("-inf"))
         o = (torch.softmax(scores, dim=-1) @ v).transpose(1, 2).reshape(B * S, d)
         h = h + bl(o, p("o")).reshape(B, S, d)
-        m = _rmsnorm(h, p("mlp_norm"), cfg.norm_eps).reshape(B * S, d)
-        h = h + bl(torch.nn.functional.silu(bl(m, p("gate"))) * bl(m, p("up")), p("down")).reshape(B, S, d)
-    logits = _rmsnorm(h, params["final_norm"], cfg.norm_eps) @ params["head"].T
-    return torch.nn.functional.cross_entropy(logits.reshape(B * S, -1), y_ids.reshape(-1))
+        m = norm(h, p("mlp_norm"))
+        h = h + bl(gated(bl(m, p("gate")), bl(m, p("up"))), p("down")).reshape(B, S, d)
+    last = norm(h, params["final_norm"])
+    if library_ops:
+        return HeadLossFunction.apply(last, params["head"], y_ids.reshape(-1))
+    return torch.nn.functional.cross_entropy(last @ params["head"].T, y_ids.reshape(-1))
 
 
 def adamw_step(params: dict, grads: dict, state: dict, step: int, cfg):
@@ -142,10 +246,11 @@ def adamw_step(params: dict, grads: dict, state: dict, step: int, cfg):
 
 
 def train_lm(init: dict, batches: torch.Tensor, cfg, device, steps: int | None = None, timing: bool = False,
-             dtype=torch.float64):
+             dtype=torch.float64, library_ops: bool = False, saved8: bool = False):
     """Losses of `steps` AdamW steps from `init` on `batches` (token ids), with
     everything outside the BitLinear calls in ``dtype``; with ``timing``, also
-    the mean device time per step in ms (CUDA events, first step excluded)."""
+    the mean device time per step in ms (CUDA events, first step excluded).
+    library_ops, saved8: as lm_loss (with dtype fp32)."""
     params = {n: t.to(device=device, dtype=dtype).contiguous().requires_grad_(True) for n, t in init.items()}
     ids_all = batches.to(device)
     state: dict = {}
@@ -154,7 +259,7 @@ def train_lm(init: dict, batches: torch.Tensor, cfg, device, steps: int | None =
         if timing:
             s, e = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
             s.record()
-        loss = lm_loss(params, ids_all[t], cfg)
+        loss = lm_loss(params, ids_all[t], cfg, library_ops, saved8)
         grads = torch.autograd.grad(loss, list(params.values()))
         adamw_step(params, dict(zip(params.keys(), grads)), state, t + 1, cfg)
         if timing:
