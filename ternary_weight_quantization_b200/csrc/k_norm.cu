@@ -212,13 +212,6 @@ __global__ void __launch_bounds__(kFwdThreads, kVecs <= 2 ? 4 : kVecs == 4 ? 2 :
     if (threadIdx.x < 4) reinterpret_cast<float4*>(sums)[threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
     __syncthreads();
   }
-  f32x2 w[kVecs][4];
-#pragma unroll
-  for (int j = 0; j < kVecs; ++j) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[j][i] = both2(1.0f);
-    if (p.weight && live(j)) load_params8(p.weight, p.p_f32, c0 + j * cs, w[j]);
-  }
   const int64_t first = kWarp ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
   const int64_t step = kWarp ? static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5) : gridDim.x, step_k = step * K;
   int rows = first < p.M ? static_cast<int>((p.M - 1 - first) / step) + 1 : 0, left = rows;
@@ -237,6 +230,13 @@ __global__ void __launch_bounds__(kFwdThreads, kVecs <= 2 ? 4 : kVecs == 4 ? 2 :
   };
 #pragma unroll
   for (int s = 0; s < kDepth; ++s) issue(mine + s * row_stride);
+  f32x2 w[kVecs][4];
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[j][i] = both2(1.0f);
+    if (p.weight && live(j)) load_params8(p.weight, p.p_f32, c0 + j * cs, w[j]);
+  }
   for (uint32_t slot = mine; rows > 0; --rows, row += step, at += step_k) {
     copy_async_wait<kDepth - 1>();
     Raw8<T> raw[kVecs];
@@ -635,16 +635,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_backward_kernel(const Nor
   const uint32_t mine = smem_u32(ring) + threadIdx.x * 16, end = mine + kDepth * row_stride;
   uint32_t buf = smem_u32(sums[0] + grp * (tpr >> 5) * 2);
   const uint32_t bufs = buf ^ (buf + static_cast<uint32_t>(sizeof(sums[0])));
-  f32x2 w[kBwdVecs][4], dw[kBwdVecs][4], db[kBwdVecs][4];
-#pragma unroll
-  for (int j = 0; j < kBwdVecs; ++j) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w[j][i] = both2(1.0f);
-      dw[j][i] = db[j][i] = 0;
-    }
-    if (p.weight && live(j)) load_params8(p.weight, p.p_f32, c0 + j * cs, w[j]);
-  }
   const int64_t first = static_cast<int64_t>(blockIdx.x) * ngrp + grp;
   const int64_t step = static_cast<int64_t>(gridDim.x) * ngrp, step_k = step * K;
   int rows = first < p.M ? static_cast<int>((p.M - 1 - first) / step) + 1 : 0, left = rows;
@@ -671,6 +661,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_backward_kernel(const Nor
   if (rows > 0) {
     mean = __ldg(mean_at);
     rstd = __ldg(rstd_at);
+  }
+  f32x2 w[kBwdVecs][4], dw[kBwdVecs][4], db[kBwdVecs][4];
+#pragma unroll
+  for (int j = 0; j < kBwdVecs; ++j) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[j][i] = both2(1.0f);
+      dw[j][i] = db[j][i] = 0;
+    }
+    if (p.weight && live(j)) load_params8(p.weight, p.p_f32, c0 + j * cs, w[j]);
   }
   for (uint32_t slot = mine; rows > 0; --rows) {
     const f32x2 nmean2 = both2(p.rms ? 0.0f : -mean), rstd2 = both2(rstd);
@@ -835,36 +835,46 @@ __global__ void __launch_bounds__(256) norm_strip_kernel(const NormBwdArgs p) {
 }
 
 // dweight, dbias from the blocks' partial rows: 32 columns per block, the
-// partial rows spread over 16 threads of each column.
-__global__ void __launch_bounds__(512) norm_join_kernel(const float* __restrict__ parts, int nparts, int K,
-                                                        void* dweight, void* dbias, int p_f32, int accumulate) {
+// partial rows (at most 148) spread over 32 threads of each column, whose
+// loads are all in flight at once.
+constexpr int kMaxParts = 148;
+
+__global__ void __launch_bounds__(1024) norm_join_kernel(const float* __restrict__ parts, int nparts, int K,
+                                                         void* dweight, void* dbias, int p_f32, int accumulate) {
   pdl_wait_primary();
   pdl_launch_dependents();
-  __shared__ float sh[2][16][33];
-  const int x = threadIdx.x & 31, yy = threadIdx.x >> 5;
+  __shared__ float sh[2][32][33];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int c = static_cast<int>(blockIdx.x) * 32 + x;
-  float a = 0.0f, b = 0.0f;
-  if (c < K) {
-#pragma unroll 4
-    for (int r = yy; r < nparts; r += 16) {
-      a += parts[static_cast<int64_t>(r) * 2 * K + c];
-      b += parts[static_cast<int64_t>(r) * 2 * K + K + c];
+  constexpr int kU = (kMaxParts + 31) / 32;
+  float a[kU], b[kU];
+#pragma unroll
+  for (int i = 0; i < kU; ++i) {
+    const int r = y + 32 * i;
+    a[i] = b[i] = 0.0f;
+    if (c < K && r < nparts) {
+      if (dweight) a[i] = parts[static_cast<int64_t>(r) * 2 * K + c];
+      if (dbias) b[i] = parts[static_cast<int64_t>(r) * 2 * K + K + c];
     }
   }
-  sh[0][yy][x] = a;
-  sh[1][yy][x] = b;
-  __syncthreads();
-  if (yy < 2 && c < K) {
-    void* out = yy == 0 ? dweight : dbias;
-    if (!out) return;
-    float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s += sh[yy][i][x];
+  for (int i = 1; i < kU; ++i) a[0] += a[i], b[0] += b[i];
+  sh[0][y][x] = a[0];
+  sh[1][y][x] = b[0];
+  __syncthreads();
+  // warp y adds column y of either sum
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    void* out = which == 0 ? dweight : dbias;
+    const int col = static_cast<int>(blockIdx.x) * 32 + y;
+    if (!out || col >= K) continue;
+    const float s = warp_sum(sh[which][x][y]);
+    if (x != 0) continue;
     if (p_f32) {
-      float* o = static_cast<float*>(out) + c;
+      float* o = static_cast<float*>(out) + col;
       *o = accumulate ? s + *o : s;
     } else {
-      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out) + c;
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out) + col;
       *o = __float2bfloat16_rn(accumulate ? s + __bfloat162float(*o) : s);
     }
   }
@@ -873,7 +883,6 @@ __global__ void __launch_bounds__(512) norm_join_kernel(const float* __restrict_
 // ---------------------------------------------------------------- host side
 constexpr int kFwdMaxK = 16384;  // 256 threads x 8 vectors of 8
 constexpr int kBwdMaxK = 8192;   // 512 threads x 16 columns (scalar: 1024 x 8)
-constexpr int kMaxParts = 148;   // partial rows of dweight and dbias
 
 int round32(int n) { return (n + 31) / 32 * 32; }
 
@@ -1052,7 +1061,7 @@ cudaError_t launch_norm_backward(const void* dy, const void* x, const int8_t* co
     e = f32 ? go(float{}) : go(__nv_bfloat16{});
   }
   if (e != cudaSuccess || !sums) return e;
-  return launch_pdl(norm_join_kernel, dim3(static_cast<unsigned>((K + 31) / 32)), dim3(512), 0, s,
+  return launch_pdl(norm_join_kernel, dim3(static_cast<unsigned>((K + 31) / 32)), dim3(1024), 0, s,
                     static_cast<const float*>(workspace), nparts, static_cast<int>(K), dweight, dbias, p_f32, accumulate);
 }
 
