@@ -270,6 +270,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
   const bool leader = rank == 0;
   const int pair = static_cast<int>(blockIdx.x >> 1), npairs = static_cast<int>(gridDim.x >> 1);
 
+  if (threadIdx.x == 32 * kWarpEpi0) {
+    // the descriptors' fetch overlaps the set-up
+    prefetch_tensormap(&map_h);
+    prefetch_tensormap(&map_w);
+    if constexpr (P == Phase::Grad) prefetch_tensormap(&map_dz);
+    if (P == Phase::Grad && p.split) prefetch_tensormap(&map_dz_lo);
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -525,16 +532,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
       tc_fence_after();
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kTile;
       uint32_t box = 0, box_lo = 0;
-#pragma unroll 1
-      for (int c = part * G::kChunks; c < (part + 1) * G::kChunks; ++c) {
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(tbase + 32 * c, r);
-        tmem_ld_wait();
-        if (c == (part + 1) * G::kChunks - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(lead(&tmem_empty[buf]));
-        }
+      // one chunk of 32 columns in registers; the next one's TMEM load is
+      // under way meanwhile
+      auto chunk = [&](uint32_t (&r)[32], int c) {
         const int col = t.b0 + 32 * c;  // first column: of the piece (Lse, Dz) or of K (Grad)
         if constexpr (P == Phase::Lse) {
           if (static_cast<unsigned>(tgt - 32 * c) < 32u) {
@@ -545,7 +545,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
           }
           if (p.v0 + col < p.V) ls.chunk(r, p.V - (p.v0 + col));
         } else if constexpr (P == Phase::Dz) {
-          if (col >= p.vcount) continue;
+          if (col >= p.vcount) return;
           const bool here = static_cast<unsigned>(tgt - 32 * c) < 32u;
           float d[32];
 #pragma unroll
@@ -582,7 +582,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
             if (last) st.store(&out1, box_lo, col & ~63, row0, false, row0 < p.M);
           }
         } else {
-          if (col >= p.K) continue;
+          if (col >= p.K) return;
 #pragma unroll
           for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * scale);
           const bool live = row0 < (t.cls == 0 ? p.M : p.vcount);
@@ -625,6 +625,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
             }
           }
         }
+      };
+      constexpr int kLast = G::kChunks - 1;
+      const int first = part * G::kChunks;
+      uint32_t ra[32], rb[32];
+      tmem_ld_32x32b_x32(tbase + 32 * first, ra);
+      tmem_ld_wait();
+#pragma unroll 1
+      for (int c = 0; c < kLast; c += 2) {
+        tmem_ld_32x32b_x32(tbase + 32 * (first + c + 1), rb);
+        chunk(ra, first + c);
+        tmem_ld_wait();
+        if (c + 1 < kLast) {
+          tmem_ld_32x32b_x32(tbase + 32 * (first + c + 2), ra);
+        } else {
+          // every load of this buffer has landed: hand it back
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(lead(&tmem_empty[buf]));
+        }
+        chunk(rb, first + c + 1);
+        tmem_ld_wait();
       }
       if constexpr (P == Phase::Lse) {
         if (row < p.M) p.part[static_cast<int64_t>(t.b0 / 128 + part) * p.M + row] = make_float2(ls.m, ls.s);
