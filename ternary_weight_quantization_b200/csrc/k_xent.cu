@@ -37,6 +37,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "bl_act8.cuh"
 #include "bl_device.cuh"
@@ -48,7 +49,7 @@ namespace {
 enum class Phase { Lse, Dz, Grad };
 
 constexpr int kWarpLoad = 0, kWarpMma = 1, kWarpEpi0 = 4;
-constexpr int kTile = 256;              // rows and columns of a pair tile
+constexpr int kTile = 256;              // rows (and, where BN says nothing else, columns) of a pair tile
 constexpr int kBlockR = 64;             // reduction per stage
 constexpr int kBox = 8192;              // one 64 x 64 bf16 box
 constexpr int kStageBytes = 4 * kBox;   // A and B: two boxes each
@@ -62,7 +63,6 @@ struct Geo {
   static constexpr int kEpiWarps = P == Phase::Grad ? 4 : 8;
   static constexpr int kSlots = P == Phase::Lse ? 0 : 2;
   static constexpr int kParts = kEpiWarps / 4;        // warps that share a TMEM lane quadrant
-  static constexpr int kChunks = 8 / kParts;          // 32-column chunks of each
   static constexpr int kThreads = 32 * (kWarpEpi0 + kEpiWarps);
   static constexpr int kOffEpi = kStages * kStageBytes;
   static constexpr int kOffBar = kOffEpi + kEpiWarps * kSlots * kEpiBox;
@@ -134,13 +134,13 @@ __device__ __forceinline__ bool next_tile(const XentParams& p, int pair, int npa
   return true;
 }
 
-template <Phase P>
+template <Phase P, int BN>
 __device__ __forceinline__ Tile decode(const XentParams& p, int u) {
   Tile t{};
   if constexpr (P != Phase::Grad) {
     // tokens fastest: the pairs at work share few tiles of W, and h stays in L2
     t.a0 = (u % p.tiles_m) * kTile;
-    t.b0 = (u / p.tiles_m) * kTile;
+    t.b0 = (u / p.tiles_m) * BN;
     t.nkb = (p.K + kBlockR - 1) / kBlockR;
     return t;
   }
@@ -168,15 +168,20 @@ __device__ __forceinline__ Tile decode(const XentParams& p, int u) {
 
 // Instruction descriptors and descriptor steps (16-byte units per 16 of the
 // reduction): K-major 32 bytes along the row, MN-major 16 rows.
-__host__ __device__ constexpr uint32_t idesc(int a_mn, int b_mn) { return make_idesc(1 /*f32*/, 1 /*bf16*/, a_mn, b_mn, kTile, kTile); }
+__host__ __device__ constexpr uint32_t idesc(int a_mn, int b_mn, int bn) {
+  return make_idesc(1 /*f32*/, 1 /*bf16*/, a_mn, b_mn, kTile, bn);
+}
 
-__device__ __forceinline__ void mma_stage(uint32_t d_tmem, uint32_t sa, uint32_t sb, bool a_mn, bool b_mn, uint32_t id,
-                                          int kb) {
-  const uint64_t ad = smem_desc_sw128(sa, a_mn ? kBox : 16, 1024);
-  const uint64_t bd = smem_desc_sw128(sb, b_mn ? kBox : 16, 1024);
-  const uint64_t as = a_mn ? 128 : 2, bs = b_mn ? 128 : 2;
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, bool mn) {
+  return smem_desc_sw128(saddr, mn ? kBox : 16, 1024);
+}
+
+template <bool kAMn, bool kBMn, int BN>
+__device__ __forceinline__ void mma_stage(uint32_t d_tmem, uint64_t ad, uint64_t bd, int kb) {
+  constexpr uint64_t as = kAMn ? 128 : 2, bs = kBMn ? 128 : 2;
 #pragma unroll
-  for (int kk = 0; kk < 4; ++kk) mma_f16_pair(d_tmem, ad + kk * as, bd + kk * bs, id, (kb | kk) != 0);
+  for (int kk = 0; kk < 4; ++kk)
+    mma_f16_pair(d_tmem, ad + kk * as, bd + kk * bs, idesc(kAMn, kBMn, BN), (kb | kk) != 0);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -209,11 +214,11 @@ struct Stager {
     __syncwarp();
     return base + (seq++ % kSlots) * kEpiBox;
   }
-  // `live`: the box has rows inside the tensor.
-  __device__ __forceinline__ void store(const CUtensorMap* map, uint32_t box, int x, int y, bool add, bool live) {
+  // (The box's first row lies inside the tensor: see `any`.)
+  __device__ __forceinline__ void store(const CUtensorMap* map, uint32_t box, int x, int y, bool add) {
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0 && live) {
+    if (lane == 0) {
       if (add) tma_add_2d(map, box, x, y);
       else tma_store_2d(map, box, x, y);
       bulk_commit_group();
@@ -246,13 +251,25 @@ struct LseState {
   }
 };
 
-template <Phase P>
+// Boxes of 64 rows, of the `most` that a CTA's share of an operand has, that
+// hold rows below `limit`. In the logit phases the others are not loaded: rows
+// of A and of B reach only their own rows and columns of D, which are not used
+// there. (In Grad the tests cost more than they save: 4096 tokens, K 2560,
+// vocabulary 32000: 2.34 ms with them, 2.26 without.)
+__device__ __forceinline__ int boxes(int limit, int row, int most) {
+  const int n = (limit - row + 63) >> 6;
+  return n < 0 ? 0 : n < most ? n : most;
+}
+
+template <Phase P, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
     xent_kernel(const __grid_constant__ CUtensorMap map_h, const __grid_constant__ CUtensorMap map_w,
                 const __grid_constant__ CUtensorMap map_dz, const __grid_constant__ CUtensorMap map_dz_lo,
                 const __grid_constant__ CUtensorMap out0, const __grid_constant__ CUtensorMap out1,
                 const __grid_constant__ XentParams p) {
   using G = Geo<P>;
+  static_assert(BN == 256 || (BN == 128 && P != Phase::Grad), "tile widths");
+  constexpr int kChunks = BN / 32 / G::kParts;  // 32-column chunks of an epilogue warp
   constexpr int kStages = G::kStages, kEpiWarps = G::kEpiWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -316,46 +333,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
       bool ok = true;
       int u;
       for (int i = 0; ok && next_tile(p, pair, npairs, i, u); ++i) {
-        const Tile t = decode<P>(p, u);
-        const int a0 = t.a0 + static_cast<int>(rank) * 128, b0 = t.b0 + static_cast<int>(rank) * 128;
-        const int half = t.nkb >> 1;
-        for (int kb = 0; kb < t.nkb; ++kb) {
-          if (!wait(&empty[stage], phase ^ 1)) {
-            ok = false;
-            break;
+        const Tile t = decode<P, BN>(p, u);
+        const int a0 = t.a0 + static_cast<int>(rank) * 128, b0 = t.b0 + static_cast<int>(rank) * (BN / 2);
+        // both CTAs' boxes arrive on the leader's barrier
+        uint32_t bytes = 2 * kStageBytes;
+        int na = 2, nb = 2;
+        if constexpr (P != Phase::Grad) {
+          na = boxes(p.M, a0, 2);
+          nb = boxes(p.vcount, b0, BN / 128);
+          bytes = kBox * (boxes(p.M, t.a0, 2) + boxes(p.M, t.a0 + 128, 2) + boxes(p.vcount, t.b0, BN / 128) +
+                          boxes(p.vcount, t.b0 + BN / 2, BN / 128));
+        }
+        // one loop per kind of tile: a stage must be requested in the few hundred
+        // cycles that the tensor cores take for one
+        auto each = [&](int n, auto load) {
+          for (int kb = 0; kb < n; ++kb) {
+            if (!wait(&empty[stage], phase ^ 1)) {
+              ok = false;
+              return;
+            }
+            issued_parity[stage] = static_cast<int>(phase);
+            if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
+            load(kb, lead(&full[stage]), smem + stage * kStageBytes);
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1;
+            }
           }
-          issued_parity[stage] = static_cast<int>(phase);
-          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
-          const uint32_t bar = lead(&full[stage]);
-          uint8_t* sa = smem + stage * kStageBytes;
-          uint8_t* sb = sa + 2 * kBox;
-          if constexpr (P != Phase::Grad) {
+        };
+        // K-major: (reduction, row); MN-major: (row, reduction)
+        if constexpr (P != Phase::Grad) {
+          const int w0 = p.v0 + b0;
+          each(t.nkb, [&](int kb, uint32_t bar, uint8_t* sa) {
             const int k0 = kb * kBlockR;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              tma_load_2d_pair(&map_h, bar, sa + j * kBox, k0, a0 + 64 * j);
-              tma_load_2d_pair(&map_w, bar, sb + j * kBox, k0, p.v0 + b0 + 64 * j);
-            }
-          } else if (t.cls == 0) {
-            const int v = (t.kb0 + kb) * kBlockR;
+            for (int j = 0; j < 2; ++j)
+              if (j < na) tma_load_2d_pair(&map_h, bar, sa + j * kBox, k0, a0 + 64 * j);
+#pragma unroll
+            for (int j = 0; j < BN / 128; ++j)
+              if (j < nb) tma_load_2d_pair(&map_w, bar, sa + (2 + j) * kBox, k0, w0 + 64 * j);
+          });
+        } else if (t.cls == 0) {
+          const int v0 = t.kb0 * kBlockR;
+          each(t.nkb, [&](int kb, uint32_t bar, uint8_t* sa) {
+            const int v = v0 + kb * kBlockR;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               tma_load_2d_pair(&map_dz, bar, sa + j * kBox, v, a0 + 64 * j);
-              tma_load_2d_pair(&map_w, bar, sb + j * kBox, b0 + 64 * j, p.v0 + v);
+              tma_load_2d_pair(&map_w, bar, sa + (2 + j) * kBox, b0 + 64 * j, p.v0 + v);
             }
-          } else {
-            const bool lo = p.split && kb < half;
-            const int m = p.t0 + (p.split && !lo ? kb - half : kb) * kBlockR;
-            const CUtensorMap* md = lo ? &map_dz_lo : &map_dz;
+          });
+        } else {
+          auto of = [&](const CUtensorMap* dz) {
+            return [&, dz](int kb, uint32_t bar, uint8_t* sa) {
+              const int m = p.t0 + kb * kBlockR;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              tma_load_2d_pair(md, bar, sa + j * kBox, a0 + 64 * j, m);
-              tma_load_2d_pair(&map_h, bar, sb + j * kBox, b0 + 64 * j, m);
-            }
-          }
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1;
+              for (int j = 0; j < 2; ++j) {
+                tma_load_2d_pair(dz, bar, sa + j * kBox, a0 + 64 * j, m);
+                tma_load_2d_pair(&map_h, bar, sa + (2 + j) * kBox, b0 + 64 * j, m);
+              }
+            };
+          };
+          if (p.split) {
+            each(t.nkb >> 1, of(&map_dz_lo));
+            if (ok) each(t.nkb >> 1, of(&map_dz));
+          } else {
+            each(t.nkb, of(&map_dz));
           }
         }
       }
@@ -375,28 +418,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
       bool ok = true;
       int u;
       for (int i = 0; ok && next_tile(p, pair, npairs, i, u); ++i) {
-        const Tile t = decode<P>(p, u);
+        const Tile t = decode<P, BN>(p, u);
         if (t.nkb == 0) continue;
         if (!wait(&tmem_empty[buf], buf_phase ^ 1)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * kTile);
-        for (int kb = 0; kb < t.nkb; ++kb) {
-          if (!wait(&full[stage], phase)) {
-            ok = false;
-            break;
+        auto each = [&](auto a_mn, auto b_mn) {
+          constexpr bool kAMn = decltype(a_mn)::value, kBMn = decltype(b_mn)::value;
+          const uint64_t ad0 = operand_desc(s0, kAMn), bd0 = operand_desc(s0 + 2 * kBox, kBMn);
+          for (int kb = 0; kb < t.nkb; ++kb) {
+            if (!wait(&full[stage], phase)) {
+              ok = false;
+              return;
+            }
+            tc_fence_after();
+            const uint64_t at = static_cast<uint64_t>(stage) * (kStageBytes >> 4);
+            mma_stage<kAMn, kBMn, BN>(d_tmem, ad0 + at, bd0 + at, kb);
+            mma_commit_pair(&empty[stage], 0x3);
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1;
+            }
           }
-          tc_fence_after();
-          const uint32_t sa = s0 + stage * kStageBytes, sb = sa + 2 * kBox;
-          if constexpr (P != Phase::Grad) mma_stage(d_tmem, sa, sb, false, false, idesc(0, 0), kb);
-          else if (t.cls == 0) mma_stage(d_tmem, sa, sb, false, true, idesc(0, 1), kb);
-          else mma_stage(d_tmem, sa, sb, true, true, idesc(1, 1), kb);
-          mma_commit_pair(&empty[stage], 0x3);
-          if (kb == t.nkb - 1) mma_commit_pair(&tmem_full[buf], 0x3);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1;
-          }
-        }
+          mma_commit_pair(&tmem_full[buf], 0x3);
+        };
+        using K = std::false_type;
+        using MN = std::true_type;
+        if constexpr (P != Phase::Grad) each(K{}, K{});
+        else if (t.cls == 0) each(K{}, MN{});
+        else each(MN{}, MN{});
         if (++buf == 2) {
           buf = 0;
           buf_phase ^= 1;
@@ -506,7 +556,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
     uint32_t buf_phase = 0;
     int u;
     for (int i = 0; next_tile(p, pair, npairs, i, u); ++i) {
-      const Tile t = decode<P>(p, u);
+      const Tile t = decode<P, BN>(p, u);
       if (t.nkb == 0) continue;
       const int row0 = t.a0 + static_cast<int>(rank) * 128 + q * 32;  // first D row of the warp
       const int row = row0 + lane;
@@ -531,6 +581,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
       if (!wait(&tmem_full[buf], buf_phase)) break;
       tc_fence_after();
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kTile;
+      const bool any = row0 < (P == Phase::Grad && t.cls == 1 ? p.vcount : p.M);  // rows of the warp that are used
       uint32_t box = 0, box_lo = 0;
       // one chunk of 32 columns in registers; the next one's TMEM load is
       // under way meanwhile
@@ -569,7 +620,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
             st_shared_v4(box_chunk(box, lane, (c & 1) * 4 + j), hi[4 * j] & keep, hi[4 * j + 1] & keep,
                          hi[4 * j + 2] & keep, hi[4 * j + 3] & keep);
           const bool last = (c & 1) || col + 32 >= p.vcount;
-          if (last) st.store(&out0, box, col & ~63, row0, false, row0 < p.M);
+          if (last) st.store(&out0, box, col & ~63, row0, false);
           if (p.split) {
             if ((c & 1) == 0) box_lo = st.template next<1>();
 #pragma unroll
@@ -579,20 +630,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
             for (int j = 0; j < 4; ++j)
               st_shared_v4(box_chunk(box_lo, lane, (c & 1) * 4 + j), hi[4 * j] & keep, hi[4 * j + 1] & keep,
                            hi[4 * j + 2] & keep, hi[4 * j + 3] & keep);
-            if (last) st.store(&out1, box_lo, col & ~63, row0, false, row0 < p.M);
+            if (last) st.store(&out1, box_lo, col & ~63, row0, false);
           }
         } else {
           if (col >= p.K) return;
 #pragma unroll
           for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * scale);
-          const bool live = row0 < (t.cls == 0 ? p.M : p.vcount);
           const bool f32 = t.cls == 0 ? p.h_f32 != 0 : p.w_f32 != 0;
           if (f32) {
             box = st.next();
 #pragma unroll
             for (int j = 0; j < 8; ++j) st_shared_v4(box_chunk(box, lane, j), r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-            if (t.cls == 0) st.store(&out0, box, col, t.slice * p.rows_pad + row0, p.h_add != 0, live);
-            else st.store(&out1, box, col, p.v0 + row0, p.w_add != 0, live);
+            if (t.cls == 0) st.store(&out0, box, col, t.slice * p.rows_pad + row0, p.h_add != 0);
+            else st.store(&out1, box, col, p.v0 + row0, p.w_add != 0);
           } else {
             if (t.cls == 1 && p.w_add && row < p.vcount) {
               // one rounding: the bf16 contents are added to the fp32 sum
@@ -620,35 +670,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
                            pack_bf16x2(__uint_as_float(r[8 * j + 5]), __uint_as_float(r[8 * j + 4])),
                            pack_bf16x2(__uint_as_float(r[8 * j + 7]), __uint_as_float(r[8 * j + 6])));
             if ((c & 1) || col + 32 >= p.K) {
-              if (t.cls == 0) st.store(&out0, box, col & ~63, row0, false, live);
-              else st.store(&out1, box, col & ~63, p.v0 + row0, false, live);
+              if (t.cls == 0) st.store(&out0, box, col & ~63, row0, false);
+              else st.store(&out1, box, col & ~63, p.v0 + row0, false);
             }
           }
         }
       };
-      constexpr int kLast = G::kChunks - 1;
-      const int first = part * G::kChunks;
-      uint32_t ra[32], rb[32];
-      tmem_ld_32x32b_x32(tbase + 32 * first, ra);
-      tmem_ld_wait();
+      constexpr int kLast = kChunks - 1;
+      const int first = part * kChunks;
+      auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(lead(&tmem_empty[buf]));
+      };
+      if (any) {
+        uint32_t ra[32], rb[32];
+        tmem_ld_32x32b_x32(tbase + 32 * first, ra);
+        tmem_ld_wait();
 #pragma unroll 1
-      for (int c = 0; c < kLast; c += 2) {
-        tmem_ld_32x32b_x32(tbase + 32 * (first + c + 1), rb);
-        chunk(ra, first + c);
-        tmem_ld_wait();
-        if (c + 1 < kLast) {
-          tmem_ld_32x32b_x32(tbase + 32 * (first + c + 2), ra);
-        } else {
-          // every load of this buffer has landed: hand it back
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(lead(&tmem_empty[buf]));
+        for (int c = 0; c < kLast; c += 2) {
+          tmem_ld_32x32b_x32(tbase + 32 * (first + c + 1), rb);
+          chunk(ra, first + c);
+          tmem_ld_wait();
+          if (c + 1 < kLast) tmem_ld_32x32b_x32(tbase + 32 * (first + c + 2), ra);
+          else release();  // every load of this buffer has landed
+          chunk(rb, first + c + 1);
+          tmem_ld_wait();
         }
-        chunk(rb, first + c + 1);
-        tmem_ld_wait();
+      } else {
+        release();
       }
       if constexpr (P == Phase::Lse) {
-        if (row < p.M) p.part[static_cast<int64_t>(t.b0 / 128 + part) * p.M + row] = make_float2(ls.m, ls.s);
+        if (row < p.M) p.part[static_cast<int64_t>(t.b0 / (BN / 2) + part) * p.M + row] = make_float2(ls.m, ls.s);
       }
       if (++buf == 2) {
         buf = 0;
@@ -766,14 +819,14 @@ void share_tiles(XentParams& p, int npairs) {
   p.more = static_cast<int>(more);
 }
 
-template <Phase P>
+template <Phase P, int BN>
 cudaError_t launch_phase(const CUtensorMap (&maps)[6], XentParams& p, cudaStream_t s) {
   static int pairs_of[64] = {};  // pairs resident at once, by device
   int dev = 0;
   cudaGetDevice(&dev);
   int pairs = dev >= 0 && dev < 64 ? pairs_of[dev] : 0;
   if (!pairs) {
-    if (cudaError_t e = cudaFuncSetAttribute(xent_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<P>::kSmemBytes);
+    if (cudaError_t e = cudaFuncSetAttribute(xent_kernel<P, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<P>::kSmemBytes);
         e != cudaSuccess)
       return e;
     pairs = device_sm_count() / 2;
@@ -782,7 +835,7 @@ cudaError_t launch_phase(const CUtensorMap (&maps)[6], XentParams& p, cudaStream
     cfg.blockDim = dim3(Geo<P>::kThreads);
     cfg.dynamicSmemBytes = Geo<P>::kSmemBytes;
     int clusters = 0;
-    if (cudaOccupancyMaxActiveClusters(&clusters, xent_kernel<P>, &cfg) == cudaSuccess && clusters > 0 && clusters < pairs)
+    if (cudaOccupancyMaxActiveClusters(&clusters, xent_kernel<P, BN>, &cfg) == cudaSuccess && clusters > 0 && clusters < pairs)
       pairs = clusters;
     cudaGetLastError();
     if (dev >= 0 && dev < 64) pairs_of[dev] = pairs;
@@ -791,7 +844,7 @@ cudaError_t launch_phase(const CUtensorMap (&maps)[6], XentParams& p, cudaStream
   if (ntiles == 0) return cudaSuccess;
   const int n = ntiles < pairs ? ntiles : pairs;
   share_tiles(p, n);
-  return launch_pdl(xent_kernel<P>, dim3(2 * n), dim3(Geo<P>::kThreads), Geo<P>::kSmemBytes, s, maps[0], maps[1],
+  return launch_pdl(xent_kernel<P, BN>, dim3(2 * n), dim3(Geo<P>::kThreads), Geo<P>::kSmemBytes, s, maps[0], maps[1],
                     maps[2], maps[3], maps[4], maps[5], p);
 }
 
@@ -844,8 +897,22 @@ Plan make_plan(int64_t M, int64_t V, int64_t K, bool f32) {
 
 }  // namespace
 
+// Columns of a tile of logits: 128 where such tiles still find a pair each, so
+// that twice the SMs share the weights' loads and the epilogue (64 tokens, K
+// 512, vocabulary 8192: forward KERNEL128 us, with 256 columns KERNEL256 us);
+// else 256, which loads a third fewer bytes per product.
+static int logit_columns(int64_t M, int64_t vocab) {
+  return static_cast<int64_t>(tiles_of(M)) * ((vocab + 127) / 128) <= 74 ? 128 : 256;
+}
+
+// (maximum, sum) pairs per token: two per tile.
+static int logit_parts(int64_t M, int64_t V) {
+  const int bn = logit_columns(M, V);
+  return 2 * static_cast<int>((V + bn - 1) / bn);
+}
+
 size_t xent_forward_workspace_bytes(int64_t M, int64_t V, int64_t K) {
-  return align256(static_cast<size_t>(tiles_of(V)) * M * 16) + align256(static_cast<size_t>(M) * 8);
+  return align256(static_cast<size_t>(logit_parts(M, V)) * M * 8) + align256(static_cast<size_t>(M) * 8);
 }
 
 size_t xent_backward_workspace_bytes(int64_t M, int64_t V, int64_t K, int dw_is_f32) {
@@ -867,16 +934,17 @@ cudaError_t launch_xent_forward(const void* h, const void* W, const int64_t* tar
   p.err = err;
   p.tiles_m = tiles_of(M);
   p.tiles_k = tiles_of(K);
-  const int tiles_v = tiles_of(V);
-  p.ntiles_a = p.tiles_m * tiles_v;
+  const int bn = logit_columns(M, V), parts = logit_parts(M, V);
+  p.ntiles_a = p.tiles_m * parts / 2;
   p.h = static_cast<const uint4*>(h);
   p.W = static_cast<const uint4*>(W);
   p.part = static_cast<float2*>(workspace);
-  p.tlogit = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + align256(static_cast<size_t>(tiles_v) * M * 16));
-  if (cudaError_t e = launch_phase<Phase::Lse>(maps, p, s); e != cudaSuccess) return e;
+  p.tlogit = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + align256(static_cast<size_t>(parts) * M * 8));
+  const cudaError_t e = bn == 128 ? launch_phase<Phase::Lse, 128>(maps, p, s) : launch_phase<Phase::Lse, 256>(maps, p, s);
+  if (e != cudaSuccess) return e;
   return launch_pdl(xent_join_kernel, dim3(static_cast<unsigned>((M + kJoinTokens - 1) / kJoinTokens)),
                     dim3(kJoinTokens * kJoinSplit), 0, s,
-                    static_cast<const float2*>(p.part), 2 * tiles_v, p.M, p.V, static_cast<const float2*>(p.tlogit), targets,
+                    static_cast<const float2*>(p.part), parts, p.M, p.V, static_cast<const float2*>(p.tlogit), targets,
                     loss, lse);
 }
 
@@ -940,9 +1008,11 @@ cudaError_t launch_xent_backward(const void* h, const void* W, const int64_t* ta
       return cudaErrorInvalidValue;
     p.hm = i == 0 && dW ? static_cast<uint4*>(hm) : nullptr;
     p.find_scale = i == 0;
-    p.ntiles_a = p.tiles_m * tiles_of(p.vcount);
+    const int bn = logit_columns(M, p.vcount);
+    p.ntiles_a = p.tiles_m * ((p.vcount + bn - 1) / bn);
     p.ntiles_b = 0;
-    if (cudaError_t e = launch_phase<Phase::Dz>(zm, p, s); e != cudaSuccess) return e;
+    const cudaError_t e = bn == 128 ? launch_phase<Phase::Dz, 128>(zm, p, s) : launch_phase<Phase::Dz, 256>(zm, p, s);
+    if (e != cudaSuccess) return e;
     // an fp32 dW joins partial sums of 1024 tokens, one launch each (the
     // launches order the additions)
     const int step = f32 ? kF32Tokens : p.M;
@@ -961,7 +1031,7 @@ cudaError_t launch_xent_backward(const void* h, const void* W, const int64_t* ta
       // a tile also costs its epilogue, about 4 k-blocks
       p.cost_a = (p.dw_first ? cost_w : cost_h) + 4;
       p.cost_b = (p.dw_first ? cost_h : cost_w) + 4;
-      if (cudaError_t e = launch_phase<Phase::Grad>(gm, p, s); e != cudaSuccess) return e;
+      if (cudaError_t e = launch_phase<Phase::Grad, 256>(gm, p, s); e != cudaSuccess) return e;
       if (!dW) break;
     }
   }

@@ -87,10 +87,12 @@ def test_empty_work_is_ok_without_gpu():
 
 
 def test_workspace_sizes():
-    # forward: a (maximum, sum) pair per token and 128 vocabulary entries, and
-    # the target's logit per token (twice)
+    # forward: a (maximum, sum) pair per token and 128 vocabulary entries (64
+    # where the tiles are few), and the target's logit per token (twice)
     assert bl.bl_linear_xent_forward_workspace_size(2048, 8192, 512) == 64 * 2048 * 8 + 2048 * 8
     assert bl.bl_linear_xent_forward_workspace_size(1, 257, 8) == 256 + 256
+    assert bl.bl_linear_xent_forward_workspace_size(256, 9472, 8) == 148 * 256 * 8 + 256 * 8
+    assert bl.bl_linear_xent_forward_workspace_size(256, 9473, 8) == 2 * 38 * 256 * 8 + 256 * 8
     assert bl.bl_linear_xent_forward_workspace_size(0, 8192, 512) == 0
     assert bl.bl_linear_xent_forward_workspace_size(4, 8192, 60) == 0
     # backward: never the logits of the whole vocabulary (here 1 GiB in bf16)
