@@ -153,12 +153,17 @@ __device__ __forceinline__ void tma_load_2d(const CUtensorMap* map, uint64_t* ba
 // TMA load of this CTA's share of a CTA-pair operand: data lands in this
 // CTA's shared memory, completion is counted on an mbarrier that may live in
 // the peer CTA (the pair's leader). No multicast.
-__device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* map, uint32_t bar_cluster, void* dst, int x, int y) {
+__device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* map, uint32_t bar_cluster, uint32_t dst, int x,
+                                                 int y) {
   asm volatile(
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
-      "[%2];" ::"r"(smem_u32(dst)),
+      "[%2];" ::"r"(dst),
       "l"(map), "r"(bar_cluster), "r"(x), "r"(y)
       : "memory");
+}
+
+__device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* map, uint32_t bar_cluster, void* dst, int x, int y) {
+  tma_load_2d_pair(map, bar_cluster, smem_u32(dst), x, y);
 }
 
 // TMA store of a shared-memory tile to the box of `map` at (x, y); the

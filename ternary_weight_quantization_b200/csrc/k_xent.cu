@@ -68,7 +68,7 @@ struct Geo {
   static constexpr int kOffBar = kOffEpi + kEpiWarps * kSlots * kEpiBox;
   static constexpr int kNumBars = 2 * kStages + 5;    // full, empty, tmem_full[2], tmem_empty[2], done
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  // TMEM base, abort flag, issued parities; epilogue maxima at 64
+  // TMEM base, abort flag; epilogue maxima at 64
   static constexpr int kSmemBytes = kOffMisc + 128 + 1024 /*base alignment*/;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
@@ -280,7 +280,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
   uint64_t* done_bar = tmem_full + 4;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + G::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + G::kOffMisc + 4);
-  int* issued_parity = reinterpret_cast<int*>(smem + G::kOffMisc + 8);  // [kStages]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -298,7 +297,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      issued_parity[s] = -1;
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tmem_full[b], 1);
@@ -329,7 +327,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
   if (warp == kWarpLoad) {
     if (lane == 0) {
       int stage = 0;
-      uint32_t phase = 0;
+      uint32_t phase = 0, issued = 0;  // stages requested so far
+      const uint32_t bars = lead(full), smem0 = smem_u32(smem);
       bool ok = true;
       int u;
       for (int i = 0; ok && next_tile(p, pair, npairs, i, u); ++i) {
@@ -352,9 +351,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
               ok = false;
               return;
             }
-            issued_parity[stage] = static_cast<int>(phase);
             if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
-            load(kb, lead(&full[stage]), smem + stage * kStageBytes);
+            load(kb, bars + 8 * stage, smem0 + stage * kStageBytes);
+            ++issued;
             if (++stage == kStages) {
               stage = 0;
               phase ^= 1;
@@ -364,18 +363,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
         // K-major: (reduction, row); MN-major: (row, reduction)
         if constexpr (P != Phase::Grad) {
           const int w0 = p.v0 + b0;
-          each(t.nkb, [&](int kb, uint32_t bar, uint8_t* sa) {
-            const int k0 = kb * kBlockR;
+          if (na == 2 && nb == BN / 128) {
+            each(t.nkb, [&](int kb, uint32_t bar, uint32_t sa) {
+              const int k0 = kb * kBlockR;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-              if (j < na) tma_load_2d_pair(&map_h, bar, sa + j * kBox, k0, a0 + 64 * j);
+              for (int j = 0; j < 2; ++j) tma_load_2d_pair(&map_h, bar, sa + j * kBox, k0, a0 + 64 * j);
 #pragma unroll
-            for (int j = 0; j < BN / 128; ++j)
-              if (j < nb) tma_load_2d_pair(&map_w, bar, sa + (2 + j) * kBox, k0, w0 + 64 * j);
-          });
+              for (int j = 0; j < BN / 128; ++j) tma_load_2d_pair(&map_w, bar, sa + (2 + j) * kBox, k0, w0 + 64 * j);
+            });
+          } else {
+            each(t.nkb, [&](int kb, uint32_t bar, uint32_t sa) {
+              const int k0 = kb * kBlockR;
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                if (j < na) tma_load_2d_pair(&map_h, bar, sa + j * kBox, k0, a0 + 64 * j);
+#pragma unroll
+              for (int j = 0; j < BN / 128; ++j)
+                if (j < nb) tma_load_2d_pair(&map_w, bar, sa + (2 + j) * kBox, k0, w0 + 64 * j);
+            });
+          }
         } else if (t.cls == 0) {
           const int v0 = t.kb0 * kBlockR;
-          each(t.nkb, [&](int kb, uint32_t bar, uint8_t* sa) {
+          each(t.nkb, [&](int kb, uint32_t bar, uint32_t sa) {
             const int v = v0 + kb * kBlockR;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -385,7 +394,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
           });
         } else {
           auto of = [&](const CUtensorMap* dz) {
-            return [&, dz](int kb, uint32_t bar, uint8_t* sa) {
+            return [&, dz](int kb, uint32_t bar, uint32_t sa) {
               const int m = p.t0 + kb * kBlockR;
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
@@ -403,10 +412,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
         }
       }
       if (leader && (!ok || *abort_flag)) {
-        // let every copy already issued land before the pair exits
+        // let every copy already issued land before the pair exits: the last
+        // request of each stage that was requested at all
         const unsigned long long deadline = globaltimer_ns() + kWaitLimitNs;
-        for (int s = 0; s < kStages; ++s)
-          if (issued_parity[s] >= 0) mbar_drain_until(&full[s], static_cast<uint32_t>(issued_parity[s]), deadline);
+        for (uint32_t s = 0; s < kStages && s < issued; ++s)
+          mbar_drain_until(&full[s], (issued - s - 1) / kStages & 1, deadline);
       }
     }
     __syncwarp();
