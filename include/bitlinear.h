@@ -386,7 +386,7 @@ bl_status bl_linear_xent_forward(const void* h, const void* W, const int64_t* ta
  *
  * The vocabulary is taken in pieces: each piece's logits are formed again and
  * its dz kept, in bf16, only until its share of dH and dW has been added (at
- * most 64 MiB of dz, or 256 columns; dW in fp32 keeps dz to 16 significant
+ * most 128 MiB of dz, or 256 columns; dW in fp32 keeps dz to 16 significant
  * bits, as the sum of two bf16 numbers, and joins partial sums of 1024 tokens
  * in fp32). Sums over pieces are kept in fp32 and always added in the same
  * order: the same inputs give the same bits.

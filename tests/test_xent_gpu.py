@@ -95,7 +95,7 @@ def check(b, h, W, t, dl, dw_dtype=BF, dW0=None):
 # output box (32), the reduction block (64) and K's multiple of 8
 SIZES = [(1, 1, 8), (1, 2, 8), (2, 31, 16), (3, 33, 64), (1, 1000, 64), (31, 255, 72), (33, 256, 128), (127, 257, 136),
          (128, 64, 264), (129, 511, 40), (255, 513, 512), (256, 1024, 256), (257, 300, 520), (300, 5003, 200),
-         (513, 769, 1000), (64, 8192, 512)]
+         (513, 769, 1000), (64, 8192, 512), (200, 9472, 64), (200, 9473, 64), (257, 4736, 72), (65, 129, 24), (192, 128, 8)]
 
 
 @pytest.mark.parametrize("dw_dtype", [BF, F32])
@@ -105,7 +105,7 @@ def test_sizes(M, V, K, dw_dtype):
     check(run(*args, dw_dtype), *args, dw_dtype)
 
 
-@pytest.mark.parametrize("M,V,K,dw_dtype", [(8192, 8200, 64, BF), (2100, 20001, 72, F32), (4096, 17000, 136, BF),
+@pytest.mark.parametrize("M,V,K,dw_dtype", [(8192, 8200, 64, BF), (8192, 20001, 64, BF), (2100, 20001, 72, F32), (4096, 17000, 136, BF),
                                             (1025, 40000, 64, F32)])
 def test_pieces_of_the_vocabulary_and_partial_sums(M, V, K, dw_dtype):
     args = case(M, V, K, seed=7, left_out=0.1)
