@@ -329,3 +329,97 @@ def test_rows_leave_neighbours_alone_and_repeat():
     again = run_norm(x, w, bias, dy, False, True)
     for a, c in ((again.dweight, b.dweight), (again.dbias, b.dbias), (again.dx, b.dx)):
         assert torch.equal(a, c)
+
+
+@pytest.mark.parametrize("K", [32768, 32765])
+def test_offsets_past_32_bits(K):
+    """More than 2^31 values: rows near the end against the same rows alone."""
+    M, tail = 2 ** 31 // K + 40, 16
+    x = torch.zeros(M, K, dtype=BF, device="cuda")
+    x[-tail:] = rnd(tail, K, seed=1, dtype=BF)
+    dy = torch.zeros(M, K, dtype=BF, device="cuda")
+    dy[-tail:] = rnd(tail, K, seed=2, dtype=BF)
+    w = rnd(K, seed=3)
+
+    def run(x, dy):
+        m = x.shape[0]
+        s, out, s2 = bl.Act8.allocate(m, K), torch.empty_like(x), bl.Act8.allocate(m, K)
+        bl.bl_act8_encode(x, s)
+        bl.bl_act8_decode(s, out)
+        got = [s.codes[-tail:].clone(), s.scales[-tail:].clone(), out[-tail:].clone()]
+        y, rstd = out, torch.empty(m, device="cuda")
+        bl.bl_swiglu_forward(x, dy, y, s, s2)
+        got.append(y[-tail:].clone())
+        bl.bl_norm_forward(x, w, None, 1e-6, y, None, rstd, rms=True, saved8=s)
+        got += [y[-tail:].clone(), rstd[-tail:].clone(), s.codes[-tail:].clone()]
+        dw, dx = torch.empty(K, device="cuda"), y
+        ws = torch.empty(bl.bl_norm_backward_workspace_size(m, K), dtype=torch.uint8, device="cuda")
+        bl.bl_norm_backward(dy, s, w, None, rstd, dx, dw, None, ws, rms=True)
+        got += [dx[-tail:].clone()]
+        ok()
+        return got, dw
+    (a, dwa), (b, dwb) = run(x, dy), run(x[-tail:].clone(), dy[-tail:].clone())
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+    # the other rows' dy is 0: the same terms, added in another order (two sums
+    # of `tail` terms and zeros)
+    xh = saved_values(x[-tail:])[2].double() * b[5].double()[:, None]
+    assert bool(((dwa - dwb).double().abs() <= 2 * (tail + 4) * U * (dy[-tail:].double() * xh).abs().sum(0)).all())
+
+
+def test_calls_on_other_streams_and_side_by_side():
+    """Every call on a stream given to it, and two chains on two streams at once
+    (their own buffers), against the same calls on the current stream."""
+    M, K = 260, 520
+    args = [norm_case(M, K, BF, F32, False, True, seed=s) for s in (1, 2)]
+
+    def chain(x, w, bias, dy, stream=None):
+        n, s = bl.NormBuffers.allocate(M, K, BF, F32, bias=True, saved8=True), bl.SwigluBuffers.allocate(M, K, BF)
+        out = torch.empty_like(x)
+        bl.bl_norm_forward(x, w, bias, 1e-6, n.y, n.mean, n.rstd, saved8=n.saved8, stream=stream)
+        bl.bl_swiglu_forward(n.y, x, s.y, s.gate8, s.up8, stream=stream)
+        bl.bl_swiglu_backward(dy, s.gate8, s.up8, s.dgate, s.dup, stream=stream)
+        bl.bl_norm_backward(s.dgate, n.saved8, w, n.mean, n.rstd, n.dx, n.dweight, n.dbias, n.workspace, stream=stream)
+        bl.bl_act8_encode(n.dx, n.saved8, stream=stream)
+        bl.bl_act8_decode(n.saved8, out, stream=stream)
+        return [n.y, s.y, s.dgate, s.dup, n.dx, n.dweight, n.dbias, out]
+    want = [chain(*a) for a in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in args]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[chain(*a, stream=s) for a, s in zip(args, streams)] for _ in range(5)]
+    ok()
+    for run in got:
+        for a, b in zip(run, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_refused_on_the_gpu():
+    """The quick binding refuses what the checks in Python refuse, before
+    anything is launched."""
+    M, K = 4, 64
+    x, w, y = rnd(M, K, dtype=BF), rnd(K), rnd(M, K, dtype=BF)
+    mean, rstd = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+    s8 = bl.Act8.allocate(M, K)
+    for bad in (dict(x=x.half()), dict(x=x.t()), dict(x=x[:2]), dict(x=x.cpu()), dict(weight=w[:-1]), dict(weight=w.half()),
+                dict(bias=w.to(BF)), dict(mean=mean.double()), dict(rstd=rstd.cpu()), dict(y=y.float()),
+                dict(saved8=bl.Act8.allocate(M, K + 128))):
+        a = dict(x=x, weight=w, bias=w, eps=1e-6, y=y, mean=mean, rstd=rstd, saved8=s8) | bad
+        with pytest.raises(ValueError):
+            bl.bl_norm_forward(**a)
+    with pytest.raises(bl.BitLinearError, match="eps"):
+        bl.bl_norm_forward(x, w, None, float("nan"), y, mean, rstd)
+    with pytest.raises(bl.BitLinearError, match="null"):
+        bl.bl_norm_forward(x, w, None, 1e-6, y, None, rstd)
+    with pytest.raises(bl.BitLinearError, match="workspace"):
+        bl.bl_norm_backward(y, x, w, mean, rstd, y, w, None, torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(bl.BitLinearError, match="workspace"):
+        bl.bl_norm_backward(y, x, w, mean, rstd, y, w, None, None)
+    odd = torch.empty(M * K + 8, dtype=BF, device="cuda")[1:M * K + 1].view(M, K)
+    with pytest.raises(bl.BitLinearError, match="aligned"):
+        bl.bl_act8_encode(odd, s8)
+    with pytest.raises(bl.BitLinearError, match="same memory"):
+        bl.bl_swiglu_backward(x, s8, s8, y, y)
+    with pytest.raises(ValueError):
+        bl.bl_swiglu_forward(x, y, x.float())
+    ok()

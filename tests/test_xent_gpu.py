@@ -266,3 +266,89 @@ def test_other_stream_and_graphs_sharing_a_workspace():
     for o, w in zip(outs, want):
         assert torch.equal(o.loss, w.loss) and torch.equal(o.dH, w.dH) and torch.equal(o.dW, w.dW)
     assert bl.bl_get_last_error() == 0
+
+
+def test_weight_offsets_past_32_bits():
+    """A head of more than 2^31 weights: loss, lse and the gradients' last rows
+    against 64-bit sums over blocks of the vocabulary."""
+    M, K = 3, 1024
+    V = 2 ** 31 // K + 3000
+    g = torch.Generator(device="cuda").manual_seed(1)
+    W = torch.empty(V, K, dtype=BF, device="cuda")
+    for i in range(0, V, 65536):
+        W[i:i + 65536] = (torch.randn(min(65536, V - i), K, generator=g, device="cuda") * 0.03).to(BF)
+    h = torch.randn(M, K, generator=g, device="cuda").to(BF)
+    t = torch.tensor([V - 1, 5, V - 2000], device="cuda")
+    dl = torch.tensor([0.5, 0.25, 1.0], device="cuda")
+    b = run(h, W, t, dl)
+    hd = h.double()
+    z = torch.cat([hd @ W[i:i + 65536].double().t() for i in range(0, V, 65536)], 1)
+    ez = (K / 16 + 4) * S * 3 * K ** 0.5     # sum |h W| is below 3 sqrt(K) here (K products of mean 0.02)
+    lse = torch.logsumexp(z, 1)
+    assert bool(((b.lse.double() - lse).abs() <= ez + 8 * S * lse).all())
+    assert bool(((b.loss.double() - (lse - z[torch.arange(M), t])).abs() <= 2 * ez + 16 * S * lse).all())
+    dz = torch.exp(z - lse[:, None])
+    dz[torch.arange(M), t] -= 1
+    dz *= dl.double()[:, None]
+    want = dz[:, -3000:].t() @ hd
+    tol = (2.0 ** -8 + 2 * ez + 1e-5) * (dz[:, -3000:].abs().t() @ hd.abs())
+    assert bool(((b.dW[-3000:].double() - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol) + 1e-36).all())
+    dH = sum(dz[:, i:i + 65536] @ W[i:i + 65536].double() for i in range(0, V, 65536))
+    mag = sum(dz[:, i:i + 65536].abs() @ W[i:i + 65536].double().abs() for i in range(0, V, 65536))
+    tol = (2.0 ** -8 + 2 * ez + 1e-5 + V / 16 * S / 8) * mag
+    assert bool(((b.dH.double() - dH).abs() <= tol + 2.0 ** -8 * (dH.abs() + tol)).all())
+
+
+def test_two_calls_side_by_side():
+    """Two steps on two streams at once, each with its own buffers."""
+    args = [case(300, 5000, 256, seed=s) for s in (31, 32)]
+    want = [run(*a) for a in args]
+    streams = [torch.cuda.Stream() for _ in args]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    bufs = [[bl.XentBuffers.allocate(300, 5000, 256) for _ in args] for _ in range(6)]
+    torch.cuda.synchronize()
+    for row in bufs:
+        for (h, W, t, dl), b, s in zip(args, row, streams):
+            bl.bl_linear_xent_forward(h, W, t, b.loss, b.lse, b.workspace, stream=s)
+            bl.bl_linear_xent_backward(h, W, t, b.lse, dl, b.dH, b.dW, b.workspace, stream=s)
+    torch.cuda.synchronize()
+    for row in bufs:
+        for b, w in zip(row, want):
+            assert torch.equal(b.loss, w.loss) and torch.equal(b.dH, w.dH) and torch.equal(b.dW, w.dW)
+    assert bl.bl_get_last_error() == 0
+
+
+def test_uniform_and_wide_ranges_of_dloss():
+    """A mean (equal dloss), signs, zeros and magnitudes far apart."""
+    h, W, t, _ = case(200, 600, 128, seed=8)
+    for dl in (torch.full((200,), 1 / 777.0), torch.linspace(-1, 1, 200), torch.zeros(200),
+               torch.logspace(-30, 3, 200), torch.full((200,), -1e-20)):
+        dl = dl.to(torch.float32).cuda()
+        b = run(h, W, t, dl)
+        check(b, h, W, t, dl)
+    # equal dloss: dz's target term is exact before the products, so the whole
+    # gradient is off by the other terms' roundings and the result's own only
+    dl = torch.full((200,), 1 / 777.0, device="cuda")
+    b = run(h, W, t, dl)
+    p = torch.softmax(h.double() @ W.double().t(), 1)
+    p[torch.arange(200), t] -= 1
+    want = (p / 777.0) @ W.double()
+    assert float((b.dH.double() - want).norm()) <= 1.5 * 2.0 ** -9 * float(want.norm())
+
+
+def test_refused_on_the_gpu():
+    h, W, t, dl = case(4, 100, 64)
+    b = bl.XentBuffers.allocate(4, 100, 64)
+    for bad in (dict(h=h.float()), dict(W=W[:, :32]), dict(targets=t.int()), dict(loss=b.loss.double()), dict(lse=b.lse[:2]),
+                dict(h=h.cpu()), dict(workspace=b.workspace.cpu()), dict(W=W.t().contiguous().t())):
+        a = dict(h=h, W=W, targets=t, loss=b.loss, lse=b.lse, workspace=b.workspace) | bad
+        with pytest.raises(ValueError):
+            bl.bl_linear_xent_forward(**a)
+    with pytest.raises(bl.BitLinearError, match="workspace"):
+        bl.bl_linear_xent_forward(h, W, t, b.loss, b.lse, b.workspace[:16])
+    with pytest.raises(bl.BitLinearError, match="multiple of 8"):
+        bl.bl_linear_xent_forward(h[:, :60].contiguous(), W[:, :60].contiguous(), t, b.loss, b.lse, b.workspace)
+    with pytest.raises(ValueError):
+        bl.bl_linear_xent_backward(h, W, t, b.lse, dl, b.dH, b.dW.half(), b.workspace)
+    assert bl.bl_get_last_error() == 0
