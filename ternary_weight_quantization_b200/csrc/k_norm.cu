@@ -137,6 +137,10 @@ __device__ __forceinline__ void group_sum2(float (&v)[2], uint32_t buf, int t, i
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+// Through L1: for neighbouring 16-byte halves of a sector taken by two copies.
+__device__ __forceinline__ void copy_async16_l1(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy_async8(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -154,8 +158,8 @@ __device__ __forceinline__ void issue8(uint32_t dst, uint32_t stride, const __nv
   copy_async16(dst, src);
 }
 __device__ __forceinline__ void issue8(uint32_t dst, uint32_t stride, const float* src) {
-  copy_async16(dst, src);
-  copy_async16(dst + stride, src + 4);
+  copy_async16_l1(dst, src);
+  copy_async16_l1(dst + stride, src + 4);
 }
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
