@@ -950,7 +950,7 @@ def run_extras(args, local_rank):
     the same GPU (N = 1 only): the down-projection step, the 8-layer stack
     (step time and peak memory), the few-token forward, the sign-gradient
     step and the decoder LM (throughput and its largest loss gap to the
-    stored oracle curve). Each keeps its own mode's timing rules with fewer
+    stored oracle curve; also with the library's norms, gating and head loss). Each keeps its own mode's timing rules with fewer
     steps; the headline line above is unaffected."""
     import copy
     short = copy.copy(args)
@@ -978,8 +978,11 @@ def run_extras(args, local_rank):
     line = run_signsgd(copy.copy(short), 0, 1, local_rank)
     extras["signsgd"] = keep(line, ["value", "unit", "ms_per_step", "unfused_ms_per_step", "kernels"])
     line = run_lm(copy.copy(short), 0, 1, local_rank)
-    extras["lm"] = keep(line, ["value", "unit", "ms_per_step", "loss_first", "loss_last", "max_abs_dloss_vs_oracle",
-                               "dtype"])
+    lm_keys = ["value", "unit", "ms_per_step", "loss_first", "loss_last", "max_abs_dloss_vs_oracle", "dtype"]
+    extras["lm"] = keep(line, lm_keys)
+    lib = copy.copy(short)
+    lib.lm_ops = "library"
+    extras["lm_library_ops"] = keep(run_lm(lib, 0, 1, local_rank), lm_keys)
     torch.cuda.empty_cache()
     return extras
 

@@ -153,17 +153,12 @@ __device__ __forceinline__ void tma_load_2d(const CUtensorMap* map, uint64_t* ba
 // TMA load of this CTA's share of a CTA-pair operand: data lands in this
 // CTA's shared memory, completion is counted on an mbarrier that may live in
 // the peer CTA (the pair's leader). No multicast.
-__device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* map, uint32_t bar_cluster, uint32_t dst, int x,
-                                                 int y) {
+__device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* map, uint32_t bar_cluster, void* dst, int x, int y) {
   asm volatile(
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
-      "[%2];" ::"r"(dst),
+      "[%2];" ::"r"(smem_u32(dst)),
       "l"(map), "r"(bar_cluster), "r"(x), "r"(y)
       : "memory");
-}
-
-__device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* map, uint32_t bar_cluster, void* dst, int x, int y) {
-  tma_load_2d_pair(map, bar_cluster, smem_u32(dst), x, y);
 }
 
 // TMA store of a shared-memory tile to the box of `map` at (x, y); the
@@ -171,14 +166,6 @@ __device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* map, uint32_
 // issuing thread.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src_smem, int x, int y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
-               "r"(src_smem), "r"(x), "r"(y)
-               : "memory");
-}
-
-// As tma_store_2d, adding the tile's fp32 values to what the tensor holds
-// (each element one rounded fp32 addition at L2).
-__device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, uint32_t src_smem, int x, int y) {
-  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
                "r"(src_smem), "r"(x), "r"(y)
                : "memory");
 }

@@ -4,7 +4,6 @@
 
 #include <cstddef>
 #include <cstdint>
-#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace bl {
@@ -149,12 +148,6 @@ cudaError_t launch_selftest_timeout(int* err, cudaStream_t s);
 
 // Number of SMs of the current device (cached per device).
 int device_sm_count();
-
-// Tensor map of a row-major 2D array of bf16 (f32: fp32) elements with
-// 128-byte swizzled boxes of box_inner x box_outer elements; false (and a
-// launch detail) when the driver rejects it.
-bool make_swizzled_map(CUtensorMap* m, const void* base, bool f32, uint64_t inner, uint64_t outer, uint64_t row_bytes,
-                       uint32_t box_inner, uint32_t box_outer, const char* what);
 
 // Detail of the last host-side launch failure on this thread ("" if none).
 const char* launch_detail();

@@ -1642,12 +1642,6 @@ int choose_bn(int rows_a, int rows_b, int red, int npairs, const BnCost* cands, 
 
 }  // namespace
 
-bool make_swizzled_map(CUtensorMap* m, const void* base, bool f32, uint64_t inner, uint64_t outer, uint64_t row_bytes,
-                       uint32_t box_inner, uint32_t box_outer, const char* what) {
-  return make_map_2d(m, base, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, inner, outer,
-                     row_bytes, box_inner, box_outer, CU_TENSOR_MAP_SWIZZLE_128B, what);
-}
-
 const char* launch_detail() { return g_launch_detail; }
 
 void clear_launch_detail() { g_launch_detail[0] = 0; }

@@ -44,6 +44,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include <cstdint>
 #include <type_traits>
@@ -191,6 +192,23 @@ __device__ __forceinline__ void mma_stage(uint32_t d_tmem, uint64_t ad, uint64_t
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk)
     mma_f16_pair(d_tmem, ad + kk * as, bd + kk * bs, idesc(kAMn, kBMn, BN), (kb | kk) != 0);
+}
+
+// tma_load_2d_pair to a shared-memory address.
+__device__ __forceinline__ void load_pair(const CUtensorMap* map, uint32_t bar_cluster, uint32_t dst, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+      "[%2];" ::"r"(dst),
+      "l"(map), "r"(bar_cluster), "r"(x), "r"(y)
+      : "memory");
+}
+
+// As tma_store_2d, adding the tile's fp32 values to what the tensor holds
+// (each element one rounded fp32 addition at L2).
+__device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, uint32_t src_smem, int x, int y) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+               "r"(src_smem), "r"(x), "r"(y)
+               : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -375,19 +393,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
             each(t.nkb, [&](int kb, uint32_t bar, uint32_t sa) {
               const int k0 = kb * kBlockR;
 #pragma unroll
-              for (int j = 0; j < 2; ++j) tma_load_2d_pair(&map_h, bar, sa + j * kBox, k0, a0 + 64 * j);
+              for (int j = 0; j < 2; ++j) load_pair(&map_h, bar, sa + j * kBox, k0, a0 + 64 * j);
 #pragma unroll
-              for (int j = 0; j < BN / 128; ++j) tma_load_2d_pair(&map_w, bar, sa + (2 + j) * kBox, k0, w0 + 64 * j);
+              for (int j = 0; j < BN / 128; ++j) load_pair(&map_w, bar, sa + (2 + j) * kBox, k0, w0 + 64 * j);
             });
           } else {
             each(t.nkb, [&](int kb, uint32_t bar, uint32_t sa) {
               const int k0 = kb * kBlockR;
 #pragma unroll
               for (int j = 0; j < 2; ++j)
-                if (j < na) tma_load_2d_pair(&map_h, bar, sa + j * kBox, k0, a0 + 64 * j);
+                if (j < na) load_pair(&map_h, bar, sa + j * kBox, k0, a0 + 64 * j);
 #pragma unroll
               for (int j = 0; j < BN / 128; ++j)
-                if (j < nb) tma_load_2d_pair(&map_w, bar, sa + (2 + j) * kBox, k0, w0 + 64 * j);
+                if (j < nb) load_pair(&map_w, bar, sa + (2 + j) * kBox, k0, w0 + 64 * j);
             });
           }
         } else if (t.cls == 0) {
@@ -396,8 +414,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
             const int v = v0 + kb * kBlockR;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              tma_load_2d_pair(&map_dz, bar, sa + j * kBox, v, a0 + 64 * j);
-              tma_load_2d_pair(&map_w, bar, sa + (2 + j) * kBox, b0 + 64 * j, p.v0 + v);
+              load_pair(&map_dz, bar, sa + j * kBox, v, a0 + 64 * j);
+              load_pair(&map_w, bar, sa + (2 + j) * kBox, b0 + 64 * j, p.v0 + v);
             }
           });
         } else {
@@ -406,8 +424,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
               const int m = p.t0 + kb * kBlockR;
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                tma_load_2d_pair(dz, bar, sa + j * kBox, a0 + 64 * j, m);
-                tma_load_2d_pair(&map_h, bar, sa + (2 + j) * kBox, b0 + 64 * j, m);
+                load_pair(dz, bar, sa + j * kBox, a0 + 64 * j, m);
+                load_pair(&map_h, bar, sa + (2 + j) * kBox, b0 + 64 * j, m);
               }
             };
           };
@@ -823,6 +841,26 @@ __global__ void __launch_bounds__(256) xent_dh_kernel(const float4* __restrict__
 
 // ---------------------------------------------------------------- host side
 
+// Tensor map of a row-major 2D array of bf16 (f32: fp32) elements with 128-byte
+// swizzled boxes; false when the driver rejects it.
+bool make_map(CUtensorMap* m, const void* base, bool f32, uint64_t inner, uint64_t outer, uint64_t row_bytes,
+              uint32_t box_inner, uint32_t box_outer) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  if (!encode) return false;
+  const cuuint64_t dims[2] = {inner, outer}, strides[1] = {row_bytes};
+  const cuuint32_t box[2] = {box_inner, box_outer}, steps[2] = {1, 1};
+  return encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
+                dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Spreads the second kind of tiles so that the pairs end together: the least
 // end time at which they all fit. With ntiles_a = qP + e, the first e pairs
 // are busy with q + 1 of the first kind, the others with q.
@@ -895,15 +933,21 @@ Plan make_plan(int64_t M, int64_t V, int64_t K, bool f32) {
   q.piece = ((V + q.pieces - 1) / q.pieces + kTile - 1) / kTile * kTile;
   q.pieces = static_cast<int>((V + q.piece - 1) / q.piece);
   q.rows_pad = (M + kTile - 1) / kTile * kTile;
-  // few tiles of dH: its reduction over the piece is cut into slices, so that
-  // they occupy the SMs next to dW's tiles (at most 8: with up to 32 the partial
-  // sums cost what the shorter tiles save, 256 tokens, K 1024, vocabulary 20000
-  // backward 46.9 us against 52.2)
-  const int64_t tiles = static_cast<int64_t>(tiles_of(M)) * tiles_of(K);
-  const int64_t nkb = (V < q.piece ? V : q.piece) / kBlockR;
-  int64_t slices = 74 / tiles;
-  if (slices > 8) slices = 8;
+  // dH has few tiles, each with the whole piece to sum over, next to dW's many
+  // with the tokens: its reduction is cut into slices of at most two thirds of
+  // a pair's even share of all k-blocks (a tile's epilogue counted as 8), so
+  // that no pair is left alone with one. Measured on B200 (backward): 5 tokens,
+  // K 72, vocabulary 68159: 36 us, with at most 8 slices 61;
+  // 2048 x 512 x 8192: 59 us either way (4 slices).
+  const int64_t vcount = V < q.piece ? V : q.piece;
+  const int64_t tiles = static_cast<int64_t>(tiles_of(M)) * tiles_of(K), nkb = (vcount + kBlockR - 1) / kBlockR;
+  const int64_t tokens = M < kF32Tokens || !f32 ? M : kF32Tokens;
+  const int64_t wkb = (tokens + kBlockR - 1) / kBlockR * (f32 ? 2 : 1) + 8;
+  const int64_t share = (tiles * nkb + tiles_of(vcount) * tiles_of(K) * wkb) / 74 + 8;
+  int64_t slices = (3 * nkb + 2 * share - 1) / (2 * share);
+  if (slices > 32) slices = 32;
   if (slices > nkb) slices = nkb;
+  if (tiles >= 74) slices = 1;
   q.slices = slices < 1 ? 1 : static_cast<int>(slices);
   q.sums = q.pieces > 1 || q.slices > 1;
   size_t off = align256(static_cast<size_t>(M) * q.piece * 2);
@@ -946,8 +990,8 @@ size_t xent_backward_workspace_bytes(int64_t M, int64_t V, int64_t K, int dw_is_
 cudaError_t launch_xent_forward(const void* h, const void* W, const int64_t* targets, int64_t M, int64_t V, int64_t K,
                                 float* loss, float* lse, void* workspace, int* err, cudaStream_t s) {
   CUtensorMap maps[6] = {};
-  if (!make_swizzled_map(&maps[0], h, false, K, M, K * 2, 64, 64, "h") ||
-      !make_swizzled_map(&maps[1], W, false, K, V, K * 2, 64, 64, "W"))
+  if (!make_map(&maps[0], h, false, K, M, K * 2, 64, 64) ||
+      !make_map(&maps[1], W, false, K, V, K * 2, 64, 64))
     return cudaErrorInvalidValue;
   XentParams p{};
   p.M = static_cast<int>(M);
@@ -1007,16 +1051,15 @@ cudaError_t launch_xent_backward(const void* h, const void* W, const int64_t* ta
   p.dW = dW;
 
   CUtensorMap zm[6] = {}, gm[6] = {};  // maps of Dz and of Grad
-  if (!make_swizzled_map(&zm[0], h, false, K, M, K * 2, 64, 64, "h") ||
-      !make_swizzled_map(&zm[1], W, false, K, V, K * 2, 64, 64, "W") ||
-      !make_swizzled_map(&gm[0], hm, false, K, M, K * 2, 64, 64, "h (dW)"))
+  if (!make_map(&zm[0], h, false, K, M, K * 2, 64, 64) ||
+      !make_map(&zm[1], W, false, K, V, K * 2, 64, 64) ||
+      !make_map(&gm[0], hm, false, K, M, K * 2, 64, 64))
     return cudaErrorInvalidValue;
   gm[1] = zm[1];
-  if (dH && !(q.sums ? make_swizzled_map(&gm[4], sum, true, K, static_cast<uint64_t>(q.slices) * q.rows_pad, K * 4, 32, 32,
-                                         "sums of dH")
-                     : make_swizzled_map(&gm[4], dH, false, K, M, K * 2, 64, 32, "dH")))
+  if (dH && !(q.sums ? make_map(&gm[4], sum, true, K, static_cast<uint64_t>(q.slices) * q.rows_pad, K * 4, 32, 32)
+                     : make_map(&gm[4], dH, false, K, M, K * 2, 64, 32)))
     return cudaErrorInvalidValue;
-  if (dW && !make_swizzled_map(&gm[5], dW, f32, K, V, K * (f32 ? 4 : 2), f32 ? 32 : 64, 32, "dW"))
+  if (dW && !make_map(&gm[5], dW, f32, K, V, K * (f32 ? 4 : 2), f32 ? 32 : 64, 32))
     return cudaErrorInvalidValue;
 
   for (int i = 0; i < q.pieces; ++i) {
@@ -1024,11 +1067,11 @@ cudaError_t launch_xent_backward(const void* h, const void* W, const int64_t* ta
     p.vcount = static_cast<int>(V - p.v0 < q.piece ? V - p.v0 : q.piece);
     // dz of this piece: rows of `piece` elements, of which vcount are used
     // (the products read zeros beyond them)
-    if (!make_swizzled_map(&gm[2], dz, false, p.vcount, M, q.piece * 2, 64, 64, "dz") ||
-        !make_swizzled_map(&zm[4], dz, false, p.vcount, M, q.piece * 2, 64, 32, "dz (store)"))
+    if (!make_map(&gm[2], dz, false, p.vcount, M, q.piece * 2, 64, 64) ||
+        !make_map(&zm[4], dz, false, p.vcount, M, q.piece * 2, 64, 32))
       return cudaErrorInvalidValue;
-    if (f32 && (!make_swizzled_map(&gm[3], lo, false, p.vcount, M, q.piece * 2, 64, 64, "dz remainder") ||
-                !make_swizzled_map(&zm[5], lo, false, p.vcount, M, q.piece * 2, 64, 32, "dz remainder (store)")))
+    if (f32 && (!make_map(&gm[3], lo, false, p.vcount, M, q.piece * 2, 64, 64) ||
+                !make_map(&zm[5], lo, false, p.vcount, M, q.piece * 2, 64, 32)))
       return cudaErrorInvalidValue;
     p.hm = i == 0 && dW ? static_cast<uint4*>(hm) : nullptr;
     p.find_scale = i == 0;

@@ -40,6 +40,7 @@ from __future__ import annotations
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import bitlinear as b
 
@@ -123,6 +124,7 @@ class RMSNormFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, gy):
         weight, rstd, *kept = ctx.saved_tensors
         x = b.Act8(*kept) if ctx.saved8 else kept[0]
@@ -148,6 +150,7 @@ class SwigluFunction(torch.autograd.Function):
         return y.to(gate.dtype)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, gy):
         gc, gs, uc, us = ctx.saved_tensors
         dy = gy.to(torch.bfloat16).contiguous()
@@ -173,6 +176,7 @@ class HeadLossFunction(torch.autograd.Function):
         return (buf.loss.sum() * share).to(h.dtype)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g):
         h, head, targets, lse, share = ctx.saved_tensors
         (M, K), V = h.shape, head.shape[0]
