@@ -119,6 +119,18 @@ cudaError_t launch_xent_backward(const void* h, const void* W, const int64_t* ta
                                  const float* dloss, int64_t M, int64_t V, int64_t K, void* dH, void* dW,
                                  int dw_is_f32, int accumulate, void* workspace, int* err, cudaStream_t s);
 
+// The same for a few tokens (k_xent_few.cu): whether it takes the call; the
+// forward leaves xent_few_parts (maximum, sum) pairs per token, [part][M], and
+// the targets' logits (the tensor cores', and in fp32).
+bool xent_few(int64_t M);
+int xent_few_parts(int64_t V, int64_t K);
+size_t xent_few_workspace_bytes(int64_t M, int64_t V, int64_t K);
+cudaError_t launch_xent_few_forward(const void* h, const void* W, const int64_t* targets, int64_t M, int64_t V,
+                                    int64_t K, float2* part, float2* tlogit, cudaStream_t s);
+cudaError_t launch_xent_few_backward(const void* h, const void* W, const int64_t* targets, const float* lse,
+                                     const float* dloss, int64_t M, int64_t V, int64_t K, void* dH, void* dW,
+                                     int dw_is_f32, int accumulate, void* workspace, cudaStream_t s);
+
 // Activations in 8 bits and the SwiGLU gate (k_act8.cu); the code arrays of
 // the SwiGLU forward may be null.
 cudaError_t launch_act8_encode(const void* x, int f32, int64_t M, int64_t K, int8_t* codes, float* scales,

@@ -980,40 +980,49 @@ static int logit_parts(int64_t M, int64_t V) {
 }
 
 size_t xent_forward_workspace_bytes(int64_t M, int64_t V, int64_t K) {
-  return align256(static_cast<size_t>(logit_parts(M, V)) * M * 8) + align256(static_cast<size_t>(M) * 8);
+  const int parts = xent_few(M) ? xent_few_parts(V, K) : logit_parts(M, V);
+  return align256(static_cast<size_t>(parts) * M * 8) + align256(static_cast<size_t>(M) * 8);
 }
 
 size_t xent_backward_workspace_bytes(int64_t M, int64_t V, int64_t K, int dw_is_f32) {
+  if (xent_few(M)) return xent_few_workspace_bytes(M, V, K);
   return make_plan(M, V, K, dw_is_f32 != 0).bytes;
 }
 
 cudaError_t launch_xent_forward(const void* h, const void* W, const int64_t* targets, int64_t M, int64_t V, int64_t K,
                                 float* loss, float* lse, void* workspace, int* err, cudaStream_t s) {
-  CUtensorMap maps[6] = {};
-  if (!make_map(&maps[0], h, false, K, M, K * 2, 64, 64) ||
-      !make_map(&maps[1], W, false, K, V, K * 2, 64, 64))
-    return cudaErrorInvalidValue;
-  XentParams p{};
-  p.M = static_cast<int>(M);
-  p.V = static_cast<int>(V);
-  p.K = static_cast<int>(K);
-  p.vcount = p.V;
-  p.targets = targets;
-  p.err = err;
-  p.tiles_m = tiles_of(M);
-  p.tiles_k = tiles_of(K);
-  const int bn = logit_columns(M, V), parts = logit_parts(M, V);
-  p.ntiles_a = p.tiles_m * parts / 2;
-  p.h = static_cast<const uint4*>(h);
-  p.W = static_cast<const uint4*>(W);
-  p.part = static_cast<float2*>(workspace);
-  p.tlogit = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + align256(static_cast<size_t>(parts) * M * 8));
-  const cudaError_t e = bn == 128 ? launch_phase<Phase::Lse, 128>(maps, p, s) : launch_phase<Phase::Lse, 256>(maps, p, s);
+  const bool few = xent_few(M);
+  const int bn = logit_columns(M, V), parts = few ? xent_few_parts(V, K) : logit_parts(M, V);
+  float2* part = static_cast<float2*>(workspace);
+  float2* tlogit =
+      reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + align256(static_cast<size_t>(parts) * M * 8));
+  cudaError_t e;
+  if (few) {
+    e = launch_xent_few_forward(h, W, targets, M, V, K, part, tlogit, s);
+  } else {
+    CUtensorMap maps[6] = {};
+    if (!make_map(&maps[0], h, false, K, M, K * 2, 64, 64) || !make_map(&maps[1], W, false, K, V, K * 2, 64, 64))
+      return cudaErrorInvalidValue;
+    XentParams p{};
+    p.M = static_cast<int>(M);
+    p.V = static_cast<int>(V);
+    p.K = static_cast<int>(K);
+    p.vcount = p.V;
+    p.targets = targets;
+    p.err = err;
+    p.tiles_m = tiles_of(M);
+    p.tiles_k = tiles_of(K);
+    p.ntiles_a = p.tiles_m * parts / 2;
+    p.h = static_cast<const uint4*>(h);
+    p.W = static_cast<const uint4*>(W);
+    p.part = part;
+    p.tlogit = tlogit;
+    e = bn == 128 ? launch_phase<Phase::Lse, 128>(maps, p, s) : launch_phase<Phase::Lse, 256>(maps, p, s);
+  }
   if (e != cudaSuccess) return e;
   return launch_pdl(xent_join_kernel, dim3(static_cast<unsigned>((M + kJoinTokens - 1) / kJoinTokens)),
-                    dim3(kJoinTokens * kJoinSplit), 0, s,
-                    static_cast<const float2*>(p.part), parts, p.M, p.V, static_cast<const float2*>(p.tlogit), targets,
-                    loss, lse);
+                    dim3(kJoinTokens * kJoinSplit), 0, s, static_cast<const float2*>(part), parts, static_cast<int>(M),
+                    static_cast<int>(V), static_cast<const float2*>(tlogit), targets, loss, lse);
 }
 
 cudaError_t launch_xent_backward(const void* h, const void* W, const int64_t* targets, const float* lse,
@@ -1023,6 +1032,8 @@ cudaError_t launch_xent_backward(const void* h, const void* W, const int64_t* ta
     if (dW && !accumulate) return cudaMemsetAsync(dW, 0, static_cast<size_t>(V) * K * (dw_is_f32 ? 4 : 2), s);
     return cudaSuccess;
   }
+  if (xent_few(M))
+    return launch_xent_few_backward(h, W, targets, lse, dloss, M, V, K, dH, dW, dw_is_f32, accumulate, workspace, s);
   const bool f32 = dW && dw_is_f32;
   const Plan q = make_plan(M, V, K, dw_is_f32 != 0);
   uint8_t* ws = static_cast<uint8_t*>(workspace);

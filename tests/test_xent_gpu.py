@@ -352,3 +352,54 @@ def test_refused_on_the_gpu():
     with pytest.raises(ValueError):
         bl.bl_linear_xent_backward(h, W, t, b.lse, dl, b.dH, b.dW.half(), b.workspace)
     assert bl.bl_get_last_error() == 0
+
+
+# a few tokens: their own kernels, by groups of 8 tokens, units of 16 rows of W,
+# steps of 32 columns (128 at once) and tiles of 64; a vocabulary of less than
+# one unit, and one whose units are dealt out unevenly
+FEW = [(1, 5, 8), (1, 33, 2048), (2, 31, 2056), (3, 129, 4088), (4, 4737, 4096), (4, 20001, 512), (5, 4, 2048), (5, 1, 8), (6, 9473, 520),
+       (7, 40000, 16), (8, 3, 2040), (8, 1000, 2048), (8, 66000, 72), (5, 700, 2056), (8, 300, 4096), (9, 700, 512), (4, 300, 4104),
+       (16, 1009, 136), (17, 1009, 136), (25, 15, 264), (32, 17, 8192), (32, 40001, 160), (11, 1, 65536), (1, 37889, 24), (33, 500, 264)]
+
+
+@pytest.mark.parametrize("dw_dtype", [BF, F32])
+@pytest.mark.parametrize("M,V,K", FEW)
+def test_few_tokens(M, V, K, dw_dtype):
+    args = case(M, V, K, seed=M * V + K, left_out=0.3 if M > 3 else 0.0)
+    check(run(*args, dw_dtype), *args, dw_dtype)
+
+
+@pytest.mark.parametrize("M,V,K", [(3, 2500, 4096), (8, 2500, 512), (13, 3000, 200), (32, 900, 1000)])
+@pytest.mark.parametrize("dw_dtype", [BF, F32])
+def test_few_tokens_left_out_accumulated_and_parts(M, V, K, dw_dtype):
+    h, W, t, dl = case(M, V, K, seed=2)
+    t[1], dl[1] = -1, float("nan")
+    clean = h.clone()
+    h[1], clean[1] = float("nan"), 0.0
+    dW0 = torch.randn(V, K, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(dw_dtype)
+    b = run(h, W, t, dl, dw_dtype, dW=dW0.clone(), accumulate=True)
+    b.lse[1] = torch.logsumexp(clean[1].double() @ W.double().t(), 0)  # of the token itself: not a number
+    check(b, clean, W, t, dl, dw_dtype, dW0=dW0)
+    again = run(h, W, t, dl, dw_dtype, dW=dW0.clone(), accumulate=True)
+    assert torch.equal(b.dW, again.dW) and torch.equal(b.dH, again.dH) and torch.equal(b.loss, again.loss)
+    # one gradient without the other
+    dH, dW = torch.empty_like(b.dH), torch.empty_like(b.dW)
+    bl.bl_linear_xent_backward(h, W, t, again.lse, dl, dH, None, b.workspace)
+    bl.bl_linear_xent_backward(h, W, t, again.lse, dl, None, dW, b.workspace)
+    whole = run(h, W, t, dl, dw_dtype)
+    assert torch.equal(dH, whole.dH) and torch.equal(dW, whole.dW)
+    assert bl.bl_get_last_error() == 0
+
+
+@pytest.mark.parametrize("M,K", [(2, 2560), (8, 512), (20, 128)])
+def test_few_tokens_with_infinite_and_no_number_logits(M, K):
+    h, W, t, dl = case(M, 700, K, seed=4)
+    W[11, 3], h[:, 3] = float("-inf"), 1.0  # a logit of -inf: probability zero
+    t[:] = 5
+    b = run(h, W, t, dl)
+    z = h.float() @ W.float().t()
+    assert torch.isfinite(b.loss).all() and torch.allclose(b.lse, torch.logsumexp(z, 1), rtol=1e-4, atol=1e-4)
+    assert bool((b.dW[11] == 0).all())
+    W[11, 3] = float("nan")
+    b = run(h, W, t, dl)
+    assert bool(b.loss.isnan().all()) and bool(b.lse.isnan().all())
