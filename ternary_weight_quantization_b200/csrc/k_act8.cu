@@ -13,6 +13,9 @@
 // 128 values (half a warp of 8-value lanes where K % 8 == 0, else a warp, see
 // bl_act8.cuh). A block takes consecutive units, kU per thread, and issues all
 // of a thread's loads before it computes.
+//
+// Measured on B200, 4096 x 6912 bf16: A1 + A2 29.8 us (0.88 of the copy rate), U1
+// with codes + U2 78 us (0.90). 1021 x 2565 fp32 (scalar): A1 + A2 10.1 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

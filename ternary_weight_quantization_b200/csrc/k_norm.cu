@@ -20,6 +20,13 @@
 // x K floats at most), which a second launch adds in a fixed order. Rows wider
 // than 8192 columns take two passes in the backward: the row sums, then column
 // strips.
+//
+// Measured on B200 (back to back in a graph): 4096 x 2560 bf16 with the 8-bit x:
+// forward 11.5 us (4.6 TB/s), backward 19.8 (2.7 TB/s; of these 6 to 8 are the
+// start, the groups' joining and the second launch: 16384 x 2560 takes 48.6 us,
+// 0.80 of the copy rate). 4096 x 2560 fp32: 14.4 (0.90) and 29.4 us. Rows that fill
+// every thread's places spare the column tests: with them the two took 13.0 and
+// 21.3 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -935,7 +942,8 @@ cudaError_t forward_vec(const NormArgs& p, cudaStream_t s) {
 template <typename T, bool kRms, bool kSave>
 cudaError_t forward_rows(const NormArgs& p, cudaStream_t s) {
   // the most columns per thread (16, 32 or, for the widest rows, 64) that
-  // leave at most a tenth of the group's places empty
+  // leave at most a tenth of the group's places empty. Measured on B200 (bf16),
+  // 32 against 16: 4096 x 4096 with codes 14.8 and 16.9 us, 4096 x 1024 4.3 and 4.7
   const int k2 = round32((p.K + 15) / 16) * 16, k4 = round32((p.K + 31) / 32) * 32;
   if (p.K > 8192) return forward_vec<T, 8, kRms, kSave>(p, s);
   if (p.K > 4096 || 10 * (k4 - p.K) <= k4 || k4 <= k2) return forward_vec<T, 4, kRms, kSave>(p, s);
