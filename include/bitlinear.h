@@ -363,7 +363,7 @@ bl_status bl_signsgd_apply(const uint32_t* sign_words, int ranks, void* W, bl_dt
  * (infinities and NaN included) does not matter.
  * workspace: at least bl_linear_xent_forward_workspace_size(M,V,K) bytes,
  * 16-byte aligned, no initialisation, one call at a time per workspace: one
- * (maximum, sum) pair per token and 64 or 128 vocabulary entries, never the
+ * (maximum, sum) pair per token and 64 or more vocabulary entries, never the
  * logits.
  * Limits: K a multiple of 8 up to 65536, M up to 131072, V up to 2^24.
  * M == 0 is a no-op (the workspace size is then 0).
@@ -388,7 +388,8 @@ bl_status bl_linear_xent_forward(const void* h, const void* W, const int64_t* ta
  * its dz kept, in bf16, only until its share of dH and dW has been added (at
  * most 128 MiB of dz, or 256 columns; dW in fp32 keeps dz to 16 significant
  * bits, as the sum of two bf16 numbers, and joins partial sums of 1024 tokens
- * in fp32). Sums over pieces are kept in fp32 and always added in the same
+ * in fp32). Up to 8 tokens take the whole vocabulary at once, with dz to 16
+ * significant bits in 32 bytes per entry for either dW. Sums over pieces are kept in fp32 and always added in the same
  * order: the same inputs give the same bits.
  * lse is X1's output. dH [M,K] bf16 or NULL (skipped); dW [V,K] of dw_dtype
  * (BL_BF16 or BL_F32) or NULL (skipped); accumulate_dW != 0 adds to what dW

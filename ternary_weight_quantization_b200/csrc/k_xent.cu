@@ -765,7 +765,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
 // block, the tiles spread over kJoinSplit threads of each token, joined in a
 // fixed order. (8 tokens, so that a few thousand tokens fill the SMs and a
 // thread has few loads to wait for: at 2048 tokens and 1024 parts 10.8 us with
-// 32 tokens and 32 threads each.)
+// 32 tokens and 32 threads each.) With h (the few tokens' forward), the warps
+// that the last step leaves idle sum the targets' logits in fp32; they need
+// nothing of the launch before, which began after all earlier ones had ended.
 constexpr int kJoinTokens = 8, kJoinSplit = 64;
 
 __device__ __forceinline__ float2 join_parts(float2 a, float2 b) {
@@ -776,10 +778,35 @@ __device__ __forceinline__ float2 join_parts(float2 a, float2 b) {
 
 __global__ void __launch_bounds__(kJoinTokens* kJoinSplit)
     xent_join_kernel(const float2* __restrict__ part, int tiles, int M, int V, const float2* __restrict__ tlogit,
-                     const int64_t* __restrict__ targets, float* loss, float* lse) {
+                     const int64_t* __restrict__ targets, float* loss, float* lse, const __nv_bfloat16* h,
+                     const __nv_bfloat16* W, int K) {
+  __shared__ float2 sh[kJoinTokens][kJoinSplit + 1];
+  __shared__ float target_logit[kJoinTokens];
+  if (h && threadIdx.x >= 32 * kJoinTokens) {
+    const int w = (threadIdx.x >> 5) - kJoinTokens, lane = threadIdx.x & 31;
+    const int m = static_cast<int>(blockIdx.x) * kJoinTokens + w;
+    const int64_t t = m < M ? targets[m] : -1;
+    if (t >= 0 && t < V) {
+      f32x2 a[2] = {};
+#pragma unroll 2
+      for (int k = lane * 8; k < K; k += 256) {
+        Raw8<__nv_bfloat16> x, y;
+        x.load(h + static_cast<int64_t>(m) * K + k);
+        y.load(W + t * K + k);
+        f32x2 xv[4], yv[4];
+        x.get(xv);
+        y.get(yv);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i & 1] = fma2(xv[i], yv[i], a[i & 1]);
+      }
+      float z = sum2(add2(a[0], a[1]));
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) z += __shfl_xor_sync(0xffffffffu, z, s);
+      if (lane == 0) target_logit[w] = z;
+    }
+  }
   pdl_wait_primary();
   pdl_launch_dependents();
-  __shared__ float2 sh[kJoinTokens][kJoinSplit + 1];
   const float2 none = make_float2(__uint_as_float(0xFF800000u), 0.0f);
   const int x = threadIdx.x % kJoinTokens, y = threadIdx.x / kJoinTokens;
   const int m = static_cast<int>(blockIdx.x) * kJoinTokens + x;
@@ -814,6 +841,7 @@ __global__ void __launch_bounds__(kJoinTokens* kJoinSplit)
   for (int s = 16; s > 0; s >>= 1)
     a = join_parts(a, make_float2(__shfl_xor_sync(0xffffffffu, a.x, s), __shfl_xor_sync(0xffffffffu, a.y, s)));
   if (lane == 0 && mm < M) {
+    if (h) tl.y = target_logit[warp];
     float l = a.x + logf(a.y);
     float nll = 0.0f;
     if (t >= 0 && t < V) {
@@ -1027,7 +1055,9 @@ cudaError_t launch_xent_forward(const void* h, const void* W, const int64_t* tar
   if (e != cudaSuccess) return e;
   return launch_pdl(xent_join_kernel, dim3(static_cast<unsigned>((M + kJoinTokens - 1) / kJoinTokens)),
                     dim3(kJoinTokens * kJoinSplit), 0, s, static_cast<const float2*>(part), parts, static_cast<int>(M),
-                    static_cast<int>(V), static_cast<const float2*>(tlogit), targets, loss, lse);
+                    static_cast<int>(V), static_cast<const float2*>(tlogit), targets, loss, lse,
+                    few ? static_cast<const __nv_bfloat16*>(h) : nullptr, static_cast<const __nv_bfloat16*>(W),
+                    static_cast<int>(K));
 }
 
 cudaError_t launch_xent_backward(const void* h, const void* W, const int64_t* targets, const float* lse,

@@ -18,14 +18,14 @@
 //             registers, W's tiles transposed on their way out of shared memory.
 //             The third joins dH over the row blocks, in a fixed order
 //
-// The target's logit is summed once more in fp32, as in the tiles' kernel (the
-// tensor cores' sums drop up to one step of fp32 per 16 terms).
+// The join sums the target's logit once more in fp32 (the tensor cores' sums drop
+// up to one step of fp32 per 16 terms).
 //
 // Bound by HBM where W is large, by the launches (two, three) where it is not.
 // Measured on B200, forward / backward with a bf16 dW, next to the tiles' kernel:
-// one token, 131072 x 4096: 170 / 580 us (206 / 650); the forward reads W at
-// 6.3 TB/s. 4 tokens, 32000 x 2048: 24 / 71 (32 / 94). 8 tokens, 8192 x 512:
-// 6.0 / 11.3 (8.2 / 19.3). 5 tokens, 68159 x 72: 7.5 / 16.5 (16.0 / 35.8).
+// one token, 131072 x 4096: 172 / 575 us (206 / 650); the forward reads W at
+// 6.2 TB/s. 4 tokens, 32000 x 2048: 24 / 70 (32 / 94). 8 tokens, 8192 x 512:
+// 5.6 / 11.3 (8.2 / 19.3). 5 tokens, 68159 x 72: 7.4 / 16.5 (16.0 / 35.8).
 // The same kernels on two groups of 8 tokens: 16 tokens, 32000 x 2560: 37.8 / 134
 // (36.9 / 107); the tiles take over above 8.
 #include <cuda_bf16.h>
@@ -50,7 +50,7 @@ struct FewParams {
   int M, V, K;
   int ksplit;      // logits: warps that share a unit's K (a power of two, <= kWarps)
   float2* part;    // forward: [block][M]
-  float2* tlogit;  // forward: [M], the tensor cores' logit and the fp32 one
+  float2* tlogit;  // forward: [M], the targets' logits (x)
   const float* lse;
   const float* dloss;
   uint32_t* dz;    // backward: [V][8 tokens: 4 words of hi, 4 of lo]
@@ -137,6 +137,7 @@ __device__ __forceinline__ void few_logits(const FewParams& p, int row0, int col
   float acc[2][4] = {};
   constexpr int kAhead = 4;  // steps whose loads are in flight
   int k = col0;
+#pragma unroll 1  // (unrolled, the registers run out: 178 us for 172)
   for (; k + 32 * kAhead <= cols; k += 32 * kAhead) {
     uint4 w0[kAhead], w1[kAhead], x[kAhead];
 #pragma unroll
@@ -268,26 +269,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2) few_logits_kernel(const FewPar
         join(a.x, a.y, b.x, b.y);
       }
       p.part[static_cast<int64_t>(blockIdx.x) * p.M + threadIdx.x] = a;
-    }
-    // the targets' logits in fp32, a warp each
-    for (int m = blockIdx.x + (warp ^ (kWarps - 1)) * gridDim.x; m < p.M; m += gridDim.x * kWarps) {
-      const int64_t target = __ldg(p.targets + m);
-      if (target < 0 || target >= p.V) continue;
-      f32x2 a2[2] = {};
-      for (int k = lane * 8; k < p.K; k += 256) {
-        Raw8<__nv_bfloat16> x, w;
-        x.load(p.h + static_cast<int64_t>(m) * p.K + k);
-        w.load(p.W + target * p.K + k);
-        f32x2 xv[4], wv[4];
-        x.get(xv);
-        w.get(wv);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a2[i & 1] = fma2(xv[i], wv[i], a2[i & 1]);
-      }
-      float z = sum2(add2(a2[0], a2[1]));
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) z += __shfl_xor_sync(0xffffffffu, z, s);
-      if (lane == 0) p.tlogit[m].y = z;
     }
   }
 }
@@ -475,8 +456,8 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The logits' warps per unit of 16 rows: as many as it takes to give every SM
 // 8 warps, as long as each has more than one round of loads (4 steps of 32).
-// Measured on B200 (forward): 4000 x 4096 10.1 us with 8 warps, 27.9 with one;
-// 8192 x 512 5.6 with 4, 6.9 with one; 32000 x 2048 25.2 with two, 23.7 with one.
+// Measured on B200 (forward): 4000 x 4096 8.9 us with 8 warps, 27.9 with one;
+// 8192 x 512 5.3 with 4, 6.9 with one; 32000 x 2048 25.2 with two, 23.7 with one.
 int few_ksplit(int64_t V, int64_t K) {
   const int64_t units = ceil_div(V, 16), steps = ceil_div(K, 32);
   int ks = 1;
