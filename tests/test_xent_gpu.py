@@ -199,26 +199,29 @@ def test_empty_batch(dw_dtype):
     assert bool((b.dW == 0).all())
 
 
-def test_runs_repeat_and_neighbours_stay():
-    M, V, K = 333, 1111, 264
+@pytest.mark.parametrize("M", [333, 7])
+def test_runs_repeat_and_neighbours_stay(M):
+    V, K = 1111, 264
     h, W, t, dl = case(M, V, K, seed=9)
     a = run(h, W, t, dl)
     big = {"loss": torch.full((M + 8,), 7.0, device="cuda"), "dH": torch.full((M + 3, K), 7.0, dtype=BF, device="cuda"),
            "dW": torch.full((V + 3, K), 7.0, dtype=BF, device="cuda"),
+           "lse": torch.full((M + 8,), 7.0, device="cuda"),
            "ws": torch.full((a.workspace.numel() + 4096,), 0xA5, dtype=torch.uint8, device="cuda")}
     n = a.workspace.numel()
-    lse = torch.empty(M, device="cuda")
+    lse = big["lse"][:M]
     bl.bl_linear_xent_forward(h, W, t, big["loss"][:M], lse, big["ws"][:n])
     bl.bl_linear_xent_backward(h, W, t, lse, dl, big["dH"][:M], big["dW"][:V], big["ws"][:n])
     torch.cuda.synchronize()
     assert torch.equal(big["loss"][:M], a.loss) and torch.equal(big["dH"][:M], a.dH) and torch.equal(big["dW"][:V], a.dW)
-    assert bool((big["loss"][M:] == 7).all()) and bool((big["dH"][M:] == 7).all()) and bool((big["dW"][V:] == 7).all())
+    assert bool((big["loss"][M:] == 7).all()) and bool((big["lse"][M:] == 7).all()) and bool((big["dH"][M:] == 7).all()) and bool((big["dW"][V:] == 7).all())
     assert bool((big["ws"][n:] == 0xA5).all())
 
 
-def test_gradients_by_differences():
+@pytest.mark.parametrize("M", [20, 6])
+def test_gradients_by_differences(M):
     """Directional differences of the 64-bit loss at the bf16 inputs."""
-    M, V, K = 20, 300, 64
+    V, K = 300, 64
     h, W, t, dl = case(M, V, K, seed=4, left_out=0.2)
     b = run(h, W, t, dl, F32)
     live = t >= 0
@@ -238,8 +241,9 @@ def test_gradients_by_differences():
         assert abs(num - float((grad.double() * v).sum())) <= rel * float((grad.double() * v).abs().sum()) + 1e-7
 
 
-def test_other_stream_and_graphs_sharing_a_workspace():
-    M, V, K = 200, 900, 128
+@pytest.mark.parametrize("M", [200, 5])
+def test_other_stream_and_graphs_sharing_a_workspace(M):
+    V, K = 900, 128
     cases = [case(M, V, K, seed=i) for i in (21, 22)]
     want = [run(*c) for c in cases]
     side = torch.cuda.Stream()
@@ -268,18 +272,19 @@ def test_other_stream_and_graphs_sharing_a_workspace():
     assert bl.bl_get_last_error() == 0
 
 
-def test_weight_offsets_past_32_bits():
+@pytest.mark.parametrize("M", [3, 9])
+def test_weight_offsets_past_32_bits(M):
     """A head of more than 2^31 weights: loss, lse and the gradients' last rows
     against 64-bit sums over blocks of the vocabulary."""
-    M, K = 3, 1024
+    K = 1024
     V = 2 ** 31 // K + 3000
     g = torch.Generator(device="cuda").manual_seed(1)
     W = torch.empty(V, K, dtype=BF, device="cuda")
     for i in range(0, V, 65536):
         W[i:i + 65536] = (torch.randn(min(65536, V - i), K, generator=g, device="cuda") * 0.03).to(BF)
     h = torch.randn(M, K, generator=g, device="cuda").to(BF)
-    t = torch.tensor([V - 1, 5, V - 2000], device="cuda")
-    dl = torch.tensor([0.5, 0.25, 1.0], device="cuda")
+    t = torch.tensor([V - 1, 5, V - 2000] * (M // 3), device="cuda")
+    dl = torch.tensor([0.5, 0.25, 1.0] * (M // 3), device="cuda")
     b = run(h, W, t, dl)
     hd = h.double()
     z = torch.cat([hd @ W[i:i + 65536].double().t() for i in range(0, V, 65536)], 1)
@@ -299,14 +304,15 @@ def test_weight_offsets_past_32_bits():
     assert bool(((b.dH.double() - dH).abs() <= tol + 2.0 ** -8 * (dH.abs() + tol)).all())
 
 
-def test_two_calls_side_by_side():
+@pytest.mark.parametrize("M", [300, 4])
+def test_two_calls_side_by_side(M):
     """Two steps on two streams at once, each with its own buffers."""
-    args = [case(300, 5000, 256, seed=s) for s in (31, 32)]
+    args = [case(M, 5000, 256, seed=s) for s in (31, 32)]
     want = [run(*a) for a in args]
     streams = [torch.cuda.Stream() for _ in args]
     for s in streams:
         s.wait_stream(torch.cuda.current_stream())
-    bufs = [[bl.XentBuffers.allocate(300, 5000, 256) for _ in args] for _ in range(6)]
+    bufs = [[bl.XentBuffers.allocate(M, 5000, 256) for _ in args] for _ in range(6)]
     torch.cuda.synchronize()
     for row in bufs:
         for (h, W, t, dl), b, s in zip(args, row, streams):
@@ -319,20 +325,21 @@ def test_two_calls_side_by_side():
     assert bl.bl_get_last_error() == 0
 
 
-def test_uniform_and_wide_ranges_of_dloss():
+@pytest.mark.parametrize("M", [200, 8])
+def test_uniform_and_wide_ranges_of_dloss(M):
     """A mean (equal dloss), signs, zeros and magnitudes far apart."""
-    h, W, t, _ = case(200, 600, 128, seed=8)
-    for dl in (torch.full((200,), 1 / 777.0), torch.linspace(-1, 1, 200), torch.zeros(200),
-               torch.logspace(-30, 3, 200), torch.full((200,), -1e-20)):
+    h, W, t, _ = case(M, 600, 128, seed=8)
+    for dl in (torch.full((M,), 1 / 777.0), torch.linspace(-1, 1, M), torch.zeros(M),
+               torch.logspace(-30, 3, M), torch.full((M,), -1e-20)):
         dl = dl.to(torch.float32).cuda()
         b = run(h, W, t, dl)
         check(b, h, W, t, dl)
     # equal dloss: dz's target term is exact before the products, so the whole
     # gradient is off by the other terms' roundings and the result's own only
-    dl = torch.full((200,), 1 / 777.0, device="cuda")
+    dl = torch.full((M,), 1 / 777.0, device="cuda")
     b = run(h, W, t, dl)
     p = torch.softmax(h.double() @ W.double().t(), 1)
-    p[torch.arange(200), t] -= 1
+    p[torch.arange(M), t] -= 1
     want = (p / 777.0) @ W.double()
     assert float((b.dH.double() - want).norm()) <= 1.5 * 2.0 ** -9 * float(want.norm())
 
@@ -359,7 +366,7 @@ def test_refused_on_the_gpu():
 # one unit, and one whose units are dealt out unevenly
 FEW = [(1, 5, 8), (1, 33, 2048), (2, 31, 2056), (3, 129, 4088), (4, 4737, 4096), (4, 20001, 512), (5, 4, 2048), (5, 1, 8), (6, 9473, 520),
        (7, 40000, 16), (8, 3, 2040), (8, 1000, 2048), (8, 66000, 72), (5, 700, 2056), (8, 300, 4096), (9, 700, 512), (4, 300, 4104),
-       (16, 1009, 136), (17, 1009, 136), (25, 15, 264), (32, 17, 8192), (32, 40001, 160), (11, 1, 65536), (1, 37889, 24), (33, 500, 264)]
+       (16, 1009, 136), (17, 1009, 136), (25, 15, 264), (32, 17, 8192), (32, 40001, 160), (11, 1, 65536), (7, 1, 65536), (8, 40, 65536), (2, 600, 32768), (1, 37889, 24), (33, 500, 264)]
 
 
 @pytest.mark.parametrize("dw_dtype", [BF, F32])
