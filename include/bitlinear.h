@@ -388,9 +388,10 @@ bl_status bl_linear_xent_forward(const void* h, const void* W, const int64_t* ta
  * its dz kept, in bf16, only until its share of dH and dW has been added (at
  * most 128 MiB of dz, or 256 columns; dW in fp32 keeps dz to 16 significant
  * bits, as the sum of two bf16 numbers, and joins partial sums of 1024 tokens
- * in fp32). Up to 8 tokens take the whole vocabulary at once, with dz to 16
- * significant bits in 32 bytes per entry for either dW. Sums over pieces are kept in fp32 and always added in the same
- * order: the same inputs give the same bits.
+ * in fp32). Up to 16 tokens take the whole vocabulary at once, with dz to 16
+ * significant bits in 32 bytes per entry and 8 tokens for either dW. Sums over
+ * pieces are kept in fp32 and always added in the same order: the same inputs
+ * give the same bits.
  * lse is X1's output. dH [M,K] bf16 or NULL (skipped); dW [V,K] of dw_dtype
  * (BL_BF16 or BL_F32) or NULL (skipped); accumulate_dW != 0 adds to what dW
  * holds. A left-out token (X1) has dz = 0 whatever its h, lse and dloss hold:

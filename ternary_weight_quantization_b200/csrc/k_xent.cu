@@ -45,7 +45,8 @@
 // the peak: K is short, so Lse and Dz wait for the exponentials), 4096, 2560, 32000
 // in 2.05 ms; the forward alone at 2048, 2560, 131072 in 1.03 ms (1337 TFLOP/s).
 // With few tiles the time is a tile's own: about 6 us of launch, fill and epilogue
-// and 0.3 us per stage. Up to 8 tokens have kernels of their own (k_xent_few.cu).
+// and 0.3 us per stage. Up to 16 tokens have kernels of their own
+// (k_xent_few.cu).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

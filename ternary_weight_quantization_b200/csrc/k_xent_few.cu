@@ -1,7 +1,7 @@
-// The head cross-entropy for a few tokens (X1, X2 with up to 8 tokens): a
+// The head cross-entropy for a few tokens (X1, X2 with up to 16 tokens): a
 // handful of tokens leaves the tensor-core tiles of 256 empty, and what counts
 // is how fast W streams through. Here the rows of W are the 16-row operand of
-// mma.sync and the tokens its 8 columns; W goes from global memory to the
+// mma.sync and 8 or twice 8 tokens its columns; W goes from global memory to the
 // operands' registers without shared memory in between.
 //
 //   logits    a warp takes 16 rows of W. The sum over K may take its terms in
@@ -26,8 +26,10 @@
 // one token, 131072 x 4096: 172 / 575 us (206 / 650); the forward reads W at
 // 6.2 TB/s. 4 tokens, 32000 x 2048: 24 / 70 (32 / 94). 8 tokens, 8192 x 512:
 // 5.6 / 11.3 (8.2 / 19.3). 5 tokens, 68159 x 72: 7.4 / 16.5 (16.0 / 35.8).
-// The same kernels on two groups of 8 tokens: 16 tokens, 32000 x 2560: 37.8 / 134
-// (36.9 / 107); the tiles take over above 8.
+// 16 tokens, 8192 x 512: 7.2 / 14.9 (8.1 / 19.2); 2000 x 1000: 6.1 / 12.3 (10.3 /
+// 18.8); 32000 x 2560: 34.6 / 106 (35.5 / 105), with an fp32 dW 136 (134). With four
+// groups 32 tokens, 8192 x 512 took 11.6 / 30.5 (8.4 / 19.6): the reads of h outgrow
+// L1, and the tiles take over above 16.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -53,7 +55,7 @@ struct FewParams {
   float2* tlogit;  // forward: [M], the targets' logits (x)
   const float* lse;
   const float* dloss;
-  uint32_t* dz;    // backward: [V][8 tokens: 4 words of hi, 4 of lo]
+  uint32_t* dz;    // backward: [V][group of 8 tokens][4 words of hi, 4 of lo]
   float* dh_part;  // [row block][M][K], or null
   void* dW;        // or null
   int w_add;
@@ -118,28 +120,35 @@ __device__ __forceinline__ void join(float& top, float& sum, float top2, float s
   top = n;
 }
 
-// One step of 32 columns: two instructions, two accumulators, so
+// One step of 32 columns: two instructions per 8 tokens, two accumulators, so
 // that instructions do not wait on each other and the sums' chains are short.
-__device__ __forceinline__ void logits_step(float (&acc)[2][4], const uint4& w0, const uint4& w1, const uint4& x) {
-  mma16816(acc[0], w0.x, w1.x, w0.y, w1.y, x.x, x.y);
-  mma16816(acc[1], w0.z, w1.z, w0.w, w1.w, x.z, x.w);
+template <int NT>
+__device__ __forceinline__ void logits_step(float (&acc)[2][NT][4], const uint4& w0, const uint4& w1,
+                                            const uint4 (&x)[NT]) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    mma16816(acc[0][t], w0.x, w1.x, w0.y, w1.y, x[t].x, x[t].y);
+    mma16816(acc[1][t], w0.z, w1.z, w0.w, w1.w, x[t].z, x[t].w);
+  }
 }
 
-// The warp's share of the logits of 16 rows: (row lane / 4, tokens 2 (lane % 4)
-// and the next), then the same 8 rows below.
+// The warp's share of the logits of 16 rows: c[t] holds (row lane / 4, tokens
+// 8t + 2 (lane % 4) and the next), then the same 8 rows below.
+template <int NT>
 __device__ __forceinline__ void few_logits(const FewParams& p, int row0, int col0, int cols, const __nv_bfloat16* hp,
-                                           bool on, float (&c)[4]) {
+                                           const bool (&on)[NT], float (&c)[NT][4]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int last = p.V - 1;
   const __nv_bfloat16* wa = p.W + static_cast<int64_t>(row0 + g < last ? row0 + g : last) * p.K;
   const __nv_bfloat16* wb = p.W + static_cast<int64_t>(row0 + g + 8 < last ? row0 + g + 8 : last) * p.K;
+  const int64_t group = static_cast<int64_t>(8) * p.K;  // from a token to the one 8 below
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  float acc[2][4] = {};
-  constexpr int kAhead = 4;  // steps whose loads are in flight
+  float acc[2][NT][4] = {};
+  constexpr int kAhead = NT == 1 ? 4 : 3;  // steps whose loads are in flight (128 registers)
   int k = col0;
 #pragma unroll 1  // (unrolled, the registers run out: 178 us for 172)
   for (; k + 32 * kAhead <= cols; k += 32 * kAhead) {
-    uint4 w0[kAhead], w1[kAhead], x[kAhead];
+    uint4 w0[kAhead], w1[kAhead], x[kAhead][NT];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       w0[i] = load_stream(wa + k + 32 * i + 8 * q);
@@ -147,25 +156,31 @@ __device__ __forceinline__ void few_logits(const FewParams& p, int row0, int col
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
-      x[i] = on ? __ldg(reinterpret_cast<const uint4*>(hp + k + 32 * i + 8 * q)) : zero;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) logits_step(acc, w0[i], w1[i], x[i]);
+      for (int t = 0; t < NT; ++t)
+        x[i][t] = on[t] ? __ldg(reinterpret_cast<const uint4*>(hp + t * group + k + 32 * i + 8 * q)) : zero;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) logits_step<NT>(acc, w0[i], w1[i], x[i]);
   }
   if (k < cols) {  // the last columns, all requested at once as well
-    uint4 w0[kAhead], w1[kAhead], x[kAhead];
+    uint4 w0[kAhead], w1[kAhead], x[kAhead][NT];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int at = k + 32 * i + 8 * q;
       w0[i] = at < cols ? load_stream(wa + at) : zero;
       w1[i] = at < cols ? load_stream(wb + at) : zero;
-      x[i] = at < cols && on ? __ldg(reinterpret_cast<const uint4*>(hp + at)) : zero;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        x[i][t] = at < cols && on[t] ? __ldg(reinterpret_cast<const uint4*>(hp + t * group + at)) : zero;
     }
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) logits_step(acc, w0[i], w1[i], x[i]);
+    for (int i = 0; i < kAhead; ++i) logits_step<NT>(acc, w0[i], w1[i], x[i]);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = acc[0][i] + acc[1][i];
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[t][i] = acc[0][t][i] + acc[1][t][i];
 }
 
 // dz as hi + lo, a pair of tokens.
@@ -174,10 +189,10 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint3
   lo = pack_bf16x2(b - bf16_hi(hi), a - bf16_lo(hi));
 }
 
-template <bool kGrad>
+template <int NT, bool kGrad>
 __global__ void __launch_bounds__(kWarps * 32, 2) few_logits_kernel(const FewParams p) {
-  __shared__ float4 shares[2][kWarps][32];
-  __shared__ float2 pairs[kWarps][8];
+  __shared__ float4 shares[2][kWarps][NT][32];
+  __shared__ float2 pairs[kWarps][8 * NT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int ks = p.ksplit, groups = kWarps / ks, grp = warp / ks, slice = warp % ks;
   const int steps = (p.K + 31) / 32, per = (steps + ks - 1) / ks;
@@ -190,34 +205,45 @@ __global__ void __launch_bounds__(kWarps * 32, 2) few_logits_kernel(const FewPar
   pdl_wait_primary();
   pdl_launch_dependents();
 
-  const bool on = kGrad ? counts(p, g) : g < p.M;
   const __nv_bfloat16* hp = p.h + static_cast<int64_t>(g) * p.K;
-  int tgt[2];  // the lane's two tokens: their targets, or -1
-  float nlse[2], gain[2];
+  bool on[NT];
+  int tgt[NT][2];  // the lane's tokens, two of every 8: their targets, or -1
+  float nlse[NT][2], gain[NT][2], top[NT][2], sum[NT][2];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int m = 2 * q + e;
-    const bool live = counts(p, m);
-    tgt[e] = live ? static_cast<int>(__ldg(p.targets + m)) : -1;
-    nlse[e] = kGrad && live ? -__ldg(p.lse + m) * kLog2e : 0.0f;
-    gain[e] = kGrad && live ? __ldg(p.dloss + m) : 0.0f;
+  for (int t = 0; t < NT; ++t) {
+    on[t] = kGrad ? counts(p, 8 * t + g) : 8 * t + g < p.M;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int m = 8 * t + 2 * q + e;
+      const bool live = counts(p, m);
+      tgt[t][e] = live ? static_cast<int>(__ldg(p.targets + m)) : -1;
+      nlse[t][e] = kGrad && live ? -__ldg(p.lse + m) * kLog2e : 0.0f;
+      gain[t][e] = kGrad && live ? __ldg(p.dloss + m) : 0.0f;
+      top[t][e] = ninf;
+      sum[t][e] = 0.0f;
+    }
   }
-  float top[2] = {ninf, ninf}, sum[2] = {};
 
   const int units = (p.V + 15) / 16, step = gridDim.x * groups;
   int buf = 0;
   for (int first = blockIdx.x * groups; first < units; first += step) {
     __syncwarp();
     const int row0 = (first + grp) * 16;
-    float c[4];
-    if (row0 < p.V) few_logits(p, row0, col0, cols, hp, on, c);
+    float c[NT][4];
+    if (row0 < p.V) few_logits<NT>(p, row0, col0, cols, hp, on, c);
     if (ks > 1) {
-      if (row0 < p.V && slice != 0) shares[buf][warp][lane] = make_float4(c[0], c[1], c[2], c[3]);
+      if (row0 < p.V && slice != 0) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) shares[buf][warp][t][lane] = make_float4(c[t][0], c[t][1], c[t][2], c[t][3]);
+      }
       __syncthreads();
       if (slice == 0 && row0 < p.V) {
         for (int s = 1; s < ks; ++s) {
-          const float4 o = shares[buf][warp + s][lane];
-          c[0] += o.x, c[1] += o.y, c[2] += o.z, c[3] += o.w;
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const float4 o = shares[buf][warp + s][t][lane];
+            c[t][0] += o.x, c[t][1] += o.y, c[t][2] += o.z, c[t][3] += o.w;
+          }
         }
       }
       buf ^= 1;  // this one is free again after the next barrier
@@ -227,24 +253,27 @@ __global__ void __launch_bounds__(kWarps * 32, 2) few_logits_kernel(const FewPar
     for (int half = 0; half < 2; ++half) {
       const int row = row0 + g + 8 * half;
       if (row < p.V) {
-        if constexpr (kGrad) {
-          float d[2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float x = ex2(fmaf(c[2 * half + e], kLog2e, nlse[e])) - (tgt[e] == row ? 1.0f : 0.0f);
-            d[e] = tgt[e] >= 0 ? gain[e] * x : 0.0f;
-          }
-          uint32_t hi, lo;
-          split_pair(d[0], d[1], hi, lo);
-          uint32_t* at = p.dz + static_cast<int64_t>(row) * 8 + q;
-          at[0] = hi;
-          at[4] = lo;
-        } else {
+        for (int t = 0; t < NT; ++t) {
+          if constexpr (kGrad) {
+            float d[2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float z = c[2 * half + e];
-            join(top[e], sum[e], z, 1.0f);
-            if (tgt[e] == row) p.tlogit[2 * q + e].x = z;
+            for (int e = 0; e < 2; ++e) {
+              const float x = ex2(fmaf(c[t][2 * half + e], kLog2e, nlse[t][e])) - (tgt[t][e] == row ? 1.0f : 0.0f);
+              d[e] = tgt[t][e] >= 0 ? gain[t][e] * x : 0.0f;
+            }
+            uint32_t hi, lo;
+            split_pair(d[0], d[1], hi, lo);
+            uint32_t* at = p.dz + (static_cast<int64_t>(row) * NT + t) * 8 + q;
+            at[0] = hi;
+            at[4] = lo;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float z = c[t][2 * half + e];
+              join(top[t][e], sum[t][e], z, 1.0f);
+              if (tgt[t][e] == row) p.tlogit[8 * t + 2 * q + e].x = z;
+            }
           }
         }
       }
@@ -253,14 +282,16 @@ __global__ void __launch_bounds__(kWarps * 32, 2) few_logits_kernel(const FewPar
   if constexpr (!kGrad) {
     // 8 lanes hold rows of the same tokens; then the warps, in order
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int s = 4; s < 32; s *= 2) {
-        const float t2 = __shfl_xor_sync(0xffffffffu, top[e], s), s2 = __shfl_xor_sync(0xffffffffu, sum[e], s);
-        join(top[e], sum[e], t2, s2);
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int s = 4; s < 32; s *= 2) {
+          const float t2 = __shfl_xor_sync(0xffffffffu, top[t][e], s), s2 = __shfl_xor_sync(0xffffffffu, sum[t][e], s);
+          join(top[t][e], sum[t][e], t2, s2);
+        }
+        if (g == 0) pairs[warp][8 * t + 2 * q + e] = make_float2(top[t][e], sum[t][e]);
       }
-      if (g == 0) pairs[warp][2 * q + e] = make_float2(top[e], sum[e]);
-    }
     __syncthreads();
     if (threadIdx.x < p.M) {
       float2 a = make_float2(ninf, 0.0f);
@@ -274,11 +305,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) few_logits_kernel(const FewPar
 }
 
 constexpr int kRing = 4;                     // units in flight per warp
-constexpr int kSlot = 16 * 128 + 16 * 32;    // a unit's 16 rows: 64 columns of W, dz of 8 tokens
-constexpr int kProductsSmem = kWarps * kRing * kSlot;
-static_assert(kProductsSmem >= kWarps * 8 * 65 * 4, "the warps' sums take W's place");
+template <int NT>
+constexpr int kSlot = 16 * 128 + 16 * 32 * NT;  // a unit's 16 rows: 64 columns of W, dz
+template <int NT>
+constexpr int kProductsSmem = kWarps * kRing * kSlot<NT>;
+static_assert(kProductsSmem<1> >= kWarps * 8 * 65 * 4, "the warps' sums take W's place");
 
-template <bool kF32>
+template <int NT, bool kF32>
 __global__ void __launch_bounds__(kWarps * 32, 2) few_products_kernel(const FewParams p) {
   extern __shared__ uint4 ring[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
@@ -286,7 +319,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) few_products_kernel(const FewP
   const bool want_dh = p.dh_part != nullptr;
   const int units = (p.V + 15) / 16, step = gridDim.y * kWarps;
   int u = blockIdx.y * kWarps + warp;
-  const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + warp * kRing * kSlot;
+  const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + warp * kRing * kSlot<NT>;
 
   // W: 8 lanes copy a row's 128 bytes; chunk c of row r lies at place c ^ (r % 8)
   const int lr = lane >> 3, lc = c0 + 8 * (lane & 7);
@@ -297,15 +330,19 @@ __global__ void __launch_bounds__(kWarps * 32, 2) few_products_kernel(const FewP
     for (int i = 0; i < 4; ++i) {
       const int r = lr + 4 * i, row = unit * 16 + r;
       const bool in = want_w && row < p.V;
-      copy16(w_to + slot * kSlot + i * 512 + (((lane & 7) ^ (r & 7)) << 4),
+      copy16(w_to + slot * kSlot<NT> + i * 512 + (((lane & 7) ^ (r & 7)) << 4),
              in ? p.W + static_cast<int64_t>(row) * p.K + lc : p.W, in);
     }
   };
-  // dz: 2 lanes per row
+  // dz: the unit's rows are one piece of memory; 16 bytes per lane and 8 tokens
   auto request_dz = [&](int unit, int slot) {
-    const int row = unit * 16 + (lane >> 1);
-    const bool in = row < p.V;
-    copy16(mine + slot * kSlot + 2048 + lane * 16, in ? p.dz + static_cast<int64_t>(row) * 8 + (lane & 1) * 4 : p.dz, in);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int i = t * 32 + lane;
+      const bool in = unit * 16 + i / (2 * NT) < p.V;
+      copy16(mine + slot * kSlot<NT> + 2048 + i * 16, in ? p.dz + static_cast<int64_t>(unit) * 128 * NT + i * 4 : p.dz,
+             in);
+    }
   };
   // The launch before wrote dz alone, and began after all earlier ones had
   // ended: what this one reads besides dz needs no wait.
@@ -316,16 +353,17 @@ __global__ void __launch_bounds__(kWarps * 32, 2) few_products_kernel(const FewP
   }
   // dW's operand: tokens 2q and 2q + 1 at the column that puts 16 consecutive
   // bytes of the result into one lane, 64 into four
-  uint32_t hp[8];
-  {
-    const int m = 2 * q;
+  uint32_t hp[NT][8];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int m = 8 * t + 2 * q;
     const bool a = counts(p, m), b = counts(p, m + 1);
     const uint16_t* h0 = reinterpret_cast<const uint16_t*>(p.h) + static_cast<int64_t>(m) * p.K;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int c = c0 + (kF32 ? 16 * (j >> 1) + 4 * (g >> 1) + 2 * (j & 1) : 32 * (j >> 2) + 8 * (g >> 1) + 2 * (j & 3)) + (g & 1);
       const uint32_t lo = a && c < p.K ? __ldg(h0 + c) : 0u, hi = b && c < p.K ? __ldg(h0 + p.K + c) : 0u;
-      hp[j] = hi << 16 | lo;
+      hp[t][j] = hi << 16 | lo;
     }
   }
   pdl_wait_primary();
@@ -338,9 +376,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) few_products_kernel(const FewP
   // the rows that this lane names for the tiles: dz as [rows 0-7, 8-15] x [hi, lo];
   // W as [columns 16j + 0-7, 8-15] x [rows 0-7, 8-15]
   const int tr = lane & 7, tile = lane >> 3;
-  const uint32_t dz_at = mine + 2048 + ((tile & 1) * 8 + tr) * 32 + (tile >> 1) * 16;
+  const uint32_t dz_at = mine + 2048 + ((tile & 1) * 8 + tr) * (32 * NT) + (tile >> 1) * 16;
   const uint32_t w_at = mine + ((tile >> 1) * 8 + tr) * 128;
-  float acc[4][4] = {};
+  float acc[NT][4][4] = {};
   for (int slot = 0; u < units; u += step, slot = slot + 1 < kRing ? slot + 1 : 0) {
     const int row0 = u * 16;
     asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
@@ -351,26 +389,35 @@ __global__ void __launch_bounds__(kWarps * 32, 2) few_products_kernel(const FewP
       request_dz(ahead, to);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    uint32_t d[4];
-    ldmatrix4<false>(d, dz_at + slot * kSlot);
     if (want_dh) {
-      uint32_t t[4];  // hi of rows 0-7 and 8-15, then lo
-      ldmatrix4<true>(t, dz_at + slot * kSlot);
+      uint32_t w[4][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t w[4];
-        ldmatrix4<true>(w, w_at + slot * kSlot + (((2 * j + (tile & 1)) ^ tr) << 4));
-        mma16816(acc[j], w[0], w[1], w[2], w[3], t[2], t[3]);
-        mma16816(acc[j], w[0], w[1], w[2], w[3], t[0], t[1]);
+      for (int j = 0; j < 4; ++j)
+        ldmatrix4<true>(w[j], w_at + slot * kSlot<NT> + (((2 * j + (tile & 1)) ^ tr) << 4));
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        uint32_t d[4];  // hi of rows 0-7 and 8-15, then lo
+        ldmatrix4<true>(d, dz_at + slot * kSlot<NT> + 32 * t);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          mma16816(acc[t][j], w[j][0], w[j][1], w[j][2], w[j][3], d[2], d[3]);
+          mma16816(acc[t][j], w[j][0], w[j][1], w[j][2], w[j][3], d[0], d[1]);
+        }
       }
     }
     if (p.dW) {
+      uint32_t d[NT][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) ldmatrix4<false>(d[t], dz_at + slot * kSlot<NT> + 32 * t);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         __syncwarp();
         float o[4][4] = {};  // [pair of columns][row g: 2, row g + 8: 2]
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma16816(o[j], d[0], d[1], d[2], d[3], hp[4 * s + j], hp[4 * s + j]);
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma16816(o[j], d[t][0], d[t][1], d[t][2], d[t][3], hp[t][4 * s + j], hp[t][4 * s + j]);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int row = row0 + g + 8 * half;
@@ -414,18 +461,21 @@ __global__ void __launch_bounds__(kWarps * 32, 2) few_products_kernel(const FewP
   // the block's warps joined in order, where W was
   float(*joint)[8][65] = reinterpret_cast<float(*)[8][65]>(ring);
   asm volatile("cp.async.wait_group 0;" ::: "memory");
-  __syncthreads();
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int t = 0; t < NT; ++t) {
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) joint[warp][2 * q + (i & 1)][16 * j + g + 8 * (i >> 1)] = acc[j][i];
-  __syncthreads();
-  for (int i = threadIdx.x; i < 8 * 64; i += kWarps * 32) {
-    const int m = i >> 6, c = i & 63;
-    float s = 0.0f;
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += joint[w][m][c];
-    if (m < p.M && c0 + c < p.K) p.dh_part[(static_cast<int64_t>(blockIdx.y) * p.M + m) * p.K + c0 + c] = s;
+      for (int i = 0; i < 4; ++i) joint[warp][2 * q + (i & 1)][16 * j + g + 8 * (i >> 1)] = acc[t][j][i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 8 * 64; i += kWarps * 32) {
+      const int m = 8 * t + (i >> 6), c = i & 63;
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) s += joint[w][i >> 6][c];
+      if (m < p.M && c0 + c < p.K) p.dh_part[(static_cast<int64_t>(blockIdx.y) * p.M + m) * p.K + c0 + c] = s;
+    }
   }
 }
 
@@ -480,7 +530,9 @@ int few_row_blocks(int64_t V, int64_t K) {
   return static_cast<int>(warps < most ? warps : most);
 }
 
-size_t few_dz_bytes(int64_t V) { return static_cast<size_t>(V) * 32; }
+int few_groups(int64_t M) { return M <= 8 ? 1 : 2; }  // of 8 tokens: the kernels' NT
+
+size_t few_dz_bytes(int64_t M, int64_t V) { return static_cast<size_t>(V) * 32 * few_groups(M); }
 
 FewParams few_params(const void* h, const void* W, const int64_t* targets, int64_t M, int64_t V, int64_t K) {
   FewParams p{};
@@ -496,32 +548,39 @@ FewParams few_params(const void* h, const void* W, const int64_t* targets, int64
 
 template <bool kGrad>
 cudaError_t launch_logits(const FewParams& p, cudaStream_t s) {
-  return launch_pdl(few_logits_kernel<kGrad>, dim3(few_blocks(p.V, p.K)), dim3(kWarps * 32), 0, s, p);
+  const dim3 grid(few_blocks(p.V, p.K)), block(kWarps * 32);
+  return few_groups(p.M) == 1 ? launch_pdl(few_logits_kernel<1, kGrad>, grid, block, 0, s, p)
+                              : launch_pdl(few_logits_kernel<2, kGrad>, grid, block, 0, s, p);
 }
 
-template <bool kF32>
+template <int NT, bool kF32>
 cudaError_t launch_products(const FewParams& p, int row_blocks, cudaStream_t s) {
   static bool done[64] = {};  // per device: the kernel's shared memory is set
   int dev = 0;
   if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
   if (dev >= 64 || !done[dev]) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(few_products_kernel<kF32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kProductsSmem);
+    const cudaError_t e = cudaFuncSetAttribute(few_products_kernel<NT, kF32>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kProductsSmem<NT>);
     if (e != cudaSuccess) return e;
     if (dev < 64) done[dev] = true;
   }
-  return launch_pdl(few_products_kernel<kF32>, dim3(static_cast<unsigned>(ceil_div(p.K, 64)), row_blocks),
-                    dim3(kWarps * 32), kProductsSmem, s, p);
+  return launch_pdl(few_products_kernel<NT, kF32>, dim3(static_cast<unsigned>(ceil_div(p.K, 64)), row_blocks),
+                    dim3(kWarps * 32), kProductsSmem<NT>, s, p);
+}
+
+template <bool kF32>
+cudaError_t launch_products(const FewParams& p, int row_blocks, cudaStream_t s) {
+  return few_groups(p.M) == 1 ? launch_products<1, kF32>(p, row_blocks, s) : launch_products<2, kF32>(p, row_blocks, s);
 }
 
 }  // namespace
 
-bool xent_few(int64_t M) { return M <= 8; }
+bool xent_few(int64_t M) { return M <= 16; }
 
 int xent_few_parts(int64_t V, int64_t K) { return few_blocks(V, K); }
 
 size_t xent_few_workspace_bytes(int64_t M, int64_t V, int64_t K) {
-  return few_dz_bytes(V) + static_cast<size_t>(few_row_blocks(V, K)) * M * K * 4;
+  return few_dz_bytes(M, V) + static_cast<size_t>(few_row_blocks(V, K)) * M * K * 4;
 }
 
 cudaError_t launch_xent_few_forward(const void* h, const void* W, const int64_t* targets, int64_t M, int64_t V,
@@ -539,7 +598,7 @@ cudaError_t launch_xent_few_backward(const void* h, const void* W, const int64_t
   p.lse = lse;
   p.dloss = dloss;
   p.dz = static_cast<uint32_t*>(workspace);
-  float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + few_dz_bytes(V));
+  float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + few_dz_bytes(M, V));
   p.dh_part = dH ? parts : nullptr;
   p.dW = dW;
   p.w_add = accumulate;

@@ -272,7 +272,7 @@ def test_other_stream_and_graphs_sharing_a_workspace(M):
     assert bl.bl_get_last_error() == 0
 
 
-@pytest.mark.parametrize("M", [3, 9])
+@pytest.mark.parametrize("M", [3, 9, 18])
 def test_weight_offsets_past_32_bits(M):
     """A head of more than 2^31 weights: loss, lse and the gradients' last rows
     against 64-bit sums over blocks of the vocabulary."""
@@ -361,12 +361,12 @@ def test_refused_on_the_gpu():
     assert bl.bl_get_last_error() == 0
 
 
-# a few tokens: their own kernels, by groups of 8 tokens, units of 16 rows of W,
+# a few tokens: their own kernels, by one or two groups of 8 tokens, units of 16 rows of W,
 # steps of 32 columns (128 at once) and tiles of 64; a vocabulary of less than
 # one unit, and one whose units are dealt out unevenly
 FEW = [(1, 5, 8), (1, 33, 2048), (2, 31, 2056), (3, 129, 4088), (4, 4737, 4096), (4, 20001, 512), (5, 4, 2048), (5, 1, 8), (6, 9473, 520),
        (7, 40000, 16), (8, 3, 2040), (8, 1000, 2048), (8, 66000, 72), (5, 700, 2056), (8, 300, 4096), (9, 700, 512), (4, 300, 4104),
-       (16, 1009, 136), (17, 1009, 136), (25, 15, 264), (32, 17, 8192), (32, 40001, 160), (11, 1, 65536), (7, 1, 65536), (8, 40, 65536), (2, 600, 32768), (1, 37889, 24), (33, 500, 264)]
+       (16, 1009, 136), (17, 1009, 136), (25, 15, 264), (32, 17, 8192), (32, 40001, 160), (11, 1, 65536), (7, 1, 65536), (8, 40, 65536), (2, 600, 32768), (1, 37889, 24), (33, 500, 264), (9, 31, 8), (15, 4000, 8184), (16, 66001, 88), (12, 17, 65536), (10, 9473, 520)]
 
 
 @pytest.mark.parametrize("dw_dtype", [BF, F32])
