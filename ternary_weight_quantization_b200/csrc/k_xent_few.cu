@@ -1,8 +1,8 @@
 // The head cross-entropy for a few tokens (X1, X2 with up to 16 tokens): a
 // handful of tokens leaves the tensor-core tiles of 256 empty, and what counts
 // is how fast W streams through. Here the rows of W are the 16-row operand of
-// mma.sync and 8 or twice 8 tokens its columns; W goes from global memory to the
-// operands' registers without shared memory in between.
+// mma.sync and 8 or twice 8 tokens its columns; for the logits W goes from global
+// memory to the operands' registers without shared memory in between.
 //
 //   logits    a warp takes 16 rows of W. The sum over K may take its terms in
 //             any order, so a lane's 16 bytes of a row (8 consecutive values)
