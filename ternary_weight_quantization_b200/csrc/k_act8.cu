@@ -294,6 +294,12 @@ template <What what, typename T, bool kVec, int kU>
 cudaError_t launch_one(const Act8Args& p, cudaStream_t s) {
   const int64_t per = static_cast<int64_t>(kThreads / Act8Lane<kVec>::W) * kU;
   const int64_t want = (p.units + per - 1) / per;
+  // less than a block per SM: one unit per thread on more SMs (600 x 1000 bf16 in
+  // 1.7 and 1.6 us for 2.4 and 1.9, A1 and A2 with 4; at 1200 x 1024 4 per thread
+  // take 2.2 and 1.9)
+  if constexpr (kU > 1) {
+    if (want <= 148) return launch_one<what, T, kVec, 1>(p, s);
+  }
   constexpr int64_t kMaxGrid = 1 << 20;
   return launch_pdl(act8_kernel<what, T, kVec, kU>, dim3(static_cast<unsigned>(want < kMaxGrid ? want : kMaxGrid)),
                     dim3(kThreads), 0, s, p);
