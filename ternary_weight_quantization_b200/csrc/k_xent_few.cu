@@ -28,8 +28,9 @@
 // 5.6 / 11.3 (8.2 / 19.3). 5 tokens, 68159 x 72: 7.4 / 16.5 (16.0 / 35.8).
 // 16 tokens, 8192 x 512: 7.2 / 14.9 (8.1 / 19.2); 2000 x 1000: 6.1 / 12.3 (10.3 /
 // 18.8); 32000 x 2560: 34.6 / 106 (35.5 / 105), with an fp32 dW 136 (134). With four
-// groups 32 tokens, 8192 x 512 took 11.6 / 30.5 (8.4 / 19.6): the reads of h outgrow
-// L1, and the tiles take over above 16.
+// groups 32 tokens, 8192 x 512 took 11.6 / 30.5 (8.4 / 19.6): the instructions grow
+// with the tokens, and their sums leave registers for one block per SM. Above 16
+// the tiles take over.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
