@@ -399,7 +399,9 @@ bl_status bl_linear_xent_forward(const void* h, const void* W, const int64_t* ta
  * its row of dH is 0 and it adds nothing to dW. M == 0 writes dW = 0 (leaves
  * it as it is with accumulate_dW).
  * workspace: at least bl_linear_xent_backward_workspace_size(M,V,K,dw_dtype)
- * bytes, otherwise as X1's; X1's workspace may be the same memory.
+ * bytes, otherwise as X1's; X1's workspace may be the same memory. Without dW
+ * either dw_dtype will do; the size for BL_F32 is never below the one for
+ * BL_BF16.
  * Limits and errors: as X1, plus BL_ERR_DTYPE.
  */
 size_t bl_linear_xent_backward_workspace_size(int64_t M, int64_t V, int64_t K, bl_dtype dw_dtype);

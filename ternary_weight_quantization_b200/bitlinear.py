@@ -435,7 +435,8 @@ def bl_linear_xent_forward(h, W, targets, loss, lse, workspace, stream=None):
 def bl_linear_xent_backward(h, W, targets, lse, dloss, dH=None, dW=None, workspace=None, accumulate_dW=False,
                             stream=None):
     """X2: dH [M,K] bf16 and dW [V,K] (bf16|f32) of X1 (each may be None), given
-    dloss [M] f32, the gradient of each token's loss, and X1's lse."""
+    dloss [M] f32, the gradient of each token's loss, and X1's lse. Without dW a
+    workspace sized for either type of dW will do."""
     status = _quick().xent_backward(h, W, targets, lse, dloss, dH, dW, workspace, accumulate_dW, stream)
     if status is not None:
         return _check(status, "bl_linear_xent_backward")

@@ -1,0 +1,58 @@
+"""GPU: calls of the training operators that their documentation allows, in the
+shapes, buffers and views that a training loop brings them."""
+
+import pytest
+import torch
+
+import ternary_weight_quantization_b200 as bl
+from ternary_weight_quantization_b200 import lm as plm
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def rnd(*shape, seed=0, dtype=F32, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def targets(M, V, seed=0):
+    return torch.randint(-1, V, (M,), generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")
+
+
+def ok():
+    torch.cuda.synchronize()
+    assert bl.bl_get_last_error() == 0
+
+
+# ----------------------------------------------------------------- head cross-entropy: workspaces
+@pytest.mark.parametrize("M,V,K", [(391, 1739, 3312), (30, 8192, 512), (140, 700, 136), (9, 700, 136)])
+def test_dh_alone_with_the_buffers_of_an_fp32_dw(M, V, K):
+    h, W, t, dl = rnd(M, K, dtype=BF), rnd(V, K, seed=1, dtype=BF, scale=0.02), targets(M, V), torch.full((M,), 0.01, device="cuda")
+    b = bl.XentBuffers.allocate(M, V, K, F32)
+    bl.bl_linear_xent_forward(h, W, t, b.loss, b.lse, b.workspace)
+    bl.bl_linear_xent_backward(h, W, t, b.lse, dl, b.dH, None, b.workspace)
+    ok()
+    z = h.double() @ W.double().t()
+    dz = torch.softmax(z, 1)
+    dz[torch.arange(M, device="cuda"), t.clamp(min=0)] -= 1
+    dz = torch.where((t >= 0)[:, None], dz * dl.double()[:, None], 0.0)
+    want, mag = dz @ W.double(), dz.abs() @ W.double().abs()
+    # dz and dH rounded to bf16 (2^-8 each, at most); a tensor-core sum drops up
+    # to a step of fp32 per 16 terms: of the logits (an error of p's exponent)
+    # and of dH
+    e = (K / 16 + 16) * 2.0 ** -23 * float((h.double().abs() @ W.double().abs().t()).amax())
+    tol = (2.0 ** -8 + 2 * e + (V / 16 + 64) * 2.0 ** -23) * mag
+    assert bool(((b.dH.double() - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol) + 1e-36).all())
+
+
+def test_frozen_head():
+    """The loss's gradient for h alone, as when the head is not trained."""
+    M, V, K = 391, 1739, 3312
+    h, W, t = rnd(M, K).requires_grad_(True), rnd(V, K, seed=1, scale=0.02), targets(M, V)
+    dh, = torch.autograd.grad(plm.HeadLossFunction.apply(h, W, t), [h])
+    both = torch.autograd.grad(plm.HeadLossFunction.apply(h, W.requires_grad_(True), t), [h, W])
+    ok()
+    # dz goes to dH in bf16 either way; the order of dH's partial sums differs
+    assert float((dh - both[0]).norm()) <= 2.0 ** -8 * float(both[0].norm())
+    assert bool(both[1].any())
