@@ -364,8 +364,8 @@ bl_status bl_signsgd_apply(const uint32_t* sign_words, int ranks, void* W, bl_dt
  * workspace: at least bl_linear_xent_forward_workspace_size(M,V,K) bytes,
  * 16-byte aligned, no initialisation, one call at a time per workspace: one
  * (maximum, sum) pair per token and 64 or more vocabulary entries (few tokens:
- * 16 or more), never the logits. The sizes of X1 and X2 are for the call's own
- * shape: fewer tokens may need more (a short last batch asks for its own).
+ * 16 or more), never the logits. The sizes of X1 and X2 never shrink as M
+ * grows: a workspace for M tokens serves calls of fewer with the same V and K.
  * Limits: K a multiple of 8 up to 65536, M up to 131072, V up to 2^24.
  * M == 0 is a no-op (the workspace size is then 0).
  * Errors: BL_ERR_INVALID_ARG, BL_ERR_UNSUPPORTED_SHAPE, BL_ERR_ALIGNMENT,

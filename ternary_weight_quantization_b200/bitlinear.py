@@ -582,8 +582,8 @@ def bl_swiglu_backward(dy, gate8: Act8, up8: Act8, dgate, dup, stream=None):
 @dataclass
 class XentBuffers:
     """Device buffers of X1 and (backward) X2 (caller-owned, reused); one
-    workspace serves both calls, in either order on one stream. For calls of M
-    tokens: fewer may need a larger workspace."""
+    workspace serves both calls, in either order on one stream. A call of fewer
+    tokens takes their first rows and the same workspace and dW."""
     loss: torch.Tensor
     lse: torch.Tensor
     workspace: torch.Tensor

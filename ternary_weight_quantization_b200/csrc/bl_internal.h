@@ -122,7 +122,8 @@ cudaError_t launch_xent_backward(const void* h, const void* W, const int64_t* ta
 // The same for a few tokens (k_xent_few.cu): whether it takes the call; the
 // forward leaves xent_few_parts (maximum, sum) pairs per token, [part][M], and
 // the tensor cores' logits of the targets (x of a pair).
-bool xent_few(int64_t M);
+constexpr int64_t kXentFew = 16;
+inline bool xent_few(int64_t M) { return M <= kXentFew; }
 int xent_few_parts(int64_t V, int64_t K);
 size_t xent_few_workspace_bytes(int64_t M, int64_t V, int64_t K);
 cudaError_t launch_xent_few_forward(const void* h, const void* W, const int64_t* targets, int64_t M, int64_t V,

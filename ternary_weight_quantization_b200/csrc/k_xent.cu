@@ -1013,20 +1013,55 @@ static int logit_parts(int64_t M, int64_t V) {
   return 2 * static_cast<int>((V + bn - 1) / bn);
 }
 
-size_t xent_forward_workspace_bytes(int64_t M, int64_t V, int64_t K) {
-  const int parts = xent_few(M) ? xent_few_parts(V, K) : logit_parts(M, V);
+static size_t forward_bytes(int64_t M, int64_t parts) {
   return align256(static_cast<size_t>(parts) * M * 8) + align256(static_cast<size_t>(M) * 8);
 }
 
+// The workspaces never shrink as tokens are added, so that a loop's buffers
+// serve its short last batch. The forward's bytes grow with the tokens except
+// where the few tokens' kernels end and where the tiles turn from 128 to 256
+// columns: the larger of the values just before those and of the call's own.
+size_t xent_forward_workspace_bytes(int64_t M, int64_t V, int64_t K) {
+  const int64_t few = M < kXentFew ? M : kXentFew;
+  size_t most = forward_bytes(few, xent_few_parts(V, K));
+  if (few == M) return most;
+  const int64_t narrow = 74 / ((V + 127) / 128) * kTile;  // the most tokens with 128 columns
+  for (const int64_t m : {M, narrow < M ? narrow : M}) {
+    const size_t n = m > few ? forward_bytes(m, logit_parts(m, V)) : 0;
+    if (n > most) most = n;
+  }
+  return most;
+}
+
+// A bound on the plan's bytes for up to M tokens, for either type of dW where
+// that is fp32 (a call for dH alone plans as for bf16).
+//   dz     a piece holds at most kPieceBytes, or 256 columns; at most the
+//          whole vocabulary
+//   sums   make_plan's slices are ceil(3 nkb / (2 share)) with share >=
+//          tiles nkb / 74, so at most ceil(111 / tiles) (and 32, and nkb); a
+//          single slice takes sums only where the vocabulary is in pieces,
+//          which more tokens (or bytes per entry) never undo
+// Each part only grows with M and with the bytes per entry. At most 64 MiB of
+// dz and about 30 MB of sums are more than the plan itself lays out (2048
+// tokens, K 512, V 8192: 67 MB for 48; 4096, 2560, 32000: 197 for 195).
 size_t xent_backward_workspace_bytes(int64_t M, int64_t V, int64_t K, int dw_is_f32) {
   if (xent_few(M)) return xent_few_workspace_bytes(M, V, K);
-  // an fp32 buffer also serves a call for dH alone, which plans as for bf16:
-  // wider pieces, and with them more slices of dH, can ask for more (391
-  // tokens, V 1739, K 3312: 17.6 MB next to 5.4)
-  const size_t half = make_plan(M, V, K, false).bytes;
-  if (!dw_is_f32) return half;
-  const size_t own = make_plan(M, V, K, true).bytes;
-  return own > half ? own : half;
+  const int64_t per = dw_is_f32 ? 4 : 2, all = (V + kTile - 1) / kTile * kTile;
+  const int64_t piece = kPieceBytes > M * kTile * per ? kPieceBytes : M * kTile * per;
+  const int64_t whole = M * all * per;
+  const int64_t tm = tiles_of(M), tk = tiles_of(K), nkb = (V + kBlockR - 1) / kBlockR;
+  const bool pieces = make_plan(M, V, K, dw_is_f32 != 0).pieces > 1;
+  int64_t rows = pieces ? tm : 0;  // of dH's partial sums, in tiles
+  for (int64_t m = 1; m <= tm && m * tk < 74; ++m) {
+    int64_t slices = (111 + m * tk - 1) / (m * tk);
+    slices = slices > 32 ? 32 : slices;
+    slices = slices > nkb ? nkb : slices;
+    if (slices > 1 && m * slices > rows) rows = m * slices;
+  }
+  const size_t bytes = align256(static_cast<size_t>(whole < piece ? whole : piece)) +
+                       align256(static_cast<size_t>(M) * K * 2) + 256 + static_cast<size_t>(rows) * kTile * K * 4;
+  const size_t few = xent_few_workspace_bytes(kXentFew, V, K);
+  return bytes > few ? bytes : few;
 }
 
 cudaError_t launch_xent_forward(const void* h, const void* W, const int64_t* targets, int64_t M, int64_t V, int64_t K,

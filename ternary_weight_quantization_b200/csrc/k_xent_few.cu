@@ -576,8 +576,6 @@ cudaError_t launch_products(const FewParams& p, int row_blocks, cudaStream_t s) 
 
 }  // namespace
 
-bool xent_few(int64_t M) { return M <= 16; }
-
 int xent_few_parts(int64_t V, int64_t K) { return few_blocks(V, K); }
 
 size_t xent_few_workspace_bytes(int64_t M, int64_t V, int64_t K) {

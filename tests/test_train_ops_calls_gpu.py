@@ -56,3 +56,16 @@ def test_frozen_head():
     # dz goes to dH in bf16 either way; the order of dH's partial sums differs
     assert float((dh - both[0]).norm()) <= 2.0 ** -8 * float(both[0].norm())
     assert bool(both[1].any())
+
+
+@pytest.mark.parametrize("M,short,V,K,dt", [(2048, 1310, 50257, 768, BF), (257, 256, 8192, 512, F32), (40, 9, 5000, 264, BF)])
+def test_short_batch_in_the_buffers_of_a_whole_one(M, short, V, K, dt):
+    h, W, t, dl = rnd(M, K, dtype=BF), rnd(V, K, seed=1, dtype=BF, scale=0.02), targets(M, V), torch.full((M,), 0.01, device="cuda")
+    b, own = bl.XentBuffers.allocate(M, V, K, dt), bl.XentBuffers.allocate(short, V, K, dt)
+    n = short
+    for x in (b, own):
+        bl.bl_linear_xent_forward(h[:n], W, t[:n], x.loss[:n], x.lse[:n], x.workspace)
+        bl.bl_linear_xent_backward(h[:n], W, t[:n], x.lse[:n], dl[:n], x.dH[:n], x.dW, x.workspace)
+    ok()
+    assert torch.equal(b.loss[:n], own.loss) and torch.equal(b.lse[:n], own.lse)
+    assert torch.equal(b.dH[:n], own.dH) and torch.equal(b.dW, own.dW) and bool(own.dW.isfinite().all())
