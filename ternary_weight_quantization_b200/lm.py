@@ -107,6 +107,14 @@ class BitLinearFunction(torch.autograd.Function):
         return dX.to(ctx.out_dtype), dW.to(ctx.w_dtype)
 
 
+def _operand(t: torch.Tensor) -> torch.Tensor:
+    """t as the training operators take it: contiguous and on a 16-byte
+    boundary. A view may start anywhere in its storage (the targets of a batch
+    of one sequence are its ids from the second on)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class RMSNormFunction(torch.autograd.Function):
     """y [M, K] = RMS norm of x [M, K] with gain weight [K]; x is kept for the
     backward as it is, or (saved8) in 8 bits."""
@@ -114,7 +122,7 @@ class RMSNormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, eps, saved8):
         M, K = x.shape
-        x, weight = x.contiguous(), weight.contiguous()
+        x, weight = _operand(x), _operand(weight)
         y = torch.empty_like(x)
         rstd = torch.empty(M, dtype=torch.float32, device=x.device)
         keep = b.Act8.allocate(M, K, x.device) if saved8 else None
@@ -128,7 +136,7 @@ class RMSNormFunction(torch.autograd.Function):
     def backward(ctx, gy):
         weight, rstd, *kept = ctx.saved_tensors
         x = b.Act8(*kept) if ctx.saved8 else kept[0]
-        gy = gy.contiguous()
+        gy = _operand(gy)
         dx, dweight = torch.empty_like(gy), torch.empty_like(weight)
         ws = torch.empty(max(b.bl_norm_backward_workspace_size(*gy.shape), 16), dtype=torch.uint8, device=gy.device)
         b.bl_norm_backward(gy, x, weight, None, rstd, dx, dweight, None, ws, rms=True)
@@ -142,7 +150,7 @@ class SwigluFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, gate, up):
-        g, u = gate.to(torch.bfloat16).contiguous(), up.to(torch.bfloat16).contiguous()
+        g, u = _operand(gate.to(torch.bfloat16)), _operand(up.to(torch.bfloat16))
         y = torch.empty_like(g)
         g8, u8 = b.Act8.allocate(*g.shape, g.device), b.Act8.allocate(*g.shape, g.device)
         b.bl_swiglu_forward(g, u, y, g8, u8)
@@ -153,7 +161,7 @@ class SwigluFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, gy):
         gc, gs, uc, us = ctx.saved_tensors
-        dy = gy.to(torch.bfloat16).contiguous()
+        dy = _operand(gy.to(torch.bfloat16))
         dgate, dup = torch.empty_like(dy), torch.empty_like(dy)
         b.bl_swiglu_backward(dy, b.Act8(gc, gs), b.Act8(uc, us), dgate, dup)
         return dgate.to(gy.dtype), dup.to(gy.dtype)
@@ -166,8 +174,8 @@ class HeadLossFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, h, head, targets):
         (M, K), V = h.shape, head.shape[0]
-        hb, wb = h.to(torch.bfloat16).contiguous(), head.to(torch.bfloat16).contiguous()
-        targets = targets.contiguous()
+        hb, wb = _operand(h.to(torch.bfloat16)), _operand(head.to(torch.bfloat16))
+        targets = _operand(targets)
         buf = b.XentBuffers.allocate(M, V, K, backward=False, device=h.device)
         b.bl_linear_xent_forward(hb, wb, targets, buf.loss, buf.lse, buf.workspace)
         share = ((targets >= 0) & (targets < V)).sum().clamp(min=1).to(torch.float32).reciprocal()

@@ -69,3 +69,51 @@ def test_short_batch_in_the_buffers_of_a_whole_one(M, short, V, K, dt):
     ok()
     assert torch.equal(b.loss[:n], own.loss) and torch.equal(b.lse[:n], own.lse)
     assert torch.equal(b.dH[:n], own.dH) and torch.equal(b.dW, own.dW) and bool(own.dW.isfinite().all())
+
+
+# ----------------------------------------------------------------- the LM's functions
+def off(t, n=1):
+    """The same values n elements into a larger storage."""
+    x = torch.empty(t.numel() + n, dtype=t.dtype, device=t.device)[n:].view(t.shape)
+    return x.copy_(t)
+
+
+def test_views_that_start_off_a_16_byte_boundary():
+    """Inputs and gradients that are views into other tensors give what their
+    copies give."""
+    M, K, V = 6, 40, 100
+    x, w, up, gy = rnd(M, K), rnd(K, seed=1), rnd(M, K, seed=2), rnd(M, K, seed=3)
+    head, t = rnd(V, K, seed=4, scale=0.1), targets(M, V)
+    calls = {
+        "norm": (lambda a, b: plm.RMSNormFunction.apply(a, b, 1e-6, False), (x, w), gy),
+        "norm saved8": (lambda a, b: plm.RMSNormFunction.apply(a, b, 1e-6, True), (x, w), gy),
+        "gate": (plm.SwigluFunction.apply, (x, up), gy),
+        "gate bf16": (plm.SwigluFunction.apply, (x.to(BF), up.to(BF)), gy.to(BF)),
+    }
+    for name, (call, args, g) in calls.items():
+        want, got = ([a.clone().requires_grad_(True) for a in args] for _ in range(2))
+        got = [off(a.detach()).requires_grad_(True) for a in got]
+        yw, yg = call(*want), call(*got)
+        assert off(g).data_ptr() % 16 and got[0].data_ptr() % 16
+        pairs = zip([yw, *torch.autograd.grad(yw, want, g)], [yg, *torch.autograd.grad(yg, got, off(g))])
+        assert all(torch.equal(a, b) for a, b in pairs), name
+    for dt in (F32, BF):
+        h1, w1 = x.to(dt).requires_grad_(True), head.to(dt).requires_grad_(True)
+        h2, w2 = off(x.to(dt)).requires_grad_(True), off(head.to(dt)).requires_grad_(True)
+        a, b = plm.HeadLossFunction.apply(h1, w1, t), plm.HeadLossFunction.apply(h2, w2, off(t))
+        pairs = zip([a, *torch.autograd.grad(a, [h1, w1])], [b, *torch.autograd.grad(b, [h2, w2])])
+        assert all(torch.equal(p, q) for p, q in pairs), dt
+    ok()
+
+
+def test_batch_of_one_sequence():
+    """One sequence: its targets are a view that starts 8 bytes into the ids."""
+    from workloads.lm import LM_TINY, lm_batches, lm_init
+    params = {n: p.cuda().requires_grad_(True) for n, p in lm_init(LM_TINY, seed=1).items()}
+    ids = lm_batches(LM_TINY, seed=1)[0].cuda()
+    one = plm.lm_loss(params, ids[:1], LM_TINY, library_ops=True)
+    assert all(bool(g.isfinite().all()) for g in torch.autograd.grad(one, list(params.values())))
+    # a zero head: every probability is 1 / V, exactly in fp32 up to the log
+    import math
+    assert abs(float(one.detach()) - math.log(LM_TINY.vocab)) <= 16 * 2.0 ** -23 * math.log(LM_TINY.vocab)
+    ok()
