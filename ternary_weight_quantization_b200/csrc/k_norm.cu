@@ -119,8 +119,8 @@ __device__ __forceinline__ float rsqrt_of(float v) {
   return v > 0.0f && v < __uint_as_float(0x7F800000u) ? fmaf(0.5f * r, e, r) : r;
 }
 
-// The same for two values, whose buffer (8 bytes per warp) is given by its
-// shared-memory address.
+// The same for two values, whose buffer (a float2 per warp: 8-byte accesses) is
+// given by its shared-memory address.
 __device__ __forceinline__ void group_sum2(float (&v)[2], uint32_t buf, int t, int tpr, int barrier) {
   v[0] = warp_sum(v[0]);
   v[1] = warp_sum(v[1]);
@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_backward_kernel(const Nor
   pdl_wait_primary();
   pdl_launch_dependents();
   extern __shared__ uint4 ring[];  // the rows in flight; afterwards the groups' sums
-  __shared__ float sums[2][kBwdThreads / 32 * 2];
+  __shared__ float2 sums[2][kBwdThreads / 32];
   using Ring = RowRing<T, kSaved>;
   constexpr int kDepth = kBwdDepth<T>;
   const int tpr = p.tpr, K = p.K;
@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_backward_kernel(const Nor
   auto live = [&](int j) { return kFull || c0 + j * cs < K; };
   const uint32_t stride = blockDim.x * 16, row_stride = kBwdVecs * Ring::kPieces * stride;
   const uint32_t mine = smem_u32(ring) + threadIdx.x * 16, end = mine + kDepth * row_stride;
-  uint32_t buf = smem_u32(sums[0] + grp * (tpr >> 5) * 2);
+  uint32_t buf = smem_u32(sums[0] + grp * (tpr >> 5));
   const uint32_t bufs = buf ^ (buf + static_cast<uint32_t>(sizeof(sums[0])));
   const int64_t first = static_cast<int64_t>(blockIdx.x) * ngrp + grp;
   const int64_t step = static_cast<int64_t>(gridDim.x) * ngrp, step_k = step * K;
@@ -738,11 +738,11 @@ __global__ void __launch_bounds__(1024, 1) norm_backward_scalar_kernel(const Nor
   pdl_wait_primary();
   pdl_launch_dependents();
   extern __shared__ uint4 ring[];  // the groups' sums
-  __shared__ float sums[2][32 * 2];
+  __shared__ float2 sums[2][32];
   const int tpr = p.tpr, K = p.K;
   const int ngrp = blockDim.x / tpr;
   const int grp = threadIdx.x / tpr, t = threadIdx.x % tpr;
-  const uint32_t sum0 = smem_u32(sums[0] + grp * (tpr >> 5) * 2);
+  const uint32_t sum0 = smem_u32(sums[0] + grp * (tpr >> 5));
   f32x2 w[4], dw[4] = {}, db[4] = {};
   load_weights<false>(p, t, tpr, w);
   int par = 0;
