@@ -144,18 +144,41 @@ __device__ __forceinline__ void store_codes(const float (&v)[4], const Act8Scale
   if (l == 0 && u.len > 0) scales[idx] = s.scale;
 }
 
-// 1 / (1 + exp(-g)). For bf16 results the hardware's approximations (a few
-// fp32 ulp) are far below the rounding to 8 bits; fp32 results take expf and
-// the rounded division.
+// 1 / (1 + exp(-g)); for bf16 results by way of 2^24 times it (kSigmoidUnit puts
+// the factor back: powers of two, so no bit of a normal value changes). For those
+// the hardware's approximations (a few fp32 ulp) are far below the rounding to
+// 8 bits, but its reciprocal flushes what is below 2^-126 to zero: from g =
+// -87.4 to -88.7, where 1 + exp(-g) is still finite, a large `up` or dy makes
+// that visible. fp32 results take expf and the rounded division.
+constexpr float kSigmoidUnit = 1.0f / 16777216.0f;
+__device__ __forceinline__ float ex2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 template <typename T>
 __device__ __forceinline__ float sigmoid(float g) {
-  if constexpr (sizeof(T) == 2) {
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-    return r;
-  } else {
+  if constexpr (sizeof(T) == 2)
+    return rcp_fast(fmaf(ex2_fast(g * -1.4426950408889634f), kSigmoidUnit, kSigmoidUnit)) * kSigmoidUnit;
+  else
     return __fdiv_rn(1.0f, 1.0f + expf(-g));
+}
+template <typename T>
+__device__ __forceinline__ f32x2 sigmoid(f32x2 g) {
+  float a, b;
+  if constexpr (sizeof(T) == 2) {
+    const f32x2 unit = both2(kSigmoidUnit);
+    split2(mul2(g, both2(-1.4426950408889634f)), a, b);
+    split2(fma2(pair2(ex2_fast(a), ex2_fast(b)), unit, unit), a, b);
+    return mul2(pair2(rcp_fast(a), rcp_fast(b)), unit);
+  } else {
+    split2(g, a, b);
+    return pair2(sigmoid<T>(a), sigmoid<T>(b));
   }
 }
 
@@ -166,9 +189,7 @@ __device__ __forceinline__ void gate_forward(float g, float u, float& y) {
 }
 template <typename T>
 __device__ __forceinline__ void gate_forward(f32x2 g, f32x2 u, f32x2& y) {
-  float a, b;
-  split2(g, a, b);
-  y = mul2(mul2(g, pair2(sigmoid<T>(a), sigmoid<T>(b))), u);
+  y = mul2(mul2(g, sigmoid<T>(g)), u);
 }
 template <typename T>
 __device__ __forceinline__ void gate_backward(float d, float g, float u, float& dg, float& du) {
@@ -178,10 +199,8 @@ __device__ __forceinline__ void gate_backward(float d, float g, float u, float& 
 }
 template <typename T>
 __device__ __forceinline__ void gate_backward(f32x2 d, f32x2 g, f32x2 u, f32x2& dg, f32x2& du) {
-  float a, b;
-  split2(g, a, b);
   const f32x2 one = both2(1.0f);
-  const f32x2 s = pair2(sigmoid<T>(a), sigmoid<T>(b)), ds = mul2(d, s);
+  const f32x2 s = sigmoid<T>(g), ds = mul2(d, s);
   dg = mul2(mul2(ds, u), fma2(g, fma2(s, both2(-1.0f), one), one));
   du = mul2(ds, g);
 }

@@ -117,3 +117,34 @@ def test_batch_of_one_sequence():
     import math
     assert abs(float(one.detach()) - math.log(LM_TINY.vocab)) <= 16 * 2.0 ** -23 * math.log(LM_TINY.vocab)
     ok()
+
+
+# ----------------------------------------------------------------- SwiGLU
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("K", [136, 131])
+def test_gates_far_below_zero_next_to_large_values(K, dtype):
+    """1 / (1 + exp(-g)) down to where exp(-g) leaves fp32 (g = -88.7): below
+    2^-126 from g = -87.4 on, which large values of up and dy make visible."""
+    gates = torch.tensor([-80.0, -86.0, -87.0, -87.5, -88.0, -88.5, -20.0, 80.0], device="cuda")
+    M = gates.numel()
+    gate = gates[:, None].expand(M, K).to(dtype).contiguous()
+    up, dy = torch.full_like(gate, 2.0 ** 90), torch.full_like(gate, 2.0 ** 25)
+    b = bl.SwigluBuffers.allocate(M, K, dtype)
+    bl.bl_swiglu_forward(gate, up, b.y, b.gate8, b.up8)
+    bl.bl_swiglu_backward(dy, b.gate8, b.up8, b.dgate, b.dup)
+    ok()
+    half = torch.finfo(dtype).eps / 2
+
+    def close(got, want, g, what):
+        # g log2(e) rounded in exp's argument, exp, sum, quotient and products,
+        # the quotient on the grid of 2^-149 (2.4e-7 of 2.9e-39), the result
+        rel = (20 + 4 * g.abs()) * 2.0 ** -23 + 2.0 ** -21 + 2 * half
+        assert bool(((got.double() - want).abs() <= rel * want.abs()).all()), (what, got[:, 0], want[:, 0])
+    g = gate.double()
+    close(b.y, g * torch.sigmoid(g) * up.double(), g, "y")
+    # the saved value of a constant group: the constant to three roundings
+    g, u = ((t.codes.double() * t.scales.double().repeat_interleave(128, 1)[:, :K]).float().double() for t in (b.gate8, b.up8))
+    d = dy.double()
+    s = torch.sigmoid(g)
+    close(b.dup, d * g * s, g, "dup")
+    close(b.dgate, d * u * s * (1 + g * (1 - s)), g, "dgate")
