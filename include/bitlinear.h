@@ -422,6 +422,8 @@ bl_status bl_linear_xent_backward(const void* h, const void* W, const int64_t* t
  *   scale       = fp32(a * fp32(1 / 127))
  *   saved value = fp32(code * scale)
  *
+ * These roundings are the definition: next to a tie a code may be another one
+ * than rint(127 x / a), by one, with x as near to its saved value.
  * codes [M,K] int8, scales [M,G] float. A group that holds an infinity or a
  * NaN gets a NaN scale (its saved values are NaN: an overflow is not hidden).
  * bl_act8_decode writes the saved values, rounded to x_dtype. K >= 1 is any

@@ -5,8 +5,11 @@
 //   code = rint(fp32(x * inv));    scale = fp32(a * fp32(1 / 127))
 //   saved value = fp32(code * scale)
 //
-// (one reciprocal and two products per group instead of two divisions; three
-// half steps of fp32 cannot lift |x * inv| to 127.5, so codes end at 127).
+// (one reciprocal and two products per group instead of two divisions: A1 of
+// 4096 x 6912 bf16 in 17.0 us for 17.7, of 1021 x 2565 fp32 in 5.0 for 5.3. The
+// factors are within an fp32 step or two of 127 / a and a / 127, so a code is
+// another one than rint(127 x / a) only next to a tie, and as near to x. Three
+// half steps of fp32 cannot lift |x * inv| to 127.5, so codes end at 127.)
 //
 // The arithmetic on 8 consecutive values runs on pairs (packed fp32x2
 // instructions, each half rounded like the scalar one): these kernels are
