@@ -110,6 +110,11 @@ cudaError_t launch_signsgd_apply(const uint32_t* words, int ranks, void* W, int 
                                  float lr, uint8_t* packed, float* gamma, void* workspace, int* err, cudaStream_t s);
 
 // ---- Training operators next to the BitLinear layer
+// The SMs that their plans count on, B200's. Not asked of the device: the
+// workspace sizes follow from the plans and are given without one, and the
+// order of the sums, so the results' bits, does not depend on the card. Grids
+// that neither follows from ask device_sm_count().
+constexpr int kPlanSms = 148;
 // Head cross-entropy (k_xent.cu).
 size_t xent_forward_workspace_bytes(int64_t M, int64_t V, int64_t K);
 size_t xent_backward_workspace_bytes(int64_t M, int64_t V, int64_t K, int dw_is_f32);

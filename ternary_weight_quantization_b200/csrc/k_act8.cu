@@ -317,7 +317,7 @@ cudaError_t launch_one(const Act8Args& p, cudaStream_t s) {
   // 1.7 and 1.6 us for 2.4 and 1.9, A1 and A2 with 4; at 1200 x 1024 4 per thread
   // take 2.2 and 1.9)
   if constexpr (kU > 1) {
-    if (want <= 148) return launch_one<what, T, kVec, 1>(p, s);
+    if (want <= kPlanSms) return launch_one<what, T, kVec, 1>(p, s);
   }
   constexpr int64_t kMaxGrid = 1 << 20;
   return launch_pdl(act8_kernel<what, T, kVec, kU>, dim3(static_cast<unsigned>(want < kMaxGrid ? want : kMaxGrid)),

@@ -848,7 +848,7 @@ __global__ void __launch_bounds__(256) norm_strip_kernel(const NormBwdArgs p) {
 // dweight, dbias from the blocks' partial rows: 32 columns per block, the
 // partial rows (at most 148) spread over 32 threads of each column, whose
 // loads are all in flight at once.
-constexpr int kMaxParts = 148;
+constexpr int kMaxParts = kPlanSms;
 
 __global__ void __launch_bounds__(1024) norm_join_kernel(const float* __restrict__ parts, int nparts, int K,
                                                          void* dweight, void* dbias, int p_f32, int accumulate) {

@@ -955,6 +955,7 @@ struct Plan {
 // tokens, K 2560, vocabulary 32000): 32 MiB 1.72 ms, 64 MiB 1.62, 128 MiB 1.57,
 // 256 MiB (the whole vocabulary at once) 1.54.
 constexpr int64_t kPieceBytes = int64_t(128) << 20;
+constexpr int kPlanPairs = kPlanSms / 2;
 constexpr int kF32Tokens = 1024;  // tokens per partial sum of an fp32 dW
 
 Plan make_plan(int64_t M, int64_t V, int64_t K, bool f32) {
@@ -977,11 +978,11 @@ Plan make_plan(int64_t M, int64_t V, int64_t K, bool f32) {
   const int64_t tiles = static_cast<int64_t>(tiles_of(M)) * tiles_of(K), nkb = (vcount + kBlockR - 1) / kBlockR;
   const int64_t tokens = M < kF32Tokens || !f32 ? M : kF32Tokens;
   const int64_t wkb = (tokens + kBlockR - 1) / kBlockR * (f32 ? 2 : 1) + 8;
-  const int64_t share = (tiles * nkb + tiles_of(vcount) * tiles_of(K) * wkb) / 74 + 8;
+  const int64_t share = (tiles * nkb + tiles_of(vcount) * tiles_of(K) * wkb) / kPlanPairs + 8;
   int64_t slices = (3 * nkb + 2 * share - 1) / (2 * share);
   if (slices > 32) slices = 32;
   if (slices > nkb) slices = nkb;
-  if (tiles >= 74) slices = 1;
+  if (tiles >= kPlanPairs) slices = 1;
   q.slices = slices < 1 ? 1 : static_cast<int>(slices);
   q.sums = q.pieces > 1 || q.slices > 1;
   size_t off = align256(static_cast<size_t>(M) * q.piece * 2);
@@ -1004,7 +1005,7 @@ Plan make_plan(int64_t M, int64_t V, int64_t K, bool f32) {
 // 512, vocabulary 8192: forward 8.7 us, with 256 columns 9.8);
 // else 256, which loads a third fewer bytes per product.
 static int logit_columns(int64_t M, int64_t vocab) {
-  return static_cast<int64_t>(tiles_of(M)) * ((vocab + 127) / 128) <= 74 ? 128 : 256;
+  return static_cast<int64_t>(tiles_of(M)) * ((vocab + 127) / 128) <= kPlanPairs ? 128 : 256;
 }
 
 // (maximum, sum) pairs per token: two per tile.
@@ -1025,7 +1026,7 @@ size_t xent_forward_workspace_bytes(int64_t M, int64_t V, int64_t K) {
   const int64_t few = M < kXentFew ? M : kXentFew;
   size_t most = forward_bytes(few, xent_few_parts(V, K));
   if (few == M) return most;
-  const int64_t narrow = 74 / ((V + 127) / 128) * kTile;  // the most tokens with 128 columns
+  const int64_t narrow = kPlanPairs / ((V + 127) / 128) * kTile;  // the most tokens with 128 columns
   for (const int64_t m : {M, narrow < M ? narrow : M}) {
     const size_t n = m > few ? forward_bytes(m, logit_parts(m, V)) : 0;
     if (n > most) most = n;
@@ -1038,9 +1039,9 @@ size_t xent_forward_workspace_bytes(int64_t M, int64_t V, int64_t K) {
 //   dz     a piece holds at most kPieceBytes, or 256 columns; at most the
 //          whole vocabulary
 //   sums   make_plan's slices are ceil(3 nkb / (2 share)) with share >=
-//          tiles nkb / 74, so at most ceil(111 / tiles) (and 32, and nkb); a
-//          single slice takes sums only where the vocabulary is in pieces,
-//          which more tokens (or bytes per entry) never undo
+//          tiles nkb / kPlanPairs, so at most ceil(1.5 kPlanPairs / tiles) (and
+//          32, and nkb); a single slice takes sums only where the vocabulary is
+//          in pieces, which more tokens (or bytes per entry) never undo
 // Each part only grows with M and with the bytes per entry. At most 64 MiB of
 // dz and about 30 MB of sums are more than the plan itself lays out (2048
 // tokens, K 512, V 8192: 67 MB for 48; 4096, 2560, 32000: 197 for 195).
@@ -1052,8 +1053,8 @@ size_t xent_backward_workspace_bytes(int64_t M, int64_t V, int64_t K, int dw_is_
   const int64_t tm = tiles_of(M), tk = tiles_of(K), nkb = (V + kBlockR - 1) / kBlockR;
   const bool pieces = make_plan(M, V, K, dw_is_f32 != 0).pieces > 1;
   int64_t rows = pieces ? tm : 0;  // of dH's partial sums, in tiles
-  for (int64_t m = 1; m <= tm && m * tk < 74; ++m) {
-    int64_t slices = (111 + m * tk - 1) / (m * tk);
+  for (int64_t m = 1; m <= tm && m * tk < kPlanPairs; ++m) {
+    int64_t slices = (3 * kPlanPairs + 2 * m * tk - 1) / (2 * m * tk);
     slices = slices > 32 ? 32 : slices;
     slices = slices > nkb ? nkb : slices;
     if (slices > 1 && m * slices > rows) rows = m * slices;

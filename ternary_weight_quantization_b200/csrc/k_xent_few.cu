@@ -505,6 +505,8 @@ __global__ void __launch_bounds__(512) few_dh_kernel(const float* __restrict__ p
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+constexpr int64_t kWave = 2 * kPlanSms;  // blocks at work at once, two per SM
+
 // The logits' warps per unit of 16 rows: as many as it takes to give every SM
 // 8 warps, as long as each has more than one round of loads (4 steps of 32).
 // Measured on B200 (forward): 4000 x 4096 8.9 us with 8 warps, 27.9 with one;
@@ -512,13 +514,13 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int few_ksplit(int64_t V, int64_t K) {
   const int64_t units = ceil_div(V, 16), steps = ceil_div(K, 32);
   int ks = 1;
-  while (ks < kWarps && units * ks < 148 * 8 && steps > 4 * ks) ks *= 2;
+  while (ks < kWarps && units * ks < kPlanSms * 8 && steps > 4 * ks) ks *= 2;
   return ks;
 }
 
 int few_blocks(int64_t V, int64_t K) {
   const int64_t want = ceil_div(ceil_div(V, 16) * few_ksplit(V, K), kWarps);
-  return static_cast<int>(want < 296 ? want : 296);
+  return static_cast<int>(want < kWave ? want : kWave);
 }
 
 // Row blocks of the products: one wave of two blocks per SM; two waves, which
@@ -526,7 +528,8 @@ int few_blocks(int64_t V, int64_t K) {
 // 32000 x 2560 95.7 us in one wave, 87.9 in two; 8192 x 512 10.4 and 12.3.
 int few_row_blocks(int64_t V, int64_t K) {
   const int64_t warps = ceil_div(ceil_div(V, 16), kWarps), tiles = ceil_div(K, 64);
-  const int64_t one = 296 / tiles > 0 ? 296 / tiles : 1, two = 592 / tiles > 0 ? 592 / tiles : 1;
+  const int64_t one = kWave / tiles > 0 ? kWave / tiles : 1;
+  const int64_t two = 2 * kWave / tiles > 0 ? 2 * kWave / tiles : 1;
   const int64_t most = warps >= 8 * two ? two : one;
   return static_cast<int>(warps < most ? warps : most);
 }
