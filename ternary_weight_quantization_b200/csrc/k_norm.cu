@@ -106,9 +106,10 @@ __device__ __forceinline__ void group_sum(float (&v)[kN], float* buf, int t, int
 
 // s / k, with inv = fp32(1 / k): the quotient's error is made good by one
 // step with the exact remainder (a row of one value keeps its mean exactly).
+// An infinite sum has no remainder: its mean is that infinity.
 __device__ __forceinline__ float mean_of(float s, float k, float inv) {
   const float m = s * inv;
-  return fmaf(fmaf(-m, k, s), inv, m);
+  return fabsf(m) < __uint_as_float(0x7F800000u) ? fmaf(fmaf(-m, k, s), inv, m) : m;
 }
 
 // 1 / sqrt(v): the hardware's approximation and one Newton step

@@ -148,3 +148,24 @@ def test_gates_far_below_zero_next_to_large_values(K, dtype):
     s = torch.sigmoid(g)
     close(b.dup, d * g * s, g, "dup")
     close(b.dgate, d * u * s * (1 + g * (1 - s)), g, "dgate")
+
+
+# ----------------------------------------------------------------- norms
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("K", [64, 100, 1032, 8200, 10001])
+def test_mean_of_rows_with_infinities(K, dtype):
+    """The mean is the sum over K also where that is infinite; y and rstd of such
+    a row are not numbers, as the formula says, and other rows are untouched."""
+    inf = float("inf")
+    x = rnd(6, K, dtype=dtype)
+    x[1, 3], x[2, K - 1], x[3, 0], x[3, 1], x[4, 5] = inf, -inf, inf, -inf, float("nan")
+    clean = rnd(6, K, dtype=dtype)
+    y, mean, rstd = torch.empty_like(x), torch.empty(6, device="cuda"), torch.empty(6, device="cuda")
+    y2, mean2, rstd2 = torch.empty_like(x), torch.empty(6, device="cuda"), torch.empty(6, device="cuda")
+    bl.bl_norm_forward(x, None, None, 1e-6, y, mean, rstd)
+    bl.bl_norm_forward(clean, None, None, 1e-6, y2, mean2, rstd2)
+    ok()
+    assert float(mean[1]) == inf and float(mean[2]) == -inf
+    assert bool(mean[3:5].isnan().all()) and bool(rstd[1:5].isnan().all()) and bool(y[1:5].isnan().all())
+    for a, b in ((y, y2), (mean, mean2), (rstd, rstd2)):
+        assert torch.equal(a[[0, 5]], b[[0, 5]])
