@@ -358,9 +358,11 @@ bl_status bl_signsgd_apply(const uint32_t* sign_words, int ranks, void* W, bl_dt
  *
  * h [M,K] bf16, W [V,K] bf16, targets [M] int64; loss [M], lse [M] float
  * outputs. A target outside 0..V-1 marks a token that is left out (padding, a
- * prompt): its loss is 0; its lse is written like any other's. One token's
- * values never reach another's, so what a left-out token's row of h holds
- * (infinities and NaN included) does not matter.
+ * prompt): its loss is 0; its lse is written like any other's. A logit of
+ * +infinity or NaN makes its token's loss and lse NaN (-infinity is a
+ * probability of zero). One token's values never reach another's, so what a
+ * left-out token's row of h holds (infinities and NaN included) does not
+ * matter.
  * workspace: at least bl_linear_xent_forward_workspace_size(M,V,K) bytes,
  * 16-byte aligned, no initialisation, one call at a time per workspace: one
  * (maximum, sum) pair per token and 64 or more vocabulary entries (few tokens:
@@ -389,10 +391,11 @@ bl_status bl_linear_xent_forward(const void* h, const void* W, const int64_t* ta
  * its dz kept, in bf16, only until its share of dH and dW has been added (at
  * most 128 MiB of dz, or 256 columns; dW in fp32 keeps dz to 16 significant
  * bits, as the sum of two bf16 numbers, and joins partial sums of 1024 tokens
- * in fp32). Up to 16 tokens take the whole vocabulary at once, with dz to 16
- * significant bits in 32 bytes per entry and 8 tokens for either dW. Sums over
- * pieces are kept in fp32 and always added in the same order: the same inputs
- * give the same bits.
+ * in fp32; dH takes the first of the two). The tensor cores' fp32 sums may drop
+ * a last bit per 16 terms, of tokens or of a piece's vocabulary. Up to 16 tokens
+ * take the whole vocabulary at once, with dz to 16 significant bits in 32 bytes
+ * per entry and 8 tokens for either dW. Sums over pieces are kept in fp32 and
+ * always added in the same order: the same inputs give the same bits.
  * lse is X1's output. dH [M,K] bf16 or NULL (skipped); dW [V,K] of dw_dtype
  * (BL_BF16 or BL_F32) or NULL (skipped); accumulate_dW != 0 adds to what dW
  * holds. A left-out token (X1) has dz = 0 whatever its h, lse and dloss hold:

@@ -7,10 +7,11 @@
 //             dx = rstd (g - mean(g) - xhat mean(g xhat))
 //             dweight = sum over rows of dy xhat, dbias = sum over rows of dy
 //
-// Both should be bound by HBM, but the work per value is close to what an SM
-// issues while its share of the bytes arrives, so what counts is the number of
-// instructions: a thread takes 16 or 32 columns of a row, so that the row's
-// sums, addresses and reciprocals cost little per value. A group of threads
+// Both should be bound by HBM, but the work per value is near what an SM issues
+// while its share of the bytes arrives, and a row's sums are a chain of shuffles
+// and a barrier: no unit is saturated (ncu, 4096 x 2560 with the 8-bit x: SM 51
+// and 36 %, L1 41 and 58 %). So a thread takes 16 or 32 columns of a row, that the
+// row's sums, addresses and reciprocals cost little per value. A group of threads
 // walks the rows of its own; each thread copies its columns of the next rows
 // asynchronously into its own places of shared memory, which keeps the bytes
 // in flight without registers and without barriers. Forward: several blocks
@@ -21,12 +22,12 @@
 // than 8192 columns take two passes in the backward: the row sums, then column
 // strips.
 //
-// Measured on B200 (back to back in a graph): 4096 x 2560 bf16 with the 8-bit x:
-// forward 11.5 us (4.6 TB/s), backward 19.8 (2.7 TB/s; of these 6 to 8 are the
-// start, the groups' joining and the second launch: 16384 x 2560 takes 48.6 us,
-// 0.80 of the copy rate). 4096 x 2560 fp32: 14.4 (0.90) and 29.4 us. Rows that fill
-// every thread's places spare the column tests: with them the two took 13.0 and
-// 21.3 us.
+// Measured on B200 (back to back in a graph, over inputs that rotate past L2), with
+// the share of the copy rate: bf16 with the 8-bit x, 4096 x 2560: forward 13.2 us
+// (0.62), backward 19.5 (0.42; of these 6 to 8 us are the start, the groups' joining
+// and the second launch), 16384 x 2560: 41.2 (0.80) and 50.3 (0.65). 4096 x 2560 fp32:
+// 16.1 (0.81) and 28.5 (0.68). Rows that fill every thread's places spare the column
+// tests, a tenth of the time.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -23,9 +23,11 @@
 // reduction per CTA (two TMA boxes of 64 x 64, 128-byte swizzled: only the
 // coordinates and the descriptors differ between K-major and MN-major). With
 // 5 to 7 stages of 32 KB and two TMEM accumulators the tensor cores do not wait
-// for an epilogue unless it takes longer than its tile's products (K below about
-// 384 for Lse and Dz: the exponentials). All bounds are handled by TMA: rows and
-// columns outside a tensor load as zeros and are not stored.
+// for an epilogue unless it takes longer than its tile's products: for Lse and Dz,
+// with their exponentials, up to K of about 384 (forward of 2048 tokens, vocabulary
+// 9472, four even waves: 17 to 18 us from K 192 to 384, 20.4 at 512, 31 at 1024).
+// All bounds are handled by TMA: rows and columns outside a tensor load as zeros
+// and are not stored.
 //
 // Roles (384 threads per CTA): warp 0 loads, warp 1 issues the MMAs (one lane
 // of the leader CTA), warps 2 and 3 do side work on whole rows (the target's
@@ -40,10 +42,12 @@
 // alone 640, both together 690, so the two share the SM's memory path. Lse runs
 // at 0.95 of the measured bf16 peak (ncu: 425 us), Dz at 0.97 and Grad at 0.9 of
 // it (busiest pair 576 of 553 stages on average); back to back the step is held
-// by the power cap at 0.90 of the sustained rate. Whole calls, forward + backward:
-// 2048 tokens, K 512, vocabulary 8192 in 79 us (1.7 x the time of four products at
-// the peak: K is short, so Lse and Dz wait for the exponentials), 4096, 2560, 32000
-// in 2.05 ms; the forward alone at 2048, 2560, 131072 in 1.03 ms (1337 TFLOP/s).
+// by the power cap at 0.90 of the sustained rate. Whole calls, forward + backward,
+// back to back in a graph: 2048 tokens, K 512, vocabulary 8192 in 73 us (1.8 x the
+// time of four products at the peak: 256 tiles on 74 pairs are four waves for 3.46
+// waves of work, and each of five launches has its own start and end), 4096, 2560,
+// 32000 in 2.05 to 2.11 ms; the forward alone at 2048, 2560, 131072 in 1.03 to 1.04
+// ms (1320 to 1337 TFLOP/s).
 // With few tiles the time is a tile's own: about 6 us of launch, fill and epilogue
 // and 0.3 us per stage. Up to 16 tokens have kernels of their own
 // (k_xent_few.cu).

@@ -169,3 +169,29 @@ def test_mean_of_rows_with_infinities(K, dtype):
     assert bool(mean[3:5].isnan().all()) and bool(rstd[1:5].isnan().all()) and bool(y[1:5].isnan().all())
     for a, b in ((y, y2), (mean, mean2), (rstd, rstd2)):
         assert torch.equal(a[[0, 5]], b[[0, 5]])
+
+
+@pytest.mark.parametrize("M,K", [(3, 512), (16, 64), (20, 128), (300, 72)])
+def test_infinite_logits(M, K):
+    """+infinity makes its token's loss and lse NaN, other tokens keep theirs."""
+    V = 700
+    h, W, t = rnd(M, K, dtype=BF), rnd(V, K, seed=1, dtype=BF, scale=0.05), targets(M, V).clamp(min=0)
+    h[:, 3] = 0
+    b = bl.XentBuffers.allocate(M, V, K)
+    bl.bl_linear_xent_forward(h, W, t, b.loss, b.lse, b.workspace)
+    loss, lse = b.loss.clone(), b.lse.clone()
+    h2 = h.clone()
+    h2[1, 3] = 1e30
+    big = W.clone()
+    big[:, 3] = 0
+    big[11, 3] = 3e38          # token 1's logit of row 11 overflows; the others have 0 there
+    W0 = W.clone()
+    W0[:, 3] = 0
+    bl.bl_linear_xent_forward(h, W0, t, b.loss, b.lse, b.workspace)
+    torch.cuda.synchronize()
+    assert torch.equal(b.loss, loss) and torch.equal(b.lse, lse)     # h is 0 there
+    bl.bl_linear_xent_forward(h2, big, t, b.loss, b.lse, b.workspace)
+    ok()
+    rest = [i for i in range(M) if i != 1]
+    assert bool(b.loss[1].isnan()) and bool(b.lse[1].isnan())
+    assert torch.equal(b.loss[rest], loss[rest]) and torch.equal(b.lse[rest], lse[rest])
