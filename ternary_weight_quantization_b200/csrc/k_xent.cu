@@ -288,14 +288,28 @@ struct LseState {
 };
 
 // Boxes of 64 rows, of the `most` that a CTA's share of an operand has, that
-// hold rows below `limit`. In the logit phases the others are not loaded: rows
-// of A and of B reach only their own rows and columns of D, which are not used
-// there. (In Grad the tests cost more than they save: 4096 tokens, K 2560,
-// vocabulary 32000: 2.34 ms with them, 2.26 without.)
+// hold rows below `limit`.
 __device__ __forceinline__ int boxes(int limit, int row, int most) {
   const int n = (limit - row + 63) >> 6;
   return n < 0 ? 0 : n < most ? n : most;
 }
+
+// What CTA `rank` loads per stage in the logit phases: the boxes of A and of B
+// that hold rows. The others are left out: rows of A and of B reach only their
+// own rows and columns of D, which are not used there. (In Grad the tests cost
+// more than they save: 4096 tokens, K 2560, vocabulary 32000: 2.34 ms with them,
+// 2.26 without.) A CTA without any loads one all the same, of zeros or of rows
+// that are not used: the leader's stages fill only with both CTAs' boxes, which is
+// what keeps its loader from running rounds ahead of the peer's, whose waits tell
+// one round from the next by a single bit.
+template <int BN>
+struct CtaBoxes {
+  int a, b;
+  __device__ __forceinline__ CtaBoxes(const XentParams& p, const Tile& t, int rank)
+      : a(boxes(p.M, t.a0 + rank * 128, 2)), b(boxes(p.vcount, t.b0 + rank * (BN / 2), BN / 128)) {
+    if (a + b == 0) b = 1;
+  }
+};
 
 template <Phase P, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
@@ -374,10 +388,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
         uint32_t bytes = 2 * kStageBytes;
         int na = 2, nb = 2;
         if constexpr (P != Phase::Grad) {
-          na = boxes(p.M, a0, 2);
-          nb = boxes(p.vcount, b0, BN / 128);
-          bytes = kBox * (boxes(p.M, t.a0, 2) + boxes(p.M, t.a0 + 128, 2) + boxes(p.vcount, t.b0, BN / 128) +
-                          boxes(p.vcount, t.b0 + BN / 2, BN / 128));
+          const CtaBoxes<BN> first(p, t, 0), second(p, t, 1);
+          na = leader ? first.a : second.a;
+          nb = leader ? first.b : second.b;
+          bytes = kBox * (first.a + first.b + second.a + second.b);
         }
         // one loop per kind of tile: a stage must be requested in the few hundred
         // cycles that the tensor cores take for one

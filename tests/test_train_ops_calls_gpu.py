@@ -195,3 +195,30 @@ def test_infinite_logits(M, K):
     rest = [i for i in range(M) if i != 1]
     assert bool(b.loss[1].isnan()) and bool(b.lse[1].isnan())
     assert torch.equal(b.loss[rest], loss[rest]) and torch.equal(b.lse[rest], lse[rest])
+
+
+# ----------------------------------------------------------------- head cross-entropy: ragged tiles
+@pytest.mark.parametrize("M,V,K", [(359, 8263, 3888), (359, 8263, 8000), (130, 300, 32768), (300, 5120 + 64, 4096), (20, 130, 65536),
+                                   (257, 1025, 8192), (1025, 257, 8192)])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_tiles_of_which_one_cta_holds_no_rows(M, V, K, dt):
+    """Token and vocabulary tiles that end in their first half, over many stages:
+    the second CTA of the last pair has nothing to load, and no wait may run out."""
+    h, W, t, dl = rnd(M, K, dtype=BF), rnd(V, K, seed=1, dtype=BF, scale=0.02), targets(M, V), torch.full((M,), 1 / M, device="cuda")
+    b = bl.XentBuffers.allocate(M, V, K, dt)
+    for _ in range(3):
+        bl.bl_linear_xent_forward(h, W, t, b.loss, b.lse, b.workspace)
+        bl.bl_linear_xent_backward(h, W, t, b.lse, dl, b.dH, b.dW, b.workspace)
+        ok()
+    z = h.double() @ W.double().t()
+    lse = torch.logsumexp(z, 1)
+    e = (K / 16 + 16) * 2.0 ** -23 * float((h.double().abs() @ W.double().abs().t()).amax())
+    assert bool(((b.lse.double() - lse).abs() <= e + 2.0 ** -19 * (1 + lse.abs())).all())
+    dz = torch.exp(z - lse[:, None])
+    dz[torch.arange(M, device="cuda"), t.clamp(min=0)] -= 1
+    dz = torch.where((t >= 0)[:, None], dz * dl.double()[:, None], 0.0)
+    for got, a, c, n in ((b.dH, dz, W.double(), V), (b.dW, dz.t(), h.double(), M)):
+        want, mag = a @ c, a.abs() @ c.abs()
+        # dz's and the result's roundings, p's exponent, a step per 16 terms
+        tol = (2.0 ** -8 + 2 * e + (n / 16 + 64) * 2.0 ** -23) * mag
+        assert bool(((got.double() - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol) + 1e-36).all())
