@@ -222,3 +222,21 @@ def test_tiles_of_which_one_cta_holds_no_rows(M, V, K, dt):
         # dz's and the result's roundings, p's exponent, a step per 16 terms
         tol = (2.0 ** -8 + 2 * e + (n / 16 + 64) * 2.0 ** -23) * mag
         assert bool(((got.double() - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol) + 1e-36).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("K", [144, 1312, 8176, 14768, 141])
+def test_norm_backward_uses_the_rounded_saved_values(K, dtype):
+    """One row, whose dweight is dy xhat: also where a saved value lies next to
+    the mean, x - mean is that of the fp32 saved value, in every kernel."""
+    from tests.test_rows_gpu import saved_values
+    M = 1
+    for seed in range(8):
+        x, w, dy = (rnd(M, K, seed=seed) + 0.5).to(dtype), torch.ones(K, device="cuda"), rnd(M, K, seed=seed + 100, dtype=dtype)
+        b = bl.NormBuffers.allocate(M, K, dtype, F32, saved8=True)
+        bl.bl_norm_forward(x, w, None, 1e-6, b.y, b.mean, b.rstd, saved8=b.saved8)
+        bl.bl_norm_backward(dy, b.saved8, w, b.mean, b.rstd, b.dx, b.dweight, None, b.workspace)
+        ok()
+        want = dy.double() * (saved_values(x)[2].double() - b.mean.double()[:, None]) * b.rstd.double()[:, None]
+        # three roundings of half a step
+        assert bool(((b.dweight.double() - want[0]).abs() <= 3.001 * 2.0 ** -24 * want[0].abs()).all())
