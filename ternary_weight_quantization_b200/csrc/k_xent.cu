@@ -106,7 +106,7 @@ struct XentParams {
   int ntiles_a, ntiles_b, split_pair, more;
   int tiles_m, tiles_k;  // tiles over tokens and over K
   // Lse
-  float2* part;          // [2 per vocab tile][M]: (max, sum exp(z - max)) of half its columns
+  float2* part;          // [2 per vocab tile][M]: (maximum, sum) of half its columns, see LseState
   float2* tlogit;        // [M]: the target's logit, as the tile has it and as an fp32 dot product
   const uint4* W;        // rows of W
   // Dz
@@ -262,7 +262,11 @@ struct Stager {
   }
 };
 
-// ---- Lse: running maximum and sum over the tile's columns of one token.
+// ---- Lse: running maximum and sum over the tile's columns of one token. The
+// maximum is kept as m = fl(z log2 e) and the sum relative to 2^m, here and in
+// the joins: rescaling takes ex2 of the difference of two such numbers, which is
+// exactly 1 where the maximum stays. (With z kept instead, every join left the
+// rounding of z log2 e in the sum, always to the same side.)
 struct LseState {
   float m, s;
   __device__ __forceinline__ void chunk(uint32_t (&r)[32], int valid) {
@@ -273,16 +277,16 @@ struct LseState {
     float c = __uint_as_float(r[0]);
 #pragma unroll
     for (int j = 1; j < 32; ++j) c = fmaxf(c, __uint_as_float(r[j]));
-    const float n = fmaxf(m, c);
+    const float n = fmaxf(m, c * kLog2e);
     // an empty maximum (all -inf) leaves exp(-inf - 0) = 0
-    const float nl = n == __uint_as_float(0xFF800000u) ? 0.0f : n * kLog2e;
+    const float nl = n == __uint_as_float(0xFF800000u) ? 0.0f : n;
     float a0 = 0.0f, a1 = 0.0f;
 #pragma unroll
     for (int j = 0; j < 32; j += 2) {
       a0 += ex2(fmaf(__uint_as_float(r[j]), kLog2e, -nl));
       a1 += ex2(fmaf(__uint_as_float(r[j + 1]), kLog2e, -nl));
     }
-    s = fmaf(s, ex2(fmaf(m, kLog2e, -nl)), a0 + a1);
+    s = fmaf(s, ex2(m - nl), a0 + a1);
     m = n;
   }
 };
@@ -791,8 +795,8 @@ constexpr int kJoinTokens = 8, kJoinSplit = 64;
 
 __device__ __forceinline__ float2 join_parts(float2 a, float2 b) {
   const float n = fmaxf(a.x, b.x);
-  const float nl = n == __uint_as_float(0xFF800000u) ? 0.0f : n * kLog2e;
-  return make_float2(n, a.y * ex2(fmaf(a.x, kLog2e, -nl)) + b.y * ex2(fmaf(b.x, kLog2e, -nl)));
+  const float nl = n == __uint_as_float(0xFF800000u) ? 0.0f : n;
+  return make_float2(n, a.y * ex2(a.x - nl) + b.y * ex2(b.x - nl));
 }
 
 __global__ void __launch_bounds__(kJoinTokens* kJoinSplit)
@@ -861,7 +865,7 @@ __global__ void __launch_bounds__(kJoinTokens* kJoinSplit)
     a = join_parts(a, make_float2(__shfl_xor_sync(0xffffffffu, a.x, s), __shfl_xor_sync(0xffffffffu, a.y, s)));
   if (lane == 0 && mm < M) {
     if (h) tl.y = target_logit[warp];
-    float l = a.x + logf(a.y);
+    float l = fmaf(a.x, 0.6931471805599453f, logf(a.y));
     float nll = 0.0f;
     if (t >= 0 && t < V) {
       // the fp32 target logit in the place of the tile's, in lse too: a token

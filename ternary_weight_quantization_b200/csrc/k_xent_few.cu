@@ -114,10 +114,16 @@ __device__ __forceinline__ bool counts(const FewParams& p, int m) {
   return t >= 0 && t < p.V;
 }
 
-// (maximum, sum of 2^(x log2 e - maximum)) joined with another pair.
+// (maximum fl(z log2 e), sum of 2^(z log2 e - maximum)) joined with another pair,
+// and with one logit. Where the maximum stays, the sum keeps its bits.
 __device__ __forceinline__ void join(float& top, float& sum, float top2, float sum2) {
-  const float n = fmaxf(top, top2), nl = n == __uint_as_float(0xFF800000u) ? 0.0f : n * kLog2e;
-  sum = sum * ex2(fmaf(top, kLog2e, -nl)) + sum2 * ex2(fmaf(top2, kLog2e, -nl));
+  const float n = fmaxf(top, top2), nl = n == __uint_as_float(0xFF800000u) ? 0.0f : n;
+  sum = sum * ex2(top - nl) + sum2 * ex2(top2 - nl);
+  top = n;
+}
+__device__ __forceinline__ void join(float& top, float& sum, float z) {
+  const float n = fmaxf(top, z * kLog2e), nl = n == __uint_as_float(0xFF800000u) ? 0.0f : n;
+  sum = fmaf(sum, ex2(top - nl), ex2(fmaf(z, kLog2e, -nl)));
   top = n;
 }
 
@@ -272,7 +278,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) few_logits_kernel(const FewPar
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const float z = c[t][2 * half + e];
-              join(top[t][e], sum[t][e], z, 1.0f);
+              join(top[t][e], sum[t][e], z);
               if (tgt[t][e] == row) p.tlogit[8 * t + 2 * q + e].x = z;
             }
           }

@@ -240,3 +240,30 @@ def test_norm_backward_uses_the_rounded_saved_values(K, dtype):
         want = dy.double() * (saved_values(x)[2].double() - b.mean.double()[:, None]) * b.rstd.double()[:, None]
         # three roundings of half a step
         assert bool(((b.dweight.double() - want[0]).abs() <= 3.001 * 2.0 ** -24 * want[0].abs()).all())
+
+
+@pytest.mark.parametrize("M,V", [(16, 151936), (5, 1 << 20), (48, 151936), (300, 32000), (20, 1 << 20)])
+def test_lse_keeps_its_bits_over_many_joins(M, V):
+    """Logits that are exact in fp32 and all alike, or all alike but a few: lse
+    is the logit plus log V, whatever the number of partial sums."""
+    K = 8
+    h, W = torch.zeros(M, K, dtype=BF, device="cuda"), torch.zeros(V, K, dtype=BF, device="cuda")
+    h[:, 0] = torch.linspace(-90, 90, M, device="cuda").to(BF)
+    W[:, 0] = 1.0
+    W[::1000, 0] = 0.5
+    t = torch.arange(M, device="cuda") * 3 + 1
+    b = bl.XentBuffers.allocate(M, V, K, backward=False)
+    bl.bl_linear_xent_forward(h, W, t, b.loss, b.lse, b.workspace)
+    ok()
+    z = h[:, 0].double()[:, None] * torch.tensor([1.0, 0.5], device="cuda", dtype=torch.float64)
+    n = -(-V // 1000)
+    lse = torch.logsumexp(z + torch.log(torch.tensor([V - n, n], device="cuda", dtype=torch.float64)), 1)
+    # the sum: additions that a term goes through (16 in a chunk, 4 chunks, a
+    # thread's parts and 12 joins; few tokens: a lane's logits), ex2's and log's
+    # two units each; z log2 e and the result: half a step of lse each, log2 e
+    # and ln 2 another
+    adds = 40 + max(V / 128 / 64, V / (16 * 8 * 296) * 2)
+    tol = (adds / 2 + 8) * 2.0 ** -23 + 3 * 2.0 ** -24 * 2 * lse.abs()
+    assert bool(((b.lse.double() - lse).abs() <= tol).all()), ((b.lse.double() - lse).abs() / tol).max()
+    live = lse - z[:, 0]
+    assert bool(((b.loss.double() - live).abs() <= 2 * tol).all())
