@@ -346,7 +346,8 @@ bl_status bl_signsgd_apply(const uint32_t* sign_words, int ranks, void* W, bl_dt
  * with BitLinear layers runs outside its ternary projections. The pages give
  * no such operators ("bitnet-qat-train", Measured behavior, Training, trains
  * a 4-layer transformer LM around the layer); they follow the definitions
- * given at each call.
+ * given at each call. What a call writes overlaps neither what it reads nor its
+ * other outputs, but where the call says so.
  */
 
 /*

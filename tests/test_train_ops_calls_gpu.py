@@ -267,3 +267,42 @@ def test_lse_keeps_its_bits_over_many_joins(M, V):
     assert bool(((b.lse.double() - lse).abs() <= tol).all()), ((b.lse.double() - lse).abs() / tol).max()
     live = lse - z[:, 0]
     assert bool(((b.loss.double() - live).abs() <= 2 * tol).all())
+
+
+def test_calls_from_two_host_threads():
+    """Two threads, each with its own stream and buffers, at once: the same bits
+    as the calls alone, by the current stream and by one that is given."""
+    import threading
+    M, K, V = 300, 264, 5000
+    sets = [(rnd(M, K, seed=s, dtype=BF), rnd(V, K, seed=s + 1, dtype=BF, scale=0.05), targets(M, V, s), rnd(K, seed=s + 2))
+            for s in (1, 11)]
+    dl = torch.full((M,), 1 / M, device="cuda")
+
+    def chain(h, W, t, w, stream=None):
+        x, n, g = bl.XentBuffers.allocate(M, V, K), bl.NormBuffers.allocate(M, K, saved8=True), bl.SwigluBuffers.allocate(M, K)
+        bl.bl_norm_forward(h, w, None, 1e-6, n.y, n.mean, n.rstd, saved8=n.saved8, stream=stream)
+        bl.bl_swiglu_forward(n.y, h, g.y, g.gate8, g.up8, stream=stream)
+        bl.bl_linear_xent_forward(g.y, W, t, x.loss, x.lse, x.workspace, stream=stream)
+        bl.bl_linear_xent_backward(g.y, W, t, x.lse, dl, x.dH, x.dW, x.workspace, stream=stream)
+        bl.bl_swiglu_backward(x.dH, g.gate8, g.up8, g.dgate, g.dup, stream=stream)
+        bl.bl_norm_backward(g.dgate, n.saved8, w, n.mean, n.rstd, n.dx, n.dweight, None, n.workspace, stream=stream)
+        return [x.loss, x.lse, x.dH, x.dW, g.dgate, g.dup, n.dx, n.dweight]
+    want = [chain(*s) for s in sets]
+    ok()
+    got = [[], []]
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for k in range(10):
+                got[i].append(chain(*sets[i], stream=stream if k % 2 else None))
+        stream.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    ok()
+    for runs, w in zip(got, want):
+        assert len(runs) == 10
+        assert all(torch.equal(a, b) for run in runs for a, b in zip(run, w))
