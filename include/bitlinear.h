@@ -513,6 +513,143 @@ bl_status bl_swiglu_backward(const void* dy, const int8_t* gate_codes, const flo
                              int64_t M, int64_t K, void* dgate, void* dup, void* stream);
 
 /*
+ * Q1 -- RMS norm of a residual stream into INT8, with the last projection's
+ * output added on the way in: what stands between one block's output and the
+ * next block's projections, in one pass.
+ *
+ *   sum[m,k] = round_s(x[m,k] + residual[m,k])          the stream, kept
+ *   rstd[m]  = 1 / sqrt(sum_k sum[m,k]^2 / K + eps)      sums in fp32
+ *   t[m,k]   = fp32(sum[m,k] * weight[k])
+ *   a        = max(fp32(max_k |t[m,k]| * rstd[m]), 1e-5)
+ *   xq[m,k]  = rint_half_even(fp32(t[m,k] * fp32(rstd[m] * fp32(127 / a))))   in [-127, 127]
+ *   sx[m]    = fp32(a / 127)
+ *
+ * xq and sx are S2's form of y = sum * rstd * weight, which itself is not
+ * rounded to a type of its own on the way (S2 takes a bf16 x): the operand of
+ * bl_forward (K % 32 == 0) and of L1 (K % 16 == 0).
+ * x [M,K] of x_dtype, residual and sum [M,K] of s_dtype (the stream's), weight
+ * [K] of p_dtype or NULL (ones): BL_BF16 or BL_F32 each, not an fp32 x with a
+ * bf16 stream. residual and sum both NULL: x is the stream itself (s_dtype is
+ * then x_dtype). sum may be the residual itself, or x where the types agree.
+ * rstd [M] float is kept for Q2. xq [M,K] int8, sx [M] float.
+ * A row with an infinity or a NaN, and one whose sum of squares leaves fp32,
+ * gets a NaN rstd and a NaN sx (an overflow is not hidden).
+ * K is a multiple of 8 up to 8192; eps finite and >= 0. M == 0 is a no-op.
+ * Errors: BL_ERR_INVALID_ARG, BL_ERR_UNSUPPORTED_SHAPE, BL_ERR_DTYPE,
+ *         BL_ERR_ALIGNMENT, BL_ERR_ARCH, BL_ERR_CUDA.
+ */
+bl_status bl_norm_quant_forward(const void* x, bl_dtype x_dtype, const void* residual, bl_dtype s_dtype,
+                                const void* weight, bl_dtype p_dtype, int64_t M, int64_t K, float eps, void* sum,
+                                float* rstd, int8_t* xq, float* sx, void* stream);
+
+/*
+ * Q2 -- the gradients of Q1, with n[m,k] = sum[m,k] * rstd[m], g[m,k] =
+ * dy[m,k] * weight[k], dy the gradient of y (the quantiser's Jacobian is taken
+ * as 1) and dsum that of the stream behind the addition (NULL: none):
+ *
+ *   d[m,k]         = dsum[m,k] + rstd[m] * (g[m,k] - n[m,k] * sum_k(g * n) / K)
+ *   dresidual[m,k] = round_s(d[m,k])
+ *   dx[m,k]        = round_x(d[m,k])
+ *   dweight[k]     = round(sum_m dy[m,k] * n[m,k] (+ dweight[k] if accumulate))
+ *
+ * sum is Q1's (its x, where there was no residual), of s_dtype like dsum and
+ * dresidual; dy [M,K] of dy_dtype, dx [M,K] of x_dtype, dweight [K] of p_dtype.
+ * Each of dresidual, dx and dweight may be NULL (skipped); where the types of
+ * the stream and of x agree one of the first two is enough. dresidual may be
+ * dsum itself, and dx dy itself (of one type). The sums over the tokens are
+ * fp32 and always added in the same order. M == 0 writes dweight = 0 (leaves it
+ * as it is with accumulate).
+ * workspace: at least bl_norm_quant_backward_workspace_size(M,K) bytes, 16-byte
+ * aligned, no initialisation, one call at a time per workspace (not used, and
+ * may be NULL, without dweight).
+ * Errors: as Q1, plus BL_ERR_WORKSPACE.
+ */
+size_t bl_norm_quant_backward_workspace_size(int64_t M, int64_t K);
+bl_status bl_norm_quant_backward(const void* dy, bl_dtype dy_dtype, const void* dsum, const void* sum, bl_dtype s_dtype,
+                                 const void* weight, bl_dtype p_dtype, const float* rstd, int64_t M, int64_t K,
+                                 void* dresidual, void* dx, bl_dtype x_dtype, void* dweight, int accumulate,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * L1 -- the product of two INT8 operands with a scale per token and one per
+ * output channel: a layer that keeps 8-bit weights next to the ternary ones (a
+ * head, say).
+ *
+ *   acc[m,n] = sum_k xq[m,k] * wq[n,k]                        exact INT32
+ *   y[m,n]   = round(fp32(fp32(acc) * fp32(sx[m] * sw[n])))
+ *
+ * xq [M,K] int8 and sx [M] float as S2 or Q1 give them, wq [N,K] int8 and sw
+ * [N] float (S2 on the rows of a weight gives these); codes may be any INT8
+ * values. y [M,N] of y_dtype. fp32(acc) rounds sums beyond 2^24.
+ * Limits: K a multiple of 16 up to 65536, M up to 131072, N up to 2^20. M == 0
+ * is a no-op.
+ * Errors: as Q1; device timeouts via bl_get_last_error.
+ */
+bl_status bl_int8_linear_forward(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw, int64_t M,
+                                 int64_t N, int64_t K, void* y, bl_dtype y_dtype, void* stream);
+
+/*
+ * L2 -- the straight-through gradients of L1:
+ *
+ *   x_hat[m,k] = bf16_rn(fp32(xq[m,k]) * sx[m])        (as in S4)
+ *   w_hat[n,k] = bf16_rn(fp32(wq[n,k]) * sw[n])
+ *   dX[m,k] = bf16_rn(sum_n dY[m,n] * w_hat[n,k])
+ *   dW[n,k] = round(sum_m dY[m,n] * x_hat[m,k] (+ dW[n,k] if accumulate_dW))
+ *
+ * dY [M,N] bf16, N a multiple of 8. dX [M,K] bf16 or NULL (skipped); dW [N,K] of
+ * dw_dtype (BL_BF16 or BL_F32) or NULL (skipped). Sums in fp32, always added in
+ * the same order; dW in fp32 joins partial sums of 1024 tokens. M == 0 writes
+ * dW = 0 (leaves it as it is with accumulate_dW).
+ * workspace: at least bl_int8_linear_backward_workspace_size(M,N,K) bytes,
+ * 16-byte aligned, no initialisation, one call at a time per workspace: x_hat and
+ * w_hat, and fp32 parts of dX where its sums are split.
+ * Errors: as L1, plus BL_ERR_WORKSPACE.
+ */
+size_t bl_int8_linear_backward_workspace_size(int64_t M, int64_t N, int64_t K);
+bl_status bl_int8_linear_backward(const void* dY, const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
+                                  int64_t M, int64_t N, int64_t K, void* dX, void* dW, bl_dtype dw_dtype,
+                                  int accumulate_dW, void* workspace, size_t workspace_bytes, void* stream);
+
+/* A tensor of a list: its device memory, elements and type. The list itself is
+ * in host memory and is read before the call returns. */
+typedef struct bl_tensor {
+    void* data;       /* aligned to its element; may be NULL where numel is 0 */
+    int64_t numel;
+    bl_dtype dtype;
+} bl_tensor;
+
+/*
+ * C1, C2 -- the norm over all of a model's gradients, and the gradients scaled
+ * down to a largest norm (before an AdamW step, say):
+ *
+ *   norm = sqrt(sum over all tensors and elements of g^2)
+ *   out  = round(g * fp32(max_norm / norm)) where norm > max_norm, else g itself
+ *
+ * host_grads: `count` tensors of any sizes, BL_BF16 and BL_F32 mixed at will,
+ * each dense and aligned to its element (views into a packed buffer). host_out:
+ * for each the memory for its clipped values, of the same type, or NULL for
+ * clipping in place; an output is its own gradient's memory or shares memory
+ * with nothing else. norm: one float (device).
+ * Squares are added in fp32 over up to 32 values, in fp64 beyond (wholly in fp64
+ * where fp32 would overflow or vanish), always in the same order; norm is
+ * rounded once, to infinity beyond fp32, with the factor still right. A norm that
+ * is infinite or NaN because a gradient is leaves the gradients as they are: the
+ * caller sees it in norm. max_norm >= 0 (infinity: never clipped).
+ * No tensors, or only empty ones, have a norm of 0.
+ * workspace: at least bl_grad_norm_workspace_size(count) bytes, 16-byte
+ * aligned, no initialisation, one call at a time per workspace.
+ * Limits: 2^20 tensors, 2^40 elements in all.
+ * Errors: BL_ERR_INVALID_ARG (also for outputs that overlap),
+ *         BL_ERR_UNSUPPORTED_SHAPE, BL_ERR_DTYPE, BL_ERR_ALIGNMENT,
+ *         BL_ERR_WORKSPACE, BL_ERR_ARCH, BL_ERR_CUDA.
+ */
+size_t bl_grad_norm_workspace_size(int64_t count);
+bl_status bl_grad_norm(const bl_tensor* host_grads, int64_t count, float* norm, void* workspace, size_t workspace_bytes,
+                       void* stream);
+bl_status bl_clip_grads(const bl_tensor* host_grads, void* const* host_out, int64_t count, double max_norm, float* norm,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Synchronises the current device, then returns BL_OK or the first device
  * failure recorded since the last bl_reset_error (BL_ERR_TIMEOUT).
  */

@@ -68,6 +68,16 @@ SIGNATURES = {
                                 _SZ, _VP]),
     "bl_swiglu_forward": (_I32, [_VP, _VP, _I32, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _VP]),
     "bl_swiglu_backward": (_I32, [_VP, _VP, _VP, _VP, _VP, _I32, _I64, _I64, _VP, _VP, _VP]),
+    "bl_norm_quant_forward": (_I32, [_VP, _I32, _VP, _I32, _VP, _I32, _I64, _I64, ctypes.c_float, _VP, _VP, _VP, _VP, _VP]),
+    "bl_norm_quant_backward_workspace_size": (_SZ, [_I64, _I64]),
+    "bl_norm_quant_backward": (_I32, [_VP, _I32, _VP, _VP, _I32, _VP, _I32, _VP, _I64, _I64, _VP, _VP, _I32, _VP, _I32, _VP,
+                                      _SZ, _VP]),
+    "bl_int8_linear_forward": (_I32, [_VP, _VP, _VP, _VP, _I64, _I64, _I64, _VP, _I32, _VP]),
+    "bl_int8_linear_backward_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "bl_int8_linear_backward": (_I32, [_VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _VP, _VP, _I32, _I32, _VP, _SZ, _VP]),
+    "bl_grad_norm_workspace_size": (_SZ, [_I64]),
+    "bl_grad_norm": (_I32, [_VP, _I64, _VP, _VP, _SZ, _VP]),
+    "bl_clip_grads": (_I32, [_VP, _VP, _I64, ctypes.c_double, _VP, _VP, _SZ, _VP]),
 }
 
 
@@ -579,6 +589,145 @@ def bl_swiglu_backward(dy, gate8: Act8, up8: Act8, dgate, dup, stream=None):
            "bl_swiglu_backward")
 
 
+# ----------------------------------------------------------------- around the 8-bit products; the gradients' norm
+
+def bl_norm_quant_forward(x, residual, weight, eps, sum, rstd, xq, sx, stream=None):
+    """Q1: sum [M,K] = x + residual (of the residual's type; both None: x is the
+    stream), then xq [M,K] int8 and sx [M] f32, the 8-bit form of the RMS norm of
+    sum with gain weight [K] (bf16|f32, may be None); rstd [M] f32 for Q2."""
+    status = _quick().norm_quant_forward(x, residual, weight, eps, sum, rstd, xq, sx, stream)
+    if status is not None:
+        return _check(status, "bl_norm_quant_forward")
+    M, K = x.shape
+    cur = _device(x, "x")
+    dt = _dtype_code(x, "x")
+    stype, sdt = (x.dtype, dt) if residual is None else (residual.dtype, _dtype_code(residual, "residual"))
+    pdt, ptype = (BL_F32, None) if weight is None else (_dtype_code(weight, "weight"), weight.dtype)
+    p = _pointers(cur, ((x, x.dtype, (M, K), "x"), (residual, stype, (M, K), "residual"), (weight, ptype, (K,), "weight"),
+                        (sum, stype, (M, K), "sum"), (rstd, torch.float32, (M,), "rstd"), (xq, torch.int8, (M, K), "xq"),
+                        (sx, torch.float32, (M,), "sx")))
+    _check(load_library().bl_norm_quant_forward(p[0], dt, p[1], sdt, p[2], pdt, M, K, eps, *p[3:], _stream_of(stream, cur)),
+           "bl_norm_quant_forward")
+
+
+def bl_norm_quant_backward_workspace_size(M: int, K: int) -> int:
+    return load_library().bl_norm_quant_backward_workspace_size(M, K)
+
+
+def bl_norm_quant_backward(dy, dsum, sum, weight, rstd, dx=None, dresidual=None, dweight=None, workspace=None,
+                           accumulate=False, stream=None):
+    """Q2: dx [M,K] (of x's type), dresidual [M,K] (of the stream's) and dweight
+    [K] of Q1 (each may be None), given dy [M,K] (bf16|f32) and dsum [M,K], the
+    gradient of the stream behind the addition (None: zero)."""
+    status = _quick().norm_quant_backward(dy, dsum, sum, weight, rstd, dx, dresidual, dweight, workspace, accumulate,
+                                          stream)
+    if status is not None:
+        return _check(status, "bl_norm_quant_backward")
+    M, K = dy.shape
+    cur = _device(dy, "dy")
+    ddt, sdt = _dtype_code(dy, "dy"), _dtype_code(sum, "sum")
+    xdt, xtype = (sdt, None) if dx is None else (_dtype_code(dx, "dx"), dx.dtype)
+    param = weight if weight is not None else dweight
+    pdt, ptype = (BL_F32, None) if param is None else (_dtype_code(param, "weight or dweight"), param.dtype)
+    p = _pointers(cur, ((dy, dy.dtype, (M, K), "dy"), (dsum, sum.dtype, (M, K), "dsum"), (sum, sum.dtype, (M, K), "sum"),
+                        (weight, ptype, (K,), "weight"), (rstd, torch.float32, (M,), "rstd"), (dx, xtype, (M, K), "dx"),
+                        (dresidual, sum.dtype, (M, K), "dresidual"), (dweight, ptype, (K,), "dweight")))
+    ws, n = _scratch(cur, workspace)
+    _check(load_library().bl_norm_quant_backward(p[0], ddt, p[1], p[2], sdt, p[3], pdt, p[4], M, K, p[6], p[5], xdt, p[7],
+                                                 1 if accumulate else 0, ws, n, _stream_of(stream, cur)),
+           "bl_norm_quant_backward")
+
+
+def bl_int8_linear_forward(xq, sx, wq, sw, y, stream=None):
+    """L1: y [M,N] (bf16|f32) = (xq [M,K] . wq [N,K]^T) * sx [M] * sw [N], the codes int8."""
+    status = _quick().int8_linear_forward(xq, sx, wq, sw, y, stream)
+    if status is not None:
+        return _check(status, "bl_int8_linear_forward")
+    M, K = xq.shape
+    N = wq.shape[0]
+    cur = _device(xq, "xq")
+    dt = _dtype_code(y, "y")
+    p = _pointers(cur, ((xq, torch.int8, (M, K), "xq"), (sx, torch.float32, (M,), "sx"), (wq, torch.int8, (N, K), "wq"),
+                        (sw, torch.float32, (N,), "sw"), (y, y.dtype, (M, N), "y")))
+    _check(load_library().bl_int8_linear_forward(*p[:4], M, N, K, p[4], dt, _stream_of(stream, cur)),
+           "bl_int8_linear_forward")
+
+
+def bl_int8_linear_backward_workspace_size(M: int, N: int, K: int) -> int:
+    return load_library().bl_int8_linear_backward_workspace_size(M, N, K)
+
+
+def bl_int8_linear_backward(dY, xq, sx, wq, sw, dX=None, dW=None, accumulate_dW=False, stream=None, workspace=None):
+    """L2: dX [M,K] bf16 and dW [N,K] (bf16|f32) of L1 (each may be None), given
+    dY [M,N] bf16; the operands' codes taken straight through as their values."""
+    status = _quick().int8_linear_backward(dY, xq, sx, wq, sw, dX, dW, accumulate_dW, stream, workspace)
+    if status is not None:
+        return _check(status, "bl_int8_linear_backward")
+    M, N = dY.shape
+    K = xq.shape[1]
+    cur = _device(dY, "dY")
+    dwdt, wtype = (BL_BF16, None) if dW is None else (_dtype_code(dW, "dW"), dW.dtype)
+    p = _pointers(cur, ((dY, torch.bfloat16, (M, N), "dY"), (xq, torch.int8, (M, K), "xq"), (sx, torch.float32, (M,), "sx"),
+                        (wq, torch.int8, (N, K), "wq"), (sw, torch.float32, (N,), "sw"),
+                        (dX, torch.bfloat16, (M, K), "dX"), (dW, wtype, (N, K), "dW")))
+    ws, n = _scratch(cur, workspace)
+    _check(load_library().bl_int8_linear_backward(*p[:5], M, N, K, p[5], p[6], dwdt, 1 if accumulate_dW else 0, ws, n,
+                                                  _stream_of(stream, cur)), "bl_int8_linear_backward")
+
+
+class _Tensor(ctypes.Structure):
+    _fields_ = [("data", _VP), ("numel", _I64), ("dtype", _I32)]
+
+
+def bl_grad_norm_workspace_size(count: int) -> int:
+    return load_library().bl_grad_norm_workspace_size(count)
+
+
+def _tensor_list(cur, tensors, name):
+    """The bl_tensor array of a list of tensors of any shapes (bf16|f32)."""
+    out = (_Tensor * max(len(tensors), 1))()
+    for i, t in enumerate(tensors):
+        dt = _dtype_code(t, f"{name}[{i}]")
+        address, = _pointers(cur, ((t, t.dtype, t.shape, f"{name}[{i}]"),))
+        out[i] = _Tensor(address, t.numel(), dt)
+    return out
+
+
+def bl_grad_norm(grads, norm, workspace, stream=None):
+    """C1: norm [1] f32 = the 2-norm over all of grads, a list of tensors of any
+    shapes (bf16|f32, mixed at will)."""
+    status = _quick().grad_norm(grads, norm, workspace, stream)
+    if status is not None:
+        return _check(status, "bl_grad_norm")
+    grads = list(grads)
+    cur = _device(norm, "norm")
+    p = _pointers(cur, ((norm, torch.float32, (1,), "norm"),))
+    ws, n = _scratch(cur, workspace)
+    _check(load_library().bl_grad_norm(_tensor_list(cur, grads, "grads"), len(grads), p[0], ws, n, _stream_of(stream, cur)),
+           "bl_grad_norm")
+
+
+def bl_clip_grads(grads, max_norm, norm, workspace, out=None, stream=None):
+    """C2: norm [1] f32 as C1, and grads scaled by max_norm / norm where norm is
+    above max_norm: in place, or into out, a list of tensors like grads."""
+    status = _quick().clip_grads(grads, max_norm, norm, workspace, out, stream)
+    if status is not None:
+        return _check(status, "bl_clip_grads")
+    grads = list(grads)
+    cur = _device(norm, "norm")
+    p = _pointers(cur, ((norm, torch.float32, (1,), "norm"),))
+    ws, n = _scratch(cur, workspace)
+    tensors, to = _tensor_list(cur, grads, "grads"), None
+    if out is not None:
+        out = list(out)
+        if len(out) != len(grads):
+            raise ValueError(f"out has {len(out)} tensors, grads {len(grads)}")
+        to = (_VP * max(len(out), 1))(*_pointers(cur, [(o, g.dtype, g.shape, f"out[{i}]")
+                                                       for i, (o, g) in enumerate(zip(out, grads))]))
+    _check(load_library().bl_clip_grads(tensors, to, len(grads), max_norm, p[0], ws, n, _stream_of(stream, cur)),
+           "bl_clip_grads")
+
+
 @dataclass
 class XentBuffers:
     """Device buffers of X1 and (backward) X2 (caller-owned, reused); one
@@ -643,6 +792,52 @@ class SwigluBuffers:
             return torch.empty((M, K), dtype=dtype, device=device)
         return SwigluBuffers(y=empty(), gate8=Act8.allocate(M, K, device), up8=Act8.allocate(M, K, device),
                              dgate=empty(), dup=empty())
+
+
+@dataclass
+class NormQuantBuffers:
+    """Device buffers of Q1 and (backward) Q2 (caller-owned, reused). dx is there
+    where x has another type than the stream; else dresidual serves both."""
+    sum: torch.Tensor
+    rstd: torch.Tensor
+    xq: torch.Tensor
+    sx: torch.Tensor
+    dx: torch.Tensor | None = None
+    dresidual: torch.Tensor | None = None
+    dweight: torch.Tensor | None = None
+    workspace: torch.Tensor | None = None
+
+    @staticmethod
+    def allocate(M, K, x_dtype=torch.bfloat16, s_dtype=torch.bfloat16, p_dtype=torch.float32, backward=True,
+                 device="cuda"):
+        def empty(shape, dt):
+            return torch.empty(shape, dtype=dt, device=device)
+        b = NormQuantBuffers(sum=empty((M, K), s_dtype), rstd=empty(M, torch.float32), xq=empty((M, K), torch.int8),
+                             sx=empty(M, torch.float32))
+        if backward:
+            b.dx = empty((M, K), x_dtype) if x_dtype != s_dtype else None
+            b.dresidual, b.dweight = empty((M, K), s_dtype), empty(K, p_dtype)
+            b.workspace = empty(max(bl_norm_quant_backward_workspace_size(M, K), 16), torch.uint8)
+        return b
+
+
+@dataclass
+class Int8LinearBuffers:
+    """Device buffers of L1 and (backward) L2 (caller-owned, reused)."""
+    y: torch.Tensor
+    dX: torch.Tensor | None = None
+    dW: torch.Tensor | None = None
+    workspace: torch.Tensor | None = None
+
+    @staticmethod
+    def allocate(M, N, K, y_dtype=torch.bfloat16, dw_dtype=torch.bfloat16, backward=True, device="cuda"):
+        def empty(shape, dt):
+            return torch.empty(shape, dtype=dt, device=device)
+        b = Int8LinearBuffers(y=empty((M, N), y_dtype))
+        if backward:
+            b.dX, b.dW = empty((M, K), torch.bfloat16), empty((N, K), dw_dtype)
+            b.workspace = empty(max(bl_int8_linear_backward_workspace_size(M, N, K), 16), torch.uint8)
+        return b
 
 
 # ----------------------------------------------------------------- one whole step

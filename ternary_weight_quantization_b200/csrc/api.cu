@@ -3,9 +3,12 @@
 // write on timeout. See include/bitlinear.h for the contract of each call.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
+#include <memory>
+#include <new>
 
 #include "../../include/bitlinear.h"
 #include "bl_internal.h"
@@ -66,6 +69,71 @@ bl_status cuda_status(cudaError_t e, const char* what) {
   bl_status s = fail(BL_ERR_CUDA, "%s: %s%s%s", what, cudaGetErrorString(e), detail[0] ? "; " : "", detail);
   bl::clear_launch_detail();
   return s;
+}
+
+// Memory that a clipped gradient is written to.
+struct Span {
+  uintptr_t b, e;
+  bool operator<(const Span& o) const { return b < o.b; }
+};
+
+// The list as the launches take it. `host_out` null: in place.
+bl_status tensor_list(const bl_tensor* x, void* const* host_out, int64_t count, bool write, bl::ClipTensor* out, Span* spans) {
+  int64_t total = 0, nspans = 0;
+  bool moved = false;
+  for (int64_t i = 0; i < count; ++i) {
+    const bl_tensor& t = x[i];
+    if (t.dtype != BL_BF16 && t.dtype != BL_F32) return fail(BL_ERR_DTYPE, "dtype %d of tensor %lld", (int)t.dtype, (long long)i);
+    if (t.numel < 0) return fail(BL_ERR_INVALID_ARG, "tensor %lld has %lld elements", (long long)i, (long long)t.numel);
+    if (t.numel > (int64_t(1) << 40) - total)
+      return fail(BL_ERR_UNSUPPORTED_SHAPE, "more than 2^40 elements (at tensor %lld)", (long long)i);
+    total += t.numel;
+    void* to = !write ? nullptr : host_out ? host_out[i] : t.data;
+    out[i] = {t.data, to, t.numel, t.dtype == BL_F32};
+    if (t.numel == 0) continue;
+    const uintptr_t size = t.dtype == BL_F32 ? 4 : 2;
+    if (!t.data || (write && !to)) return fail(BL_ERR_INVALID_ARG, "null pointer (tensor %lld)", (long long)i);
+    if (reinterpret_cast<uintptr_t>(t.data) % size != 0 || reinterpret_cast<uintptr_t>(to) % size != 0)
+      return fail(BL_ERR_ALIGNMENT, "tensor %lld starts inside an element", (long long)i);
+    if (!write) continue;
+    moved = moved || to != t.data;
+    const uintptr_t b = reinterpret_cast<uintptr_t>(to);
+    spans[nspans++] = {b, b + static_cast<uintptr_t>(t.numel) * size};
+  }
+  if (!write) return BL_OK;
+  std::sort(spans, spans + nspans);
+  for (int64_t i = 1; i < nspans; ++i)
+    if (spans[i].b < spans[i - 1].e) return fail(BL_ERR_INVALID_ARG, "two tensors are written to the same memory");
+  // an input may share memory with its own output, from the same place, and with no other
+  for (int64_t i = 0; moved && i < count; ++i) {
+    if (x[i].numel == 0) continue;
+    const uintptr_t b = reinterpret_cast<uintptr_t>(x[i].data), e = b + static_cast<uintptr_t>(x[i].numel) * (out[i].f32 ? 4 : 2);
+    const Span* s = std::upper_bound(spans, spans + nspans, Span{b, e});
+    if (s > spans && s[-1].e > b) --s;
+    for (; s < spans + nspans && s->b < e; ++s)
+      if (out[i].in != out[i].out || s->b != b)
+        return fail(BL_ERR_INVALID_ARG, "tensor %lld overlaps what is written", (long long)i);
+  }
+  return BL_OK;
+}
+
+bl_status clip(const bl_tensor* host_grads, void* const* host_out, int64_t count, bool write, double most, float* norm,
+               void* workspace, size_t workspace_bytes, void* stream, const char* what) {
+  if (count < 0 || (count > 0 && !host_grads)) return fail(BL_ERR_INVALID_ARG, "count=%lld, or no list", (long long)count);
+  if (count > (int64_t(1) << 20)) return fail(BL_ERR_UNSUPPORTED_SHAPE, "more than 2^20 tensors");
+  if (write && !(most >= 0.0)) return fail(BL_ERR_INVALID_ARG, "max_norm must be >= 0");
+  if (!norm) return fail(BL_ERR_INVALID_ARG, "null pointer");
+  if (reinterpret_cast<uintptr_t>(norm) % 4 != 0) return fail(BL_ERR_ALIGNMENT, "norm must be 4-byte aligned");
+  std::unique_ptr<bl::ClipTensor[]> list(new (std::nothrow) bl::ClipTensor[count + 1]);
+  std::unique_ptr<Span[]> spans(new (std::nothrow) Span[write ? count + 1 : 1]);
+  if (!list || !spans) return fail(BL_ERR_INVALID_ARG, "no host memory for a list of %lld", (long long)count);
+  if (bl_status s = tensor_list(host_grads, host_out, count, write, list.get(), spans.get())) return s;
+  const size_t need = bl::grad_norm_workspace_bytes(count);
+  if (count > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+    return fail(BL_ERR_WORKSPACE, "workspace needs %zu bytes, 16-byte aligned", need);
+  int* err = nullptr;
+  if (bl_status s = current_device(&err)) return s;
+  return cuda_status(bl::launch_clip(list.get(), count, norm, most, write, workspace, static_cast<cudaStream_t>(stream)), what);
 }
 
 }  // namespace
@@ -537,6 +605,147 @@ bl_status bl_swiglu_backward(const void* dy, const int8_t* gate_codes, const flo
   return cuda_status(bl::launch_swiglu_backward(dy, gate_codes, gate_scales, up_codes, up_scales, x_dtype == BL_F32, M,
                                                 K, dgate, dup, static_cast<cudaStream_t>(stream)),
                      "bl_swiglu_backward launch");
+}
+
+// Shapes and types of the norm with an INT8 result (Q1, Q2).
+static bl_status check_norm_quant(int64_t M, int64_t K, bl_dtype x_dtype, bl_dtype s_dtype, bl_dtype p_dtype) {
+  if (M < 0) return fail(BL_ERR_INVALID_ARG, "M=%lld must be >= 0", (long long)M);
+  if (K < 8 || K % 8 != 0 || K > bl::kNormQuantMaxK)
+    return fail(BL_ERR_UNSUPPORTED_SHAPE, "K=%lld must be a multiple of 8 from 8 to %lld", (long long)K,
+                (long long)bl::kNormQuantMaxK);
+  if (M > (int64_t(1) << 30)) return fail(BL_ERR_UNSUPPORTED_SHAPE, "M=%lld too large", (long long)M);
+  if (x_dtype != BL_BF16 && x_dtype != BL_F32) return fail(BL_ERR_DTYPE, "x_dtype %d", (int)x_dtype);
+  if (s_dtype != BL_BF16 && s_dtype != BL_F32) return fail(BL_ERR_DTYPE, "s_dtype %d", (int)s_dtype);
+  if (p_dtype != BL_BF16 && p_dtype != BL_F32) return fail(BL_ERR_DTYPE, "p_dtype %d", (int)p_dtype);
+  if (x_dtype == BL_F32 && s_dtype == BL_BF16) return fail(BL_ERR_DTYPE, "an fp32 x with a bf16 residual stream");
+  return BL_OK;
+}
+
+bl_status bl_norm_quant_forward(const void* x, bl_dtype x_dtype, const void* residual, bl_dtype s_dtype,
+                                const void* weight, bl_dtype p_dtype, int64_t M, int64_t K, float eps, void* sum,
+                                float* rstd, int8_t* xq, float* sx, void* stream) {
+  g_msg[0] = 0;
+  if (bl_status s = check_norm_quant(M, K, x_dtype, s_dtype, p_dtype)) return s;
+  if (!(eps - eps == 0.0f) || eps < 0.0f) return fail(BL_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (M == 0) return BL_OK;
+  if (!x || !rstd || !xq || !sx) return fail(BL_ERR_INVALID_ARG, "null pointer");
+  if ((residual == nullptr) != (sum == nullptr)) return fail(BL_ERR_INVALID_ARG, "residual and sum go together");
+  if (!residual && x_dtype != s_dtype) return fail(BL_ERR_DTYPE, "without a residual x is the stream: s_dtype must be x_dtype");
+  if (!aligned16(x) || (residual && !aligned16(residual)) || (weight && !aligned16(weight)) || (sum && !aligned16(sum)) ||
+      !aligned16(rstd) || !aligned16(xq) || !aligned16(sx))
+    return fail(BL_ERR_ALIGNMENT, "tensors must be 16-byte aligned");
+  int* err = nullptr;
+  if (bl_status s = current_device(&err)) return s;
+  return cuda_status(bl::launch_norm_quant_forward(x, x_dtype == BL_F32, residual, s_dtype == BL_F32, weight,
+                                                   p_dtype == BL_F32, M, K, eps, sum, rstd, xq, sx,
+                                                   static_cast<cudaStream_t>(stream)),
+                     "bl_norm_quant_forward launch");
+}
+
+size_t bl_norm_quant_backward_workspace_size(int64_t M, int64_t K) {
+  g_msg[0] = 0;
+  if (M == 0 || check_norm_quant(M, K, BL_BF16, BL_BF16, BL_BF16) != BL_OK) return 0;
+  return bl::norm_quant_backward_workspace_bytes(K);
+}
+
+bl_status bl_norm_quant_backward(const void* dy, bl_dtype dy_dtype, const void* dsum, const void* sum, bl_dtype s_dtype,
+                                 const void* weight, bl_dtype p_dtype, const float* rstd, int64_t M, int64_t K,
+                                 void* dresidual, void* dx, bl_dtype x_dtype, void* dweight, int accumulate,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  g_msg[0] = 0;
+  if (bl_status s = check_norm_quant(M, K, x_dtype, s_dtype, p_dtype)) return s;
+  if (dy_dtype != BL_BF16 && dy_dtype != BL_F32) return fail(BL_ERR_DTYPE, "dy_dtype %d", (int)dy_dtype);
+  if (!dresidual && !dx && !dweight) return BL_OK;
+  if (M == 0 && (!dweight || accumulate)) return BL_OK;
+  if (M > 0 && (!dy || !sum || !rstd)) return fail(BL_ERR_INVALID_ARG, "null pointer");
+  if (M > 0 && dx && dx == dresidual) return fail(BL_ERR_INVALID_ARG, "dx and dresidual are the same memory");
+  if ((dy && !aligned16(dy)) || (dsum && !aligned16(dsum)) || (sum && !aligned16(sum)) ||
+      (weight && !aligned16(weight)) || (rstd && !aligned16(rstd)) || (dresidual && !aligned16(dresidual)) ||
+      (dx && !aligned16(dx)) || (dweight && !aligned16(dweight)))
+    return fail(BL_ERR_ALIGNMENT, "tensors must be 16-byte aligned");
+  const size_t need = bl_norm_quant_backward_workspace_size(M, K);
+  if (M > 0 && dweight && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+    return fail(BL_ERR_WORKSPACE, "workspace needs %zu bytes, 16-byte aligned", need);
+  int* err = nullptr;
+  if (bl_status s = current_device(&err)) return s;
+  return cuda_status(bl::launch_norm_quant_backward(dy, dy_dtype == BL_F32, dsum, sum, s_dtype == BL_F32, weight,
+                                                    p_dtype == BL_F32, rstd, M, K, dresidual, dx, x_dtype == BL_F32,
+                                                    dweight, accumulate != 0, workspace,
+                                                    static_cast<cudaStream_t>(stream)),
+                     "bl_norm_quant_backward launch");
+}
+
+// Shape limits of the product of INT8 operands (its INT32 sums, tile counts and
+// tensor-map coordinates fit within them).
+static bl_status check_int8(int64_t M, int64_t N, int64_t K) {
+  if (M < 0 || N < 1) return fail(BL_ERR_INVALID_ARG, "M=%lld, N=%lld", (long long)M, (long long)N);
+  if (K < 16 || K % 16 != 0 || K > 65536)
+    return fail(BL_ERR_UNSUPPORTED_SHAPE, "K=%lld must be a multiple of 16 from 16 to 65536", (long long)K);
+  if (M > 131072 || N > (int64_t(1) << 20))
+    return fail(BL_ERR_UNSUPPORTED_SHAPE, "M=%lld above 131072 or N=%lld above 2^20", (long long)M, (long long)N);
+  return BL_OK;
+}
+
+bl_status bl_int8_linear_forward(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw, int64_t M,
+                                 int64_t N, int64_t K, void* y, bl_dtype y_dtype, void* stream) {
+  g_msg[0] = 0;
+  if (bl_status s = check_int8(M, N, K)) return s;
+  if (y_dtype != BL_BF16 && y_dtype != BL_F32) return fail(BL_ERR_DTYPE, "y_dtype %d", (int)y_dtype);
+  if (M == 0) return BL_OK;
+  if (!xq || !sx || !wq || !sw || !y) return fail(BL_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(xq) || !aligned16(sx) || !aligned16(wq) || !aligned16(sw) || !aligned16(y))
+    return fail(BL_ERR_ALIGNMENT, "tensors must be 16-byte aligned");
+  int* err = nullptr;
+  if (bl_status s = current_device(&err)) return s;
+  return cuda_status(bl::launch_int8_forward(xq, sx, wq, sw, M, N, K, y, y_dtype == BL_F32, err,
+                                             static_cast<cudaStream_t>(stream)),
+                     "bl_int8_linear_forward launch");
+}
+
+size_t bl_int8_linear_backward_workspace_size(int64_t M, int64_t N, int64_t K) {
+  g_msg[0] = 0;
+  if (M == 0 || N % 8 != 0 || check_int8(M, N, K) != BL_OK) return 0;
+  return bl::int8_backward_workspace_bytes(M, N, K);
+}
+
+bl_status bl_int8_linear_backward(const void* dY, const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
+                                  int64_t M, int64_t N, int64_t K, void* dX, void* dW, bl_dtype dw_dtype,
+                                  int accumulate_dW, void* workspace, size_t workspace_bytes, void* stream) {
+  g_msg[0] = 0;
+  if (bl_status s = check_int8(M, N, K)) return s;
+  if (N % 8 != 0) return fail(BL_ERR_UNSUPPORTED_SHAPE, "N=%lld must be a multiple of 8 in the backward", (long long)N);
+  if (dw_dtype != BL_BF16 && dw_dtype != BL_F32) return fail(BL_ERR_DTYPE, "dw_dtype %d", (int)dw_dtype);
+  if (!dX && !dW) return BL_OK;
+  if (M == 0 && (!dW || accumulate_dW)) return BL_OK;
+  if (M > 0 && (!dY || !xq || !sx || !wq || !sw)) return fail(BL_ERR_INVALID_ARG, "null pointer");
+  if ((dY && !aligned16(dY)) || (xq && !aligned16(xq)) || (sx && !aligned16(sx)) || (wq && !aligned16(wq)) ||
+      (sw && !aligned16(sw)) || (dX && !aligned16(dX)) || (dW && !aligned16(dW)))
+    return fail(BL_ERR_ALIGNMENT, "tensors must be 16-byte aligned");
+  const size_t need = bl_int8_linear_backward_workspace_size(M, N, K);
+  if (M > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+    return fail(BL_ERR_WORKSPACE, "workspace needs %zu bytes, 16-byte aligned", need);
+  int* err = nullptr;
+  if (bl_status s = current_device(&err)) return s;
+  return cuda_status(bl::launch_int8_backward(dY, xq, sx, wq, sw, M, N, K, dX, dW, dw_dtype == BL_F32,
+                                              accumulate_dW != 0, workspace, err, static_cast<cudaStream_t>(stream)),
+                     "bl_int8_linear_backward launch");
+}
+
+size_t bl_grad_norm_workspace_size(int64_t count) {
+  g_msg[0] = 0;
+  return count < 1 || count > (int64_t(1) << 20) ? 0 : bl::grad_norm_workspace_bytes(count);
+}
+
+bl_status bl_grad_norm(const bl_tensor* host_grads, int64_t count, float* norm, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  g_msg[0] = 0;
+  return clip(host_grads, nullptr, count, false, 0.0, norm, workspace, workspace_bytes, stream, "bl_grad_norm launch");
+}
+
+bl_status bl_clip_grads(const bl_tensor* host_grads, void* const* host_out, int64_t count, double max_norm, float* norm,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  g_msg[0] = 0;
+  return clip(host_grads, host_out, count, true, max_norm, norm, workspace, workspace_bytes, stream, "bl_clip_grads launch");
 }
 
 bl_status bl_selftest_timeout(void* stream) {

@@ -17,6 +17,7 @@
 
 #include <cstdint>
 #include <initializer_list>
+#include <vector>
 
 #include "../../include/bitlinear.h"
 
@@ -117,6 +118,61 @@ struct Call {
       ok = false;
     }
     return static_cast<float>(v);
+  }
+
+  double real(int i) {
+    const double v = PyFloat_AsDouble(args[i]);
+    if (v == -1.0 && PyErr_Occurred()) {
+      PyErr_Clear();
+      ok = false;
+    }
+    return v;
+  }
+
+  // The dense bf16 and fp32 tensors of the list or tuple at i, on the call's
+  // device (that of a tensor read before).
+  std::vector<bl_tensor> list(int i) {
+    std::vector<bl_tensor> out;
+    if (!ok || !(PyList_Check(args[i]) || PyTuple_Check(args[i]))) {
+      ok = false;
+      return out;
+    }
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(args[i]);
+    PyObject** items = PySequence_Fast_ITEMS(args[i]);
+    out.reserve(static_cast<size_t>(n));
+    for (Py_ssize_t j = 0; j < n; ++j) {
+      if (!THPVariable_Check(items[j])) {
+        ok = false;
+        return out;
+      }
+      const at::Tensor& t = THPVariable_Unpack(items[j]);
+      const ScalarType type = t.scalar_type();
+      if (!t.is_cuda() || t.layout() != at::kStrided || !t.is_contiguous() || t.get_device() != device ||
+          (type != at::kBFloat16 && type != at::kFloat)) {
+        ok = false;
+        return out;
+      }
+      out.push_back({t.data_ptr(), t.numel(), type == at::kFloat ? BL_F32 : BL_BF16});
+    }
+    return out;
+  }
+
+  // Addresses of the list at i, whose tensors have the shapes and types of those
+  // at `like`.
+  std::vector<void*> matching(int i, int like, const std::vector<bl_tensor>& of) {
+    std::vector<void*> out;
+    const std::vector<bl_tensor> mine = list(i);
+    if (!ok || mine.size() != of.size()) {
+      ok = false;
+      return out;
+    }
+    PyObject** a = PySequence_Fast_ITEMS(args[i]);
+    PyObject** b = PySequence_Fast_ITEMS(args[like]);
+    for (size_t j = 0; j < of.size(); ++j) {
+      if (mine[j].dtype != of[j].dtype || THPVariable_Unpack(a[j]).sizes() != THPVariable_Unpack(b[j]).sizes()) ok = false;
+      out.push_back(mine[j].data);
+    }
+    return out;
   }
 
   // The call's stream: none given, the current one of the device. (A given
@@ -302,12 +358,129 @@ PyObject* swiglu_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+// x, residual, weight, eps, sum, rstd, xq, sx, stream
+PyObject* norm_quant_forward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return run<9>(args, n, [](Call& c, bl_status* status) {
+    int64_t M = 0, K = 0;
+    const ScalarType xt = c.matrix(0, &M, &K);
+    const ScalarType st = c.none(1) ? xt : c.first_type({1});
+    const ScalarType pt = c.first_type({2});
+    void* x = c.ptr(0, xt, {M, K});
+    void* r = c.ptr(1, st, {M, K}, true);
+    void* w = c.ptr(2, pt, {K}, true);
+    const float eps = c.number(3);
+    void* sum = c.ptr(4, st, {M, K}, true);
+    auto* rstd = static_cast<float*>(c.ptr(5, at::kFloat, {M}));
+    auto* xq = static_cast<int8_t*>(c.ptr(6, at::kChar, {M, K}));
+    auto* sx = static_cast<float*>(c.ptr(7, at::kFloat, {M}));
+    void* stream = c.stream(8);
+    BL_CALL(bl_norm_quant_forward(x, code(xt), r, code(st), w, code(pt), M, K, eps, sum, rstd, xq, sx, stream));
+  });
+}
+
+// dy, dsum, sum, weight, rstd, dx, dresidual, dweight, workspace, accumulate, stream
+PyObject* norm_quant_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return run<11>(args, n, [](Call& c, bl_status* status) {
+    int64_t M = 0, K = 0;
+    const ScalarType dt = c.matrix(0, &M, &K);
+    const ScalarType st = c.none(2) ? at::kFloat : c.first_type({2});
+    const ScalarType xt = c.none(5) ? st : c.first_type({5});
+    const ScalarType pt = c.first_type({3, 7});
+    void* dy = c.ptr(0, dt, {M, K});
+    void* ds = c.ptr(1, st, {M, K}, true);
+    void* sum = c.ptr(2, st, {M, K});
+    void* w = c.ptr(3, pt, {K}, true);
+    auto* rstd = static_cast<float*>(c.ptr(4, at::kFloat, {M}));
+    void* dx = c.ptr(5, xt, {M, K}, true);
+    void* dr = c.ptr(6, st, {M, K}, true);
+    void* dw = c.ptr(7, pt, {K}, true);
+    size_t bytes;
+    void* ws = c.scratch(8, &bytes);
+    const int acc = c.flag(9);
+    void* stream = c.stream(10);
+    BL_CALL(bl_norm_quant_backward(dy, code(dt), ds, sum, code(st), w, code(pt), rstd, M, K, dr, dx, code(xt), dw, acc, ws,
+                                   bytes, stream));
+  });
+}
+
+// xq, sx, wq, sw, y, stream
+PyObject* int8_linear_forward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return run<6>(args, n, [](Call& c, bl_status* status) {
+    int64_t M = 0, N = 0, K = 0;
+    const ScalarType yt = c.matrix(4, &M, &N);
+    const at::Tensor* q = c.tensor(0);
+    if (!q || q->dim() != 2) return false;
+    K = q->size(1);
+    auto* xq = static_cast<int8_t*>(c.ptr(0, at::kChar, {M, K}));
+    auto* sx = static_cast<float*>(c.ptr(1, at::kFloat, {M}));
+    auto* wq = static_cast<int8_t*>(c.ptr(2, at::kChar, {N, K}));
+    auto* sw = static_cast<float*>(c.ptr(3, at::kFloat, {N}));
+    void* y = c.ptr(4, yt, {M, N});
+    void* stream = c.stream(5);
+    BL_CALL(bl_int8_linear_forward(xq, sx, wq, sw, M, N, K, y, code(yt), stream));
+  });
+}
+
+// dY, xq, sx, wq, sw, dX, dW, accumulate_dW, stream, workspace
+PyObject* int8_linear_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return run<10>(args, n, [](Call& c, bl_status* status) {
+    int64_t M = 0, N = 0, K = 0;
+    c.matrix(0, &M, &N);
+    const at::Tensor* q = c.tensor(1);
+    if (!q || q->dim() != 2) return false;
+    K = q->size(1);
+    void* dY = c.ptr(0, at::kBFloat16, {M, N});
+    auto* xq = static_cast<int8_t*>(c.ptr(1, at::kChar, {M, K}));
+    auto* sx = static_cast<float*>(c.ptr(2, at::kFloat, {M}));
+    auto* wq = static_cast<int8_t*>(c.ptr(3, at::kChar, {N, K}));
+    auto* sw = static_cast<float*>(c.ptr(4, at::kFloat, {N}));
+    void* dX = c.ptr(5, at::kBFloat16, {M, K}, true);
+    const ScalarType wt = c.none(6) ? at::kBFloat16 : c.first_type({6});
+    void* dW = c.ptr(6, wt, {N, K}, true);
+    const int acc = c.flag(7);
+    void* stream = c.stream(8);
+    size_t bytes;
+    void* ws = c.scratch(9, &bytes);
+    BL_CALL(bl_int8_linear_backward(dY, xq, sx, wq, sw, M, N, K, dX, dW, code(wt), acc, ws, bytes, stream));
+  });
+}
+
+// grads, norm, workspace, stream
+PyObject* grad_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return run<4>(args, n, [](Call& c, bl_status* status) {
+    auto* norm = static_cast<float*>(c.ptr(1, at::kFloat, {1}));
+    const std::vector<bl_tensor> grads = c.list(0);
+    size_t bytes;
+    void* ws = c.scratch(2, &bytes);
+    void* stream = c.stream(3);
+    BL_CALL(bl_grad_norm(grads.data(), static_cast<int64_t>(grads.size()), norm, ws, bytes, stream));
+  });
+}
+
+// grads, max_norm, norm, workspace, out, stream
+PyObject* clip_grads(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return run<6>(args, n, [](Call& c, bl_status* status) {
+    auto* norm = static_cast<float*>(c.ptr(2, at::kFloat, {1}));
+    const std::vector<bl_tensor> grads = c.list(0);
+    const double most = c.real(1);
+    std::vector<void*> out;
+    if (c.ok && !c.none(4)) out = c.matching(4, 0, grads);
+    void* const* to = c.none(4) ? nullptr : out.data();
+    size_t bytes;
+    void* ws = c.scratch(3, &bytes);
+    void* stream = c.stream(5);
+    BL_CALL(bl_clip_grads(grads.data(), to, static_cast<int64_t>(grads.size()), most, norm, ws, bytes, stream));
+  });
+}
+
 #define BL_METHOD(name) \
   { #name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL, nullptr }
 
 PyMethodDef methods[] = {
     BL_METHOD(xent_forward), BL_METHOD(xent_backward), BL_METHOD(act8_encode),    BL_METHOD(act8_decode),
     BL_METHOD(norm_forward), BL_METHOD(norm_backward), BL_METHOD(swiglu_forward), BL_METHOD(swiglu_backward),
+    BL_METHOD(norm_quant_forward),  BL_METHOD(norm_quant_backward),  BL_METHOD(int8_linear_forward),
+    BL_METHOD(int8_linear_backward), BL_METHOD(grad_norm), BL_METHOD(clip_grads),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -161,6 +161,53 @@ cudaError_t launch_norm_backward(const void* dy, const void* x, const int8_t* co
                                  int64_t K, int rms, void* dx, void* dweight, void* dbias, int accumulate,
                                  void* workspace, cudaStream_t s);
 
+// dweight, dbias [K] (either may be null) from nparts (at most kPlanSms) partial
+// rows, parts [nparts][2][K], added in a fixed order (k_norm.cu).
+cudaError_t launch_norm_join(const float* parts, int nparts, int K, void* dweight, void* dbias, int p_f32,
+                             int accumulate, cudaStream_t s);
+
+// RMS norm with the residual's addition and an INT8 result (k_norm_quant.cu).
+// f32 flags: x, the residual stream, the gain, dy.
+constexpr int64_t kNormQuantMaxK = 8192;
+size_t norm_quant_backward_workspace_bytes(int64_t K);
+cudaError_t launch_norm_quant_forward(const void* x, int x_f32, const void* residual, int s_f32, const void* weight,
+                                      int p_f32, int64_t M, int64_t K, float eps, void* sum, float* rstd, int8_t* xq,
+                                      float* sx, cudaStream_t s);
+cudaError_t launch_norm_quant_backward(const void* dy, int dy_f32, const void* dsum, const void* sum, int s_f32,
+                                       const void* weight, int p_f32, const float* rstd, int64_t M, int64_t K,
+                                       void* dresidual, void* dx, int x_f32, void* dweight, int accumulate,
+                                       void* workspace, cudaStream_t s);
+
+// Product of INT8 operands with a scale per token and channel (k_int8.cu), and
+// its straight-through gradients. The backward's workspace holds both
+// operands' values in bf16, a factor of 1 and, where dX's sums are split, their
+// fp32 parts.
+cudaError_t launch_int8_forward(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw, int64_t M,
+                                int64_t N, int64_t K, void* y, int y_f32, int* err, cudaStream_t s);
+size_t int8_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
+cudaError_t launch_int8_backward(const void* dY, const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
+                                 int64_t M, int64_t N, int64_t K, void* dX, void* dW, int dw_is_f32, int accumulate,
+                                 void* workspace, int* err, cudaStream_t s);
+
+// The gradients of y = x w^T in bf16 operands, dX = dY w and dW = dY^T x, by the
+// products of the head's backward (k_xent.cu). one: a device float of value 1.
+// sums: linear_grad_sum_bytes of scratch.
+size_t linear_grad_sum_bytes(int64_t M, int64_t N, int64_t K);
+cudaError_t launch_linear_grads(const void* dY, const void* x, const void* w, int64_t M, int64_t N, int64_t K, void* dX,
+                                void* dW, int dw_is_f32, int accumulate, float* one, float* sums, int* err,
+                                cudaStream_t s);
+
+// The norm over many tensors, and their scaled copies (k_clip.cu).
+struct ClipTensor {
+  const void* in;
+  void* out;  // null: the norm alone
+  int64_t n;
+  int f32;
+};
+size_t grad_norm_workspace_bytes(int64_t count);
+cudaError_t launch_clip(const ClipTensor* tensors, int64_t count, float* norm, double most, int clip, void* workspace,
+                        cudaStream_t s);
+
 // One warp waiting on an mbarrier that is never completed (bounded wait test).
 cudaError_t launch_selftest_timeout(int* err, cudaStream_t s);
 

@@ -980,6 +980,22 @@ constexpr int64_t kPieceBytes = int64_t(128) << 20;
 constexpr int kPlanPairs = kPlanSms / 2;
 constexpr int kF32Tokens = 1024;  // tokens per partial sum of an fp32 dW
 
+// dH has few tiles, each with the whole piece to sum over, next to dW's many
+// with the tokens (wkb k-blocks each): its reduction is cut into slices of at most two thirds of
+// a pair's even share of all k-blocks (a tile's epilogue counted as 8), so
+// that no pair is left alone with one. Measured on B200 (backward): 30 tokens,
+// K 136, vocabulary 68684: 39 us, with at most 8 slices 63; 2048 tokens, K
+// 512, vocabulary 8192: 59 us either way (4 slices).
+int dh_slices(int64_t M, int64_t vcount, int64_t K, int64_t wkb) {
+  const int64_t tiles = static_cast<int64_t>(tiles_of(M)) * tiles_of(K), nkb = (vcount + kBlockR - 1) / kBlockR;
+  const int64_t share = (tiles * nkb + tiles_of(vcount) * tiles_of(K) * (wkb + 8)) / kPlanPairs + 8;
+  int64_t slices = (3 * nkb + 2 * share - 1) / (2 * share);
+  if (slices > 32) slices = 32;
+  if (slices > nkb) slices = nkb;
+  if (tiles >= kPlanPairs) slices = 1;
+  return slices < 1 ? 1 : static_cast<int>(slices);
+}
+
 Plan make_plan(int64_t M, int64_t V, int64_t K, bool f32) {
   Plan q{};
   const int64_t per_col = M * (f32 ? 4 : 2);
@@ -990,22 +1006,9 @@ Plan make_plan(int64_t M, int64_t V, int64_t K, bool f32) {
   q.piece = ((V + q.pieces - 1) / q.pieces + kTile - 1) / kTile * kTile;
   q.pieces = static_cast<int>((V + q.piece - 1) / q.piece);
   q.rows_pad = (M + kTile - 1) / kTile * kTile;
-  // dH has few tiles, each with the whole piece to sum over, next to dW's many
-  // with the tokens: its reduction is cut into slices of at most two thirds of
-  // a pair's even share of all k-blocks (a tile's epilogue counted as 8), so
-  // that no pair is left alone with one. Measured on B200 (backward): 30 tokens,
-  // K 136, vocabulary 68684: 39 us, with at most 8 slices 63; 2048 tokens, K
-  // 512, vocabulary 8192: 59 us either way (4 slices).
   const int64_t vcount = V < q.piece ? V : q.piece;
-  const int64_t tiles = static_cast<int64_t>(tiles_of(M)) * tiles_of(K), nkb = (vcount + kBlockR - 1) / kBlockR;
   const int64_t tokens = M < kF32Tokens || !f32 ? M : kF32Tokens;
-  const int64_t wkb = (tokens + kBlockR - 1) / kBlockR * (f32 ? 2 : 1) + 8;
-  const int64_t share = (tiles * nkb + tiles_of(vcount) * tiles_of(K) * wkb) / kPlanPairs + 8;
-  int64_t slices = (3 * nkb + 2 * share - 1) / (2 * share);
-  if (slices > 32) slices = 32;
-  if (slices > nkb) slices = nkb;
-  if (tiles >= kPlanPairs) slices = 1;
-  q.slices = slices < 1 ? 1 : static_cast<int>(slices);
+  q.slices = dh_slices(M, vcount, K, (tokens + kBlockR - 1) / kBlockR * (f32 ? 2 : 1));
   q.sums = q.pieces > 1 || q.slices > 1;
   size_t off = align256(static_cast<size_t>(M) * q.piece * 2);
   q.off_lo = off;
@@ -1018,6 +1021,28 @@ Plan make_plan(int64_t M, int64_t V, int64_t K, bool f32) {
   if (q.sums) off += static_cast<size_t>(q.slices) * q.rows_pad * K * 4;
   q.bytes = off;
   return q;
+}
+
+// Tiles of a Grad launch and their costs, from the vocabulary and the tokens set.
+void grad_tiles(XentParams& p, bool dh, bool dw) {
+  p.ntiles_h = dh ? p.slices * p.tiles_m * p.tiles_k : 0;
+  const int ntiles_w = dw ? tiles_of(p.vcount) * p.tiles_k : 0;
+  const int cost_h = (p.vcount + kBlockR - 1) / kBlockR / p.slices;
+  const int cost_w = (p.tcount + kBlockR - 1) / kBlockR * (p.split ? 2 : 1);
+  p.dw_first = cost_w > cost_h || p.ntiles_h == 0;
+  p.ntiles_a = p.dw_first ? ntiles_w : p.ntiles_h;
+  p.ntiles_b = p.dw_first ? p.ntiles_h : ntiles_w;
+  // a tile also costs its epilogue, about 4 k-blocks
+  p.cost_a = (p.dw_first ? cost_w : cost_h) + 4;
+  p.cost_b = (p.dw_first ? cost_h : cost_w) + 4;
+}
+
+// dH from its fp32 partial sums.
+cudaError_t join_dh(const float* sum, int64_t rows_pad, int slices, int64_t M, int64_t K, void* dH, cudaStream_t s) {
+  const int64_t nvecs = M * K / 4;
+  const int64_t want = (nvecs + 255) / 256, cap = static_cast<int64_t>(8) * device_sm_count();
+  return launch_pdl(xent_dh_kernel, dim3(static_cast<unsigned>(want < cap ? want : cap)), dim3(256), 0, s,
+                    reinterpret_cast<const float4*>(sum), rows_pad * K / 4, slices, nvecs, static_cast<uint2*>(dH));
 }
 
 }  // namespace
@@ -1197,27 +1222,86 @@ cudaError_t launch_xent_backward(const void* h, const void* W, const int64_t* ta
     for (int t0 = 0; t0 < p.M; t0 += step) {
       p.t0 = t0;
       p.tcount = p.M - t0 < step ? p.M - t0 : step;
-      p.ntiles_h = dH && t0 == 0 ? p.slices * p.tiles_m * p.tiles_k : 0;
       p.h_add = i > 0;
       p.w_add = accumulate || t0 > 0;
-      const int ntiles_w = dW ? tiles_of(p.vcount) * p.tiles_k : 0;
-      const int cost_h = (p.vcount + kBlockR - 1) / kBlockR / p.slices;
-      const int cost_w = (p.tcount + kBlockR - 1) / kBlockR * (p.split ? 2 : 1);
-      p.dw_first = cost_w > cost_h || p.ntiles_h == 0;
-      p.ntiles_a = p.dw_first ? ntiles_w : p.ntiles_h;
-      p.ntiles_b = p.dw_first ? p.ntiles_h : ntiles_w;
-      // a tile also costs its epilogue, about 4 k-blocks
-      p.cost_a = (p.dw_first ? cost_w : cost_h) + 4;
-      p.cost_b = (p.dw_first ? cost_h : cost_w) + 4;
+      grad_tiles(p, dH && t0 == 0, dW != nullptr);
       if (cudaError_t e = launch_phase<Phase::Grad, 256>(gm, p, s); e != cudaSuccess) return e;
       if (!dW) break;
     }
   }
   if (!dH || !q.sums) return cudaSuccess;
-  const int64_t nvecs = M * K / 4;
-  const int64_t want = (nvecs + 255) / 256, cap = static_cast<int64_t>(8) * device_sm_count();
-  return launch_pdl(xent_dh_kernel, dim3(static_cast<unsigned>(want < cap ? want : cap)), dim3(256), 0, s,
-                    reinterpret_cast<const float4*>(sum), q.rows_pad * K / 4, q.slices, nvecs, static_cast<uint2*>(dH));
+  return join_dh(sum, q.rows_pad, q.slices, M, K, dH, s);
+}
+
+// ---- the gradients of y = x w^T from operands in bf16: Grad alone, with dY in
+// the place of dz, x of h and w of the head
+namespace {
+
+// Slices of dX's reduction: as of dH, and each at most 131072 columns (the
+// tensor cores' sums lose up to a step of fp32 per 16 terms).
+int linear_slices(int64_t M, int64_t N, int64_t K) {
+  const int slices = dh_slices(M, N, K, (M + kBlockR - 1) / kBlockR), least = static_cast<int>((N + 131071) / 131072);
+  return slices > least ? slices : least;
+}
+int64_t pad_rows(int64_t M) { return (M + kTile - 1) / kTile * kTile; }
+
+}  // namespace
+
+// Never shrinks as tokens are added, as the sizes of the head's backward: for
+// every smaller number of token tiles a bound on its slices, those of
+// make_plan's comment (up to kPlanPairs / tiles and a half, 32, and k-blocks).
+size_t linear_grad_sum_bytes(int64_t M, int64_t N, int64_t K) {
+  const int64_t tm = tiles_of(M), tk = tiles_of(K), nkb = (N + kBlockR - 1) / kBlockR, least = (N + 131071) / 131072;
+  int64_t rows = least > 1 ? tm * least : 0;  // of the partial sums, in tiles
+  for (int64_t m = 1; m <= tm && m * tk < kPlanPairs; ++m) {
+    int64_t slices = (3 * kPlanPairs + 2 * m * tk - 1) / (2 * m * tk);
+    slices = slices > 32 ? 32 : slices;
+    slices = slices > nkb ? nkb : slices;
+    if (slices > 1 && m * slices > rows) rows = m * slices;
+  }
+  return static_cast<size_t>(rows) * kTile * K * 4;
+}
+
+cudaError_t launch_linear_grads(const void* dY, const void* x, const void* w, int64_t M, int64_t N, int64_t K, void* dX,
+                                void* dW, int dw_is_f32, int accumulate, float* one, float* sums, int* err,
+                                cudaStream_t s) {
+  const bool f32 = dW && dw_is_f32;
+  XentParams p{};
+  p.M = static_cast<int>(M);
+  p.V = static_cast<int>(N);
+  p.K = static_cast<int>(K);
+  p.vcount = p.V;
+  p.err = err;
+  p.tiles_m = tiles_of(M);
+  p.tiles_k = tiles_of(K);
+  p.scale = one;
+  p.slices = linear_slices(M, N, K);
+  p.rows_pad = static_cast<int>(pad_rows(M));
+  p.h_f32 = p.slices > 1;
+  p.w_f32 = f32;
+  p.dW = dW;
+  CUtensorMap gm[6] = {};
+  if (!make_map(&gm[2], dY, false, N, M, N * 2, 64, 64)) return cudaErrorInvalidValue;
+  if (dW && (!make_map(&gm[0], x, false, K, M, K * 2, 64, 64) ||
+             !make_map(&gm[5], dW, f32, K, N, K * (f32 ? 4 : 2), f32 ? 32 : 64, 32)))
+    return cudaErrorInvalidValue;
+  if (dX && (!make_map(&gm[1], w, false, K, N, K * 2, 64, 64) ||
+             !(p.h_f32 ? make_map(&gm[4], sums, true, K, static_cast<uint64_t>(p.slices) * p.rows_pad, K * 4, 32, 32)
+                       : make_map(&gm[4], dX, false, K, M, K * 2, 64, 32))))
+    return cudaErrorInvalidValue;
+  // maps that no tile uses are prefetched all the same
+  for (int i : {0, 1, 3, 4, 5})
+    if ((i == 3) || (!dW && (i == 0 || i == 5)) || (!dX && (i == 1 || i == 4))) gm[i] = gm[2];
+  const int step = f32 ? kF32Tokens : p.M;
+  for (int t0 = 0; t0 < p.M; t0 += step) {
+    p.t0 = t0;
+    p.tcount = p.M - t0 < step ? p.M - t0 : step;
+    p.w_add = accumulate || t0 > 0;
+    grad_tiles(p, dX && t0 == 0, dW != nullptr);
+    if (cudaError_t e = launch_phase<Phase::Grad, 256>(gm, p, s); e != cudaSuccess) return e;
+    if (!dW) break;
+  }
+  return dX && p.h_f32 ? join_dh(sums, p.rows_pad, p.slices, M, K, dX, s) : cudaSuccess;
 }
 
 }  // namespace bl
