@@ -35,7 +35,8 @@ constexpr int kThreads = 512;
 constexpr int kSegment = 4096;  // bytes
 constexpr int kBlocks = 2 * kPlanSms;  // resident at once
 constexpr int kPiece = 8;       // segments taken at a time by the backward walk
-constexpr int kU = 4;           // 16-byte vectors in flight per thread
+constexpr int kU = 4;           // 16-byte vectors whose squares are added in fp32
+constexpr int kGroups = 2;      // such groups in flight per thread where the squares are summed
 
 struct Entry {
   const void* in;
@@ -48,19 +49,8 @@ struct Table {
   Entry e[kCap];
   int first[kCap + 1];  // the tensor's first segment; at `count` the end
   int count;
+  uint16_t from[kBlocks + 1];  // tensor that holds the first segment of a block's run (the last's next: from[blocks])
 };
-
-// Tensor that holds segment s.
-template <int kCap>
-__device__ __forceinline__ int tensor_of(const Table<kCap>& t, int s) {
-  int lo = 0, hi = t.count;  // first[lo] <= s < first[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (t.first[mid] <= s) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
 
 // Elements [b, e) of a tensor that its segments [s, t) cover.
 __device__ __forceinline__ void span(int64_t n, int esize, int s, int t, int64_t& b, int64_t& e) {
@@ -98,7 +88,7 @@ __device__ __forceinline__ double squares(const uint4 (&v)[kU]) {
   // less than 2^-40 of the sum
   if (f < __uint_as_float(0x7F800000u) && f >= 8.271806e-25f) return static_cast<double>(f);
   double d = 0.0;
-#pragma unroll 1
+#pragma unroll
   for (int u = 0; u < kU; ++u) {
     const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
     if ((w[0] | w[1] | w[2] | w[3]) == 0u) continue;
@@ -128,11 +118,13 @@ __device__ __forceinline__ double sum_range(const T* p, int64_t n) {
   constexpr int kPer = 16 / sizeof(T);
   const int64_t vecs = n / kPer;
   const uint4* v = reinterpret_cast<const uint4*>(p);
-  for (int64_t i = t; i < vecs; i += kU * kThreads) {
-    uint4 r[kU];
+  for (int64_t i = t; i < vecs; i += kGroups * kU * kThreads) {
+    uint4 r[kGroups][kU];
 #pragma unroll
-    for (int u = 0; u < kU; ++u) r[u] = i + u * kThreads < vecs ? __ldg(v + i + u * kThreads) : make_uint4(0u, 0u, 0u, 0u);
-    d += squares<T>(r);
+    for (int u = 0; u < kGroups * kU; ++u)
+      r[u / kU][u % kU] = i + u * kThreads < vecs ? __ldg(v + i + u * kThreads) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) d += squares<T>(r[g]);
   }
   const int64_t tail = vecs * kPer + t;
   if (tail < n) d += square(to_f32(p[tail]));
@@ -151,11 +143,9 @@ __device__ __forceinline__ double block_sum(double d, double* buf) {
   return d;
 }
 
-// The block's run of segments.
-__device__ __forceinline__ void block_run(int segments, int& s0, int& s1) {
-  const int64_t b = blockIdx.x, g = gridDim.x;
-  s0 = static_cast<int>(segments * b / g);
-  s1 = static_cast<int>(segments * (b + 1) / g);
+// First segment of block b's run, of `blocks` equal ones.
+__host__ __device__ __forceinline__ int run_start(int segments, int b, int blocks) {
+  return static_cast<int>(static_cast<int64_t>(segments) * b / blocks);
 }
 
 template <int kCap>
@@ -163,10 +153,10 @@ __global__ void __launch_bounds__(kThreads, 2) grad_sum_kernel(const __grid_cons
   __shared__ double buf[kThreads / 32];
   pdl_wait_primary();
   pdl_launch_dependents();
-  int s, end;
-  block_run(t.first[t.count], s, end);
+  const int segments = t.first[t.count], end = run_start(segments, blockIdx.x + 1, gridDim.x);
+  int s = run_start(segments, blockIdx.x, gridDim.x);
   double d = 0.0;
-  for (int i = s < end ? tensor_of(t, s) : 0; s < end; ++i) {
+  for (int i = t.from[blockIdx.x]; s < end; ++i) {
     const int last = t.first[i + 1] < end ? t.first[i + 1] : end;
     const int64_t n = t.e[i].n2 >> 1;
     const bool f32 = t.e[i].n2 & 1;
@@ -261,9 +251,9 @@ __global__ void __launch_bounds__(kThreads, 2) grad_scale_kernel(const __grid_co
   const bool tiny = factor < 1e-30;
   k.f = static_cast<float>(tiny ? factor * 0x1p96 : factor);
   k.step = tiny ? 0x1p-96f : 1.0f;
-  int s0, end;
-  block_run(t.first[t.count], s0, end);
-  for (int i = s0 < end ? tensor_of(t, end - 1) : 0; end > s0;) {
+  const int segments = t.first[t.count], s0 = run_start(segments, blockIdx.x, gridDim.x);
+  int end = run_start(segments, blockIdx.x + 1, gridDim.x);
+  for (int i = t.from[blockIdx.x + 1]; end > s0;) {
     while (t.first[i] >= end) --i;
     int s = end - kPiece;
     if (s < s0) s = s0;
@@ -284,6 +274,11 @@ __global__ void __launch_bounds__(kThreads, 2) grad_scale_kernel(const __grid_co
 // ---------------------------------------------------------------- host side
 constexpr int kFew = 64, kMany = 1024;  // tensors per launch (parameters of 2 and 28 KB)
 
+template <int kCap>
+int grid_of(const Table<kCap>& t) {
+  return t.first[t.count] < kBlocks ? t.first[t.count] : kBlocks;
+}
+
 // Fills `t` from the tensors [i, count) that hold something, up to its capacity;
 // returns where to go on. (2^40 elements in all, the caller's limit, are 2^30
 // segments and one more per tensor.)
@@ -299,6 +294,14 @@ int64_t fill(Table<kCap>& t, const ClipTensor* x, int64_t i, int64_t count) {
     t.e[t.count] = {x[i].in, x[i].out, 2 * x[i].n + (x[i].f32 ? 1 : 0)};
     t.first[++t.count] = static_cast<int>(segments);
   }
+  if (t.count > 0) {
+    const int blocks = grid_of(t);
+    for (int b = 0, j = 0; b <= blocks; ++b) {
+      const int at = run_start(t.first[t.count], b, blocks);
+      while (j + 1 < t.count && t.first[j + 1] <= at) ++j;
+      t.from[b] = static_cast<uint16_t>(j);
+    }
+  }
   return i;
 }
 
@@ -310,7 +313,7 @@ cudaError_t launch_all(const ClipTensor* x, int64_t count, float* norm, double m
   for (int64_t i = 0; i < count;) {
     i = fill(t, x, i, count);
     if (t.count == 0) break;
-    const int grid = t.first[t.count] < kBlocks ? t.first[t.count] : kBlocks;
+    const int grid = grid_of(t);
     if (cudaError_t e = launch_pdl(grad_sum_kernel<kCap>, dim3(grid), dim3(kThreads), 0, s, t, parts + nparts); e != cudaSuccess)
       return e;
     nparts += grid;
@@ -323,7 +326,7 @@ cudaError_t launch_all(const ClipTensor* x, int64_t count, float* norm, double m
     const int64_t next = fill(t, x, i, count);
     for (int j = 0; j < t.count; ++j) in_place = in_place && t.e[j].in == t.e[j].out;
     if (t.count == 0) break;
-    const int grid = t.first[t.count] < kBlocks ? t.first[t.count] : kBlocks;
+    const int grid = grid_of(t);
     if (cudaError_t e = launch_pdl(grad_scale_kernel<kCap>, dim3(grid), dim3(kThreads), 0, s, t,
                                    static_cast<const double*>(parts), nparts, most, in_place ? 1 : 0, begin ? norm : nullptr);
         e != cudaSuccess)

@@ -4,12 +4,13 @@
 //   acc[m,n] = sum_k xq[m,k] wq[n,k]              exact INT32
 //   y[m,n]   = rn(fp32(acc) * fp32(sx[m] * sw[n]))
 //
-// Three kernels:
+// Four kernels:
 //   int8_tile_kernel  persistent CTA pairs, tcgen05.mma kind::i8 (cta_group::2),
 //                     both operands by TMA, INT32 accumulators in TMEM
-//   int8_few_kernel   a few tokens: the weights stream through mma.sync straight
-//                     from global memory, in the order that makes a lane's
-//                     16-byte loads the operands
+//   int8_few_kernel   a few tokens: the weights stream through a deep TMA ring to
+//                     mma.sync
+//   int8_mid_kernel   tens of tokens: tiles of 128 channels by all tokens, whose K
+//                     is split over a cluster
 //   int8_values_kernel  rn_bf16(code * scale) of both operands, for the gradients'
 //                     products (k_xent.cu)
 #include <cuda.h>
@@ -42,16 +43,15 @@ constexpr int kBlockK = 128;           // K per stage
 constexpr int kABytes = 128 * kBlockK; // one CTA's tokens of a stage
 constexpr uint32_t kTmemCols = 512;    // two accumulators
 constexpr int kEpiWarps = 8, kWarpEpi0 = 2, kTileThreads = 32 * (kWarpEpi0 + kEpiWarps);
-constexpr int kEpiBox = 4096;          // output box: 32 rows x 128 bytes
-
-template <int BN>
+template <typename TY, int BN>
 struct Geo {
+  static constexpr int kBox = 32 * 32 * sizeof(TY);  // an epilogue warp's output box, 32 rows x 32 columns
   static constexpr int kBBytes = BN / 2 * kBlockK;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = BN == 256 ? 6 : 7;
-  static constexpr int kSlots = BN == 256 ? 1 : 1;  // output boxes per epilogue warp
+  static constexpr int kStages = (232448 - 1280 - kEpiWarps * (kBox + 128)) / kStageBytes;
   static constexpr int kOffEpi = kStages * kStageBytes;
-  static constexpr int kOffBar = kOffEpi + kEpiWarps * kSlots * kEpiBox;
+  static constexpr int kOffScale = kOffEpi + kEpiWarps * kBox;  // a chunk's channel scales, per epilogue warp
+  static constexpr int kOffBar = kOffScale + kEpiWarps * 128;
   static constexpr int kNumBars = 2 * kStages + 5;  // full, empty, tmem_full[2], tmem_empty[2], done
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmemBytes = kOffMisc + 64 + 1024 /*base alignment*/;
@@ -79,9 +79,12 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// 16-byte chunk j of row `row` of a 32 x 128 byte box, 128-byte swizzled.
-__device__ __forceinline__ uint32_t box_chunk(uint32_t box, int row, int j) {
-  return box + static_cast<uint32_t>(row) * 128u + (static_cast<uint32_t>(j ^ (row & 7)) << 4);
+// 16-byte piece j of row `row` of an output box of 32 columns: rows of 128 bytes,
+// 128-byte swizzled (fp32), or of 64 bytes, 64-byte swizzled (bf16).
+template <int kEsize>
+__device__ __forceinline__ uint32_t box_piece(uint32_t box, int row, int j) {
+  const int turn = kEsize == 4 ? row & 7 : (row >> 1) & 3;
+  return box + static_cast<uint32_t>(row) * (32 * kEsize) + (static_cast<uint32_t>(j ^ turn) << 4);
 }
 
 // TY: type of y. kTma: y's rows start on 16-byte boundaries, so a box leaves by
@@ -90,7 +93,7 @@ template <typename TY, int BN, bool kTma>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     int8_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                      const __grid_constant__ CUtensorMap map_y, const __grid_constant__ TileParams p) {
-  using G = Geo<BN>;
+  using G = Geo<TY, BN>;
   constexpr int kStages = G::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -220,124 +223,121 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     __syncwarp();
   } else {
     const int q = warp & 3, part = (warp - kWarpEpi0) >> 2, slot0 = warp - kWarpEpi0;
-    constexpr int kChunks = BN / 64;  // 32-column chunks of a warp
-    const uint32_t boxes = smem_u32(smem + G::kOffEpi + slot0 * G::kSlots * kEpiBox);
-    uint32_t seq = 0, box = 0;
+    // 32-column chunks of the warp: the first half of the tile's, or the second
+    constexpr int kChunks = BN / 32, kFirst = (kChunks + 1) / 2;
+    const int chunks = part == 0 ? kFirst : kChunks - kFirst;
+    constexpr int kEsize = sizeof(TY);
+    const uint32_t box = smem_u32(smem + G::kOffEpi + slot0 * G::kBox);
+    const uint32_t table = smem_u32(smem + G::kOffScale + slot0 * 128);
     int buf = 0;
     uint32_t buf_phase = 0;
-    constexpr int kEsize = sizeof(TY), kPerBox = 128 / kEsize;  // columns of a box: 64 or 32
+    // What the next tile needs, requested while this one is worked on: the token's
+    // scale, and of each chunk's channels one scale per lane, which all lanes then
+    // read from shared memory. (Every lane reading all 32 from global memory, a
+    // chunk ahead: 50 us for 8192 x 8192 outputs of K 128.)
+    float next_sx = 0.0f, next_sw[kFirst];
+    auto prepare = [&](int u) {
+      if (u >= p.ntiles) return;
+      const int row = tile_row(u) + q * 32 + lane, col = tile_col(u) + part * kFirst * 32 + lane;
+      if (row < p.M) asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(next_sx) : "l"(p.sx + row));
+#pragma unroll
+      for (int c = 0; c < kFirst; ++c)
+        if (c < chunks && col + 32 * c < p.N)
+          asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(next_sw[c]) : "l"(p.sw + col + 32 * c));
+    };
+#pragma unroll
+    for (int c = 0; c < kFirst; ++c) next_sw[c] = 0.0f;
+    prepare(pair);
     for (int u = pair; u < p.ntiles; u += npairs) {
-      const int row0 = tile_row(u) + q * 32, row = row0 + lane;
-      const int col0 = tile_col(u) + part * (BN / 2);
-      const float sx = row < p.M ? __ldg(p.sx + row) : 0.0f;
-      const f32x2 sx2 = both2(sx);
+      const int row0 = tile_row(u) + q * 32;
+      const int col0 = tile_col(u) + part * kFirst * 32;
+      const f32x2 sx2 = both2(next_sx);
+      float sw[kFirst];
+#pragma unroll
+      for (int c = 0; c < kFirst; ++c) sw[c] = next_sw[c];
+      prepare(u + npairs);
+      // chunks that hold columns
+      const int left = (p.N - col0 + 31) >> 5, live = row0 >= p.M || left < 0 ? 0 : left < chunks ? left : chunks;
       if (!wait(&tmem_full[buf], buf_phase)) break;
       tc_fence_after();
-      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + part * (BN / 2);
-      auto chunk = [&](uint32_t (&r)[32], int c) {
-        const int col = col0 + 32 * c;
-        if (col >= p.N) return;
-        f32x2 v[16];
-        const float* sw = p.sw + col;
-        if (col + 32 <= p.N) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float4 w = __ldg(reinterpret_cast<const float4*>(sw) + j);
-            v[2 * j] = pair2(w.x, w.y);
-            v[2 * j + 1] = pair2(w.z, w.w);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float a = col + 2 * j < p.N ? __ldg(sw + 2 * j) : 0.0f;
-            const float b = col + 2 * j + 1 < p.N ? __ldg(sw + 2 * j + 1) : 0.0f;
-            v[j] = pair2(a, b);
-          }
-        }
-        // three roundings in fp32: of the sum, of the two scales' product, of y
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          v[j] = mul2(pair2(__int2float_rn(static_cast<int>(r[2 * j])), __int2float_rn(static_cast<int>(r[2 * j + 1]))),
-                      mul2(v[j], sx2));
-        const bool first = kEsize == 4 || (c & 1) == 0, last = kEsize == 4 || (c & 1) || col + 32 >= p.N;
-        if (first) {
-          if constexpr (kTma) {
-            if (lane == 0) bulk_wait_group_read<G::kSlots - 1>();
-          }
-          __syncwarp();
-          box = boxes + (seq++ % G::kSlots) * kEpiBox;
-        }
-        if constexpr (kEsize == 4) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(box_chunk(box, lane, j)), "l"(v[2 * j]), "l"(v[2 * j + 1])
-                         : "memory");
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            st_shared_v4(box_chunk(box, lane, (c & 1) * 4 + j), pack_bf16x2(v[4 * j]), pack_bf16x2(v[4 * j + 1]),
-                         pack_bf16x2(v[4 * j + 2]), pack_bf16x2(v[4 * j + 3]));
-        }
-        if (!last) return;
-        const int bcol = col & ~(kPerBox - 1);  // (a warp's first column is a multiple of 64)
-        if constexpr (kTma) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_2d(&map_y, box, bcol, row0);
-            bulk_commit_group();
-          }
-        } else {
-          __syncwarp();
-          const int rows = p.M - row0 < 32 ? p.M - row0 : 32;
-          for (int i = 0; i < rows; ++i) {
-#pragma unroll
-            for (int h = 0; h < kPerBox; h += 32) {
-              const int k = lane + h;
-              if (bcol + k >= p.N) continue;
-              const uint32_t from = box_chunk(box, i, k * kEsize / 16) + (k * kEsize & 15);
-              TY* to = static_cast<TY*>(p.y) + static_cast<int64_t>(row0 + i) * p.N + bcol + k;
-              if constexpr (kEsize == 4) {
-                uint32_t w;
-                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(from) : "memory");
-                *reinterpret_cast<uint32_t*>(to) = w;
-              } else {
-                uint16_t w;
-                asm volatile("ld.shared.b16 %0, [%1];" : "=h"(w) : "r"(from) : "memory");
-                *reinterpret_cast<uint16_t*>(to) = w;
-              }
-            }
-          }
-        }
-      };
+      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + part * kFirst * 32;
       auto release = [&] {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(lead(&tmem_empty[buf]));
       };
-      if (row0 < p.M) {
-        uint32_t ra[32], rb[32];
-        tmem_ld_32x32b_x32(tbase, ra);
+      if (live == 0) release();
+      uint32_t r[2][32];
+      if (live > 0) {
+        tmem_ld_32x32b_x32(tbase, r[0]);
         tmem_ld_wait();
-#pragma unroll 1
-        for (int c = 0; c < kChunks; c += 2) {
-          tmem_ld_32x32b_x32(tbase + 32 * (c + 1), rb);
-          chunk(ra, c);
-          tmem_ld_wait();
-          if (c + 2 < kChunks) tmem_ld_32x32b_x32(tbase + 32 * (c + 2), ra);
-          else release();  // every load of this buffer has landed
-          chunk(rb, c + 1);
-          tmem_ld_wait();
+      }
+#pragma unroll
+      for (int c = 0; c < kFirst; ++c) {
+        if (c >= live) break;
+        const int col = col0 + 32 * c;
+        // (the buffer is released when every load of it has landed)
+        if (c + 1 < live) tmem_ld_32x32b_x32(tbase + 32 * (c + 1), r[(c + 1) & 1]);
+        else release();
+        __syncwarp();
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(table + lane * 4), "f"(sw[c]) : "memory");
+        __syncwarp();
+        // three roundings in fp32: of the sum, of the two scales' product, of y
+        f32x2 v[16];
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          f32x2 w0, w1;
+          asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(w0), "=l"(w1) : "r"(table + j * 8));
+          const uint32_t* a = r[c & 1] + 2 * j;
+          v[j] = mul2(pair2(__int2float_rn(static_cast<int>(a[0])), __int2float_rn(static_cast<int>(a[1]))), mul2(w0, sx2));
+          v[j + 1] = mul2(pair2(__int2float_rn(static_cast<int>(a[2])), __int2float_rn(static_cast<int>(a[3]))), mul2(w1, sx2));
         }
-      } else {
-        release();
+        if (kTma && lane == 0) bulk_wait_group_read<0>();
+        __syncwarp();
+        if constexpr (kEsize == 4) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(box_piece<4>(box, lane, j)), "l"(v[2 * j]), "l"(v[2 * j + 1])
+                         : "memory");
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            st_shared_v4(box_piece<2>(box, lane, j), pack_bf16x2(v[4 * j]), pack_bf16x2(v[4 * j + 1]),
+                         pack_bf16x2(v[4 * j + 2]), pack_bf16x2(v[4 * j + 3]));
+        }
+        if constexpr (kTma) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&map_y, box, col, row0);
+            bulk_commit_group();
+          }
+        } else {
+          __syncwarp();
+          const int rows = col + lane < p.N ? p.M - row0 : 0;
+          const uint32_t in = (lane * kEsize) & 15;
+          TY* to = static_cast<TY*>(p.y) + static_cast<int64_t>(row0) * p.N + col + lane;
+#pragma unroll 16
+          for (int i = 0; i < 32; ++i, to += p.N) {
+            if constexpr (kEsize == 4) {
+              uint32_t w;
+              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(box_piece<4>(box, i, lane / 4) + in));
+              if (i < rows) *reinterpret_cast<uint32_t*>(to) = w;
+            } else {
+              uint16_t w;
+              asm volatile("ld.shared.b16 %0, [%1];" : "=h"(w) : "r"(box_piece<2>(box, i, lane / 8) + in));
+              if (i < rows) *reinterpret_cast<uint16_t*>(to) = w;
+            }
+          }
+        }
+        tmem_ld_wait();
       }
       if (++buf == 2) {
         buf = 0;
         buf_phase ^= 1;
       }
     }
-    if (kTma && lane == 0) bulk_wait_group_all();
+    if (kTma && lane == 0) bulk_wait_group_read<0>();
     __syncwarp();
   }
 
@@ -350,98 +350,373 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
 }
 
 // ---------------------------------------------------------------- a few tokens
-// A CTA takes 16 R channels, its warps consecutive shares of K in blocks of 64,
-// whose INT32 sums they add in shared memory (exact in any order). Lane (g, t) =
-// (lane / 4, lane % 4) loads bytes 16 t .. 16 t + 15 of the block of rows g and
-// g + 8, and of token g of each group of 8: words 2 s and 2 s + 1 are its operands
-// of step s of mma.sync.m16n8k32. The order of K within the block is another one
-// than the instruction's, the same for both operands.
-__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                       uint32_t b1) {
+// The weights are read once and hardly used: what counts is bytes in flight. A CTA
+// (two fit on an SM, of this kernel or of the next one, whose first loads then
+// overlap this one's end) takes tiles of 16 R channels in turn; up to four threads,
+// each with every fourth stage, keep a ring of stages (256 of K: the channels' rows
+// and the tokens', 128-byte swizzled boxes) filled by TMA, across the ends of
+// tiles (one thread takes some 250 cycles for a stage's requests, which a CTA's
+// share of HBM fills in fewer). R x S consumer warps: a
+// warp takes one group of 16 channels and every S-th stage, mma.sync.m16n8k32 on
+// operands that ldmatrix brings in the instruction's order; the S warps' INT32
+// sums are added in shared memory (exact in any order).
+constexpr int64_t kFewMost = 16;   // most tokens
+constexpr int kFewSmem = 114688;   // of a CTA: half an SM's
+
+struct FewParams {
+  int M, N, K, ntiles;
+  const float* sx;
+  const float* sw;
+  void* y;
+  int* err;
+};
+
+template <int kTok, int R>
+struct Few {
+  static constexpr int S = kTok == 1 && R == 1 ? 8 : R == 1 || (R == 2 && kTok != 2) ? 4 : 2;
+  static constexpr int kLoaders = S < 4 ? S : 4;
+  static constexpr int kWarps = R * S, kThreads = 32 * (kLoaders + kWarps), kN = 16 * R, kM = 8 * kTok;
+  static constexpr int kBoxW = kN * 128, kBoxX = kM * 128, kStageBytes = 2 * (kBoxW + kBoxX);
+  static constexpr int kSums = S * kM * kN;  // ints
+  static constexpr int kBufs = kTok == 4 ? 1 : 2;  // of them, in turn
+  static constexpr int kFixed = kBufs * kSums * 4 + 512 /*barriers*/ + 1024 /*base alignment*/;
+  // a multiple of S, so that a slot of the ring is always the same warps': they
+  // have seen its last filling when they wait for the next
+  static constexpr int kStages = (kFewSmem - kFixed) / kStageBytes / S * S;
+  static constexpr int kOffSums = kStages * kStageBytes;
+  static constexpr int kOffBar = kOffSums + kBufs * kSums * 4;  // full, empty, joined, read; the abort flag
+  static constexpr int kSmemBytes = kOffBar + 512 + 1024;
+  static_assert(kStages >= S && kSmemBytes <= kFewSmem && (2 * kStages + 2) * 8 + 8 <= 512, "shared memory");
+};
+
+__device__ __forceinline__ void mma_s8(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix2(uint32_t addr, uint32_t& a, uint32_t& b) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr) : "memory");
+}
+// 16-byte chunk c of row r of a box of 128-byte rows, 128-byte swizzled.
+__device__ __forceinline__ uint32_t few_chunk(uint32_t box, int r, int c) {
+  return box + static_cast<uint32_t>(r) * 128u + (static_cast<uint32_t>(c ^ (r & 7)) << 4);
 }
 
-constexpr int kFewWarps = 8;   // most warps of a CTA
-constexpr int64_t kFewMost = 32;  // most tokens
-
-struct FewParams {
-  const int8_t* xq;
-  const float* sx;
-  const int8_t* wq;
-  const float* sw;
-  int M, N, K;
-  void* y;
-};
-
-// kTok: groups of 8 tokens; R: groups of 16 channels; kU: blocks of K in flight.
-template <typename TY, int kTok, int R, int kU>
-__global__ void __launch_bounds__(32 * kFewWarps) int8_few_kernel(const FewParams p) {
-  extern __shared__ int sums[];  // [warps][8 kTok tokens][16 R channels]
-  constexpr int kN = 16 * R, kM = 8 * kTok;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int warps = blockDim.x >> 5;
-  const int n0 = static_cast<int>(blockIdx.x) * kN;
-  const int nb = (p.K + 63) >> 6;
-  const int b0 = nb * warp / warps, b1 = nb * (warp + 1) / warps;
-  // rows outside read the last row, whose sums go nowhere
-  const int8_t* w[2 * R];
-#pragma unroll
-  for (int i = 0; i < 2 * R; ++i) {
-    const int n = n0 + g + 8 * i;
-    w[i] = p.wq + static_cast<int64_t>(n < p.N ? n : p.N - 1) * p.K + 16 * t;
+template <typename TY, int kTok, int R>
+__global__ void __launch_bounds__(Few<kTok, R>::kThreads, 2)
+    int8_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const FewParams p) {
+  using G = Few<kTok, R>;
+  constexpr int kStages = G::kStages, S = G::S, kN = G::kN, kM = G::kM;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::kOffBar);
+  uint64_t* empty = full + kStages;
+  uint64_t* joined = empty + kStages;
+  uint64_t* read = joined + 1;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(read + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int boxes = (p.K + 127) >> 7, nst = (boxes + 1) >> 1;  // boxes of 128 of K, stages of two
+  if (threadIdx.x == 0) {
+    prefetch_tensormap(&map_w);
+    prefetch_tensormap(&map_x);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], R);
+    }
+    mbar_init(joined, G::kWarps);
+    mbar_init(read, G::kWarps);
+    *abort_flag = 0;
+    fence_mbar_init();
   }
-  const int8_t* x[kTok];
-#pragma unroll
-  for (int i = 0; i < kTok; ++i) x[i] = p.xq + static_cast<int64_t>(g + 8 * i < p.M ? g + 8 * i : p.M - 1) * p.K + 16 * t;
+  __syncthreads();
   pdl_wait_primary();
   pdl_launch_dependents();
-  int acc[R][kTok][4] = {};
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  for (int b = b0; b < b1; b += kU) {
-    uint4 wv[kU][2 * R], xv[kU][kTok];
+  if (warp < G::kLoaders) {
+    if (lane == 0) {
+      const int mine = ((p.ntiles - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1) * nst;  // the CTA's stages
+      int it = warp, st = warp % nst, u = blockIdx.x + warp / nst * gridDim.x;
+      bool ok = true;
+      for (; it < mine; it += G::kLoaders) {
+        const int stage = it % kStages;
+        if (!mbar_wait(&empty[stage], (it / kStages & 1) ^ 1, abort_flag, p.err)) {
+          ok = false;
+          break;
+        }
+        const bool two = 2 * st + 1 < boxes;
+        mbar_arrive_expect_tx(&full[stage], two ? G::kStageBytes : G::kStageBytes / 2);
+        uint8_t* at = smem + stage * G::kStageBytes;
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int k = (b + u) * 64;
-      const bool in = b + u < b1 && k + 16 * t < p.K;  // K is a multiple of 16
-#pragma unroll
-      for (int i = 0; i < 2 * R; ++i) wv[u][i] = in ? __ldg(reinterpret_cast<const uint4*>(w[i] + k)) : zero;
-#pragma unroll
-      for (int i = 0; i < kTok; ++i) xv[u][i] = in ? __ldg(reinterpret_cast<const uint4*>(x[i] + k)) : zero;
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1 && !two) break;
+          tma_load_2d(&map_w, &full[stage], at + h * G::kBoxW, (2 * st + h) * 128, u * kN);
+          tma_load_2d(&map_x, &full[stage], at + 2 * G::kBoxW + h * G::kBoxX, (2 * st + h) * 128, 0);
+        }
+        for (st += G::kLoaders; st >= nst; st -= nst) u += gridDim.x;
+      }
+      // an early end: let this thread's copies land before the CTA exits
+      if (!ok || *abort_flag) {
+        const unsigned long long deadline = globaltimer_ns() + kWaitLimitNs;
+        for (int i = it - G::kLoaders, n = 0; i >= 0 && n < kStages; i -= G::kLoaders, n += G::kLoaders)
+          mbar_drain_until(&full[i % kStages], i / kStages & 1, deadline);
+      }
     }
+    return;
+  }
+  const int cw = warp - G::kLoaders, group = cw % R, share = cw / R;
+  const int steps = (p.K + 31) >> 5;  // of 32 of K
+  // the lane's row and 16-byte half of a step, in the operands' four matrices
+  const int wrow = group * 16 + (lane & 15), whalf = lane >> 4;
+  const int xrow = kTok == 1 ? lane & 7 : (lane & 7) + (lane >> 4) * 8, xhalf = (lane >> 3) & 1;
+  int tile = 0;
+  uint32_t base = 0;  // stages of the tiles before
+  for (int u = blockIdx.x; u < p.ntiles; u += gridDim.x, ++tile, base += nst) {
+    int acc[kTok][4] = {};
+    for (uint32_t st = (share - base) & (S - 1); st < static_cast<uint32_t>(nst); st += S) {
+      const uint32_t stage = (base + st) % kStages;
+      if (!mbar_wait(&full[stage], (base + st) / kStages & 1, abort_flag, p.err)) return;
+      const uint32_t at = smem_u32(smem) + stage * G::kStageBytes;
+      const int left = steps - static_cast<int>(st) * 8;
 #pragma unroll
-    for (int u = 0; u < kU; ++u)
+      for (int step = 0; step < 8; ++step) {
+        if (step >= left) break;
+        const int box = step >> 2, c = (step & 3) * 2;
+        uint32_t a[4];
+        ldmatrix4(few_chunk(at + box * G::kBoxW, wrow, c + whalf), a);
+        const uint32_t xbox = at + 2 * G::kBoxW + box * G::kBoxX;
+        if constexpr (kTok == 1) {
+          uint32_t b0, b1;
+          ldmatrix2(few_chunk(xbox, xrow, c + xhalf), b0, b1);
+          mma_s8(acc[0], a, b0, b1);
+        } else {
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const uint4 a = wv[u][2 * r], c = wv[u][2 * r + 1];
-#pragma unroll
-        for (int i = 0; i < kTok; ++i) {
-          mma_s8(acc[r][i], a.x, c.x, a.y, c.y, xv[u][i].x, xv[u][i].y);
-          mma_s8(acc[r][i], a.z, c.z, a.w, c.w, xv[u][i].z, xv[u][i].w);
+          for (int i = 0; i < kTok; i += 2) {
+            uint32_t b[4];
+            ldmatrix4(few_chunk(xbox, xrow + 8 * i, c + xhalf), b);
+            mma_s8(acc[i], a, b[0], b[1]);
+            mma_s8(acc[i + 1], a, b[2], b[3]);
+          }
         }
       }
-  }
-  int* mine = sums + warp * kN * kM;
-#pragma unroll
-  for (int r = 0; r < R; ++r)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[stage]);
+    }
+    // two buffers in turn: a warp writes one again only after a join that every
+    // reader of it has reached; a single one only when all have read it
+    if (G::kBufs == 1 && tile > 0 && !mbar_wait(read, (tile - 1) & 1, abort_flag, p.err)) return;
+    int* sums = reinterpret_cast<int*>(smem + G::kOffSums) + tile % G::kBufs * G::kSums;
+    int* own = sums + share * kN * kM + group * 16;
+    const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int i = 0; i < kTok; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        // row g (+ 8), tokens 2 t and 2 t + 1
-        const int n = 16 * r + g + (j >> 1) * 8, m = 8 * i + 2 * t + (j & 1);
-        mine[m * kN + n] = acc[r][i][j];
-      }
+      for (int j = 0; j < 4; ++j) own[(8 * i + 2 * t + (j & 1)) * kN + g + (j >> 1) * 8] = acc[i][j];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(joined);
+    if (!mbar_wait(joined, tile & 1, abort_flag, p.err)) return;
+    for (int i = threadIdx.x - 32 * G::kLoaders; i < kN * kM; i += 32 * G::kWarps) {
+      const int n = u * kN + i % kN, m = i / kN;
+      if (m >= p.M || n >= p.N) continue;
+      int v = 0;
+#pragma unroll
+      for (int k = 0; k < S; ++k) v += sums[k * kN * kM + i];
+      store1(static_cast<TY*>(p.y) + static_cast<int64_t>(m) * p.N + n,
+             __int2float_rn(v) * __fmul_rn(__ldg(p.sx + m), __ldg(p.sw + n)));
+    }
+    if constexpr (G::kBufs == 1) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(read);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- tens of tokens
+// D = W x^T: 128 channels of one CTA by all tokens (32 or 64 columns),
+// tcgen05.mma kind::i8 (cta_group::1). There are few such tiles, so the CTAs of a
+// cluster share one: each sums its part of K, leaves its INT32 sums in its shared
+// memory, and turns its share of the tokens into y from all CTAs' sums. A thread
+// has a channel, so a warp writes 32 channels of a token at once, whatever N.
+//
+// Roles (192 threads): warp 0 loads, warp 1 issues the MMAs, warps 2..5 are the
+// epilogue. Waits are bounded as in the tiles' kernel; every thread reaches the
+// cluster's barriers whatever happened before.
+constexpr int64_t kMidMost = 64;  // most tokens
+constexpr int kMidThreads = 192;
+
+struct MidParams {
+  int M, N, K, share;  // CTAs per tile
+  const float* sx;
+  const float* sw;
+  void* y;
+  int* err;
+};
+
+template <int NT>
+struct Mid {
+  static constexpr int kW = 128 * kBlockK, kX = NT * kBlockK, kStageBytes = kW + kX;
+  static constexpr int kStages = 110 * 1024 / kStageBytes;  // two CTAs to an SM
+  static constexpr int kOffBar = kStages * kStageBytes;  // full, empty; done; TMEM base, abort flag
+  static constexpr int kOffSx = (kOffBar + (2 * kStages + 1) * 8 + 8 + 15) / 16 * 16;  // the tokens' scales
+  static constexpr int kSmemBytes = kOffSx + NT * 4 + 1024 /*base alignment*/;
+  static_assert(kSmemBytes <= 232448 && NT * 512 <= kOffBar, "the sums fit in the ring");
+};
+
+__device__ __forceinline__ int ld_cluster(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <typename TY, int NT>
+__global__ void __launch_bounds__(kMidThreads)
+    int8_mid_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const MidParams p) {
+  using G = Mid<NT>;
+  constexpr int kStages = G::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::kOffBar);
+  uint64_t* empty = full + kStages;
+  uint64_t* done = empty + kStages;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank()), share = p.share;
+  const int n0 = static_cast<int>(blockIdx.x) / share * 128;
+  const int boxes = (p.K + kBlockK - 1) / kBlockK;
+  const int kb0 = boxes * rank / share, nkb = boxes * (rank + 1) / share - kb0;
+  if (threadIdx.x == 0) {
+    prefetch_tensormap(&map_w);
+    prefetch_tensormap(&map_x);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_one(tmem_holder, NT);
+    tmem_relinquish_one();
+  }
+  tc_fence_before();
   __syncthreads();
-  for (int i = threadIdx.x; i < kN * kM; i += blockDim.x) {
-    const int n = n0 + i % kN, m = i / kN;
-    if (m >= p.M || n >= p.N) continue;
-    int s = 0;
-    for (int v = 0; v < warps; ++v) s += sums[v * kN * kM + i];
-    store1(static_cast<TY*>(p.y) + static_cast<int64_t>(m) * p.N + n,
-           __int2float_rn(s) * __fmul_rn(__ldg(p.sx + m), __ldg(p.sw + n)));
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  pdl_wait_primary();
+  pdl_launch_dependents();  // (after the allocation: a dependent's must not come first)
+  if (warp == 0) {
+    if (lane == 0) {
+      int kb = 0;
+      for (; kb < nkb; ++kb) {
+        const int s = kb % kStages;
+        if (!mbar_wait(&empty[s], (kb / kStages & 1) ^ 1, abort_flag, p.err)) break;
+        mbar_arrive_expect_tx(&full[s], G::kStageBytes);
+        uint8_t* at = smem + s * G::kStageBytes;
+        tma_load_2d(&map_w, &full[s], at, (kb0 + kb) * kBlockK, n0);
+        tma_load_2d(&map_x, &full[s], at + G::kW, (kb0 + kb) * kBlockK, 0);
+      }
+      if (kb < nkb || *abort_flag) {
+        const unsigned long long deadline = globaltimer_ns() + kWaitLimitNs;
+        for (int i = kb - 1; i >= 0 && i >= kb - kStages; --i)
+          mbar_drain_until(&full[i % kStages], i / kStages & 1, deadline);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t kIdesc = make_idesc(2 /*s32*/, 1 /*s8*/, 0, 0, 128, NT);
+      const uint32_t s0 = smem_u32(smem);
+      const uint64_t ad0 = smem_desc_sw128(s0, 16, 1024), bd0 = smem_desc_sw128(s0 + G::kW, 16, 1024);
+      for (int kb = 0; kb < nkb; ++kb) {
+        const int s = kb % kStages;
+        if (!mbar_wait(&full[s], kb / kStages & 1, abort_flag, p.err)) break;
+        tc_fence_after();
+        const uint64_t at = static_cast<uint64_t>(s) * (G::kStageBytes >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kBlockK / 32; ++kk) mma_i8_one(tmem, ad0 + at + kk * 2, bd0 + at + kk * 2, kIdesc, (kb | kk) != 0);
+        mma_commit_one(&empty[s]);
+      }
+      mma_commit_one(done);
+    }
+  }
+  __syncwarp();
+  const int q = warp & 3, row = q * 32 + lane, n = n0 + row;
+  const float4* sx = reinterpret_cast<const float4*>(smem + G::kOffSx);
+  if (warp >= 2) {
+    if (row < NT) reinterpret_cast<float*>(smem + G::kOffSx)[row] = row < p.M ? __ldg(p.sx + row) : 0.0f;
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+  }
+  const float sw = warp >= 2 && n < p.N ? __ldg(p.sw + n) : 0.0f;
+  bool ok = true;
+  TY* y = static_cast<TY*>(p.y) + n;
+  if (warp >= 2) {
+    ok = mbar_wait(done, 0, abort_flag, p.err);
+    tc_fence_after();
+  } else if (lane == 0) {
+    mbar_drain(done, 0);  // nothing reads the ring any more
+  }
+  __syncwarp();
+  int* sums = reinterpret_cast<int*>(smem);  // [NT][128]
+  if (warp >= 2 && ok) {
+    const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll 1
+    for (int c = 0; c < NT && c < p.M; c += 32) {
+      uint32_t r[32];
+      tmem_ld_32x32b_x32(base + c, r);
+      tmem_ld_wait();
+      if (share > 1) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          sums[(c + j) * 128 + row] = static_cast<int>(r[j]);
+      } else if (n < p.N) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 s4 = sx[(c + j) / 4];
+          const float s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (c + j + i < p.M)
+              store1(y + static_cast<int64_t>(c + j + i) * p.N, __int2float_rn(static_cast<int>(r[j + i])) * __fmul_rn(s[i], sw));
+        }
+      }
+    }
+  }
+  if (share > 1) {
+    cluster_sync_all();
+    if (warp >= 2 && ok && n < p.N) {
+      const int m0 = p.M * rank / share, m1 = p.M * (rank + 1) / share;
+      constexpr int kU = 16;  // tokens in flight per thread
+      const uint32_t at = smem_u32(sums + row);
+      for (int m = m0; m < m1; m += kU) {
+        int v[kU] = {};
+        for (int k = 0; k < share; ++k) {
+          const uint32_t from = map_to_rank(at + m * 512, k);
+          int t[kU];
+#pragma unroll
+          for (int i = 0; i < kU; ++i) t[i] = m + i < m1 ? ld_cluster(from + i * 512) : 0;
+#pragma unroll
+          for (int i = 0; i < kU; ++i) v[i] += t[i];
+        }
+#pragma unroll
+        for (int i = 0; i < kU; ++i)
+          if (m + i < m1)
+            store1(y + static_cast<int64_t>(m + i) * p.N, __int2float_rn(v[i]) * __fmul_rn(reinterpret_cast<const float*>(sx)[m + i], sw));
+      }
+    }
+    cluster_sync_all();  // a CTA's sums stay until all have read them
+  } else {
+    tc_fence_before();
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_one(tmem, NT);
   }
 }
 
@@ -493,7 +768,8 @@ __global__ void __launch_bounds__(256) int8_values_kernel(const ValuesParams p) 
 // ---------------------------------------------------------------- host side
 
 bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType type, uint64_t inner, uint64_t outer,
-              uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer) {
+              uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
+              CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -506,14 +782,13 @@ bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType type, uint64
   const cuuint64_t dims[2] = {inner, outer}, strides[1] = {row_bytes};
   const cuuint32_t box[2] = {box_inner, box_outer}, steps[2] = {1, 1};
   return encode(m, type, 2, const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename TY, int BN, bool kTma>
 cudaError_t launch_tiles(const CUtensorMap (&maps)[3], const TileParams& p, cudaStream_t s) {
   auto kernel = int8_tile_kernel<TY, BN, kTma>;
-  constexpr int kSmem = Geo<BN>::kSmemBytes;
+  constexpr int kSmem = Geo<TY, BN>::kSmemBytes;
   static int pairs_of[64] = {};  // pairs resident at once, by device
   int dev = 0;
   cudaGetDevice(&dev);
@@ -536,43 +811,122 @@ cudaError_t launch_tiles(const CUtensorMap (&maps)[3], const TileParams& p, cuda
   return launch_pdl(kernel, dim3(2 * n), dim3(kTileThreads), kSmem, s, maps[0], maps[1], maps[2], p);
 }
 
-template <typename TY>
+template <typename TY, int BN>
 cudaError_t forward_tiles(const int8_t* xq, const int8_t* wq, TileParams p, cudaStream_t s) {
-  p.tiles_m = (p.M + kRows - 1) / kRows;
-  // narrow tiles where they still find a pair each: twice the SMs share the
-  // weights' loads
-  const int narrow = p.tiles_m * ((p.N + 127) / 128);
-  const bool half = narrow <= device_sm_count() / 2;
-  const int bn = half ? 128 : 256;
-  p.ntiles = p.tiles_m * ((p.N + bn - 1) / bn);
+  p.ntiles = p.tiles_m * ((p.N + BN - 1) / BN);
   const bool tma = static_cast<int64_t>(p.N) * sizeof(TY) % 16 == 0;
   CUtensorMap maps[3] = {};
   if (!make_map(&maps[0], xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, p.M, p.K, kBlockK, 128) ||
-      !make_map(&maps[1], wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, p.N, p.K, kBlockK, bn / 2) ||
+      !make_map(&maps[1], wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, p.N, p.K, kBlockK, BN / 2) ||
       (tma && !make_map(&maps[2], p.y, sizeof(TY) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                        p.N, p.M, static_cast<uint64_t>(p.N) * sizeof(TY), 128 / sizeof(TY), 32)))
+                        p.N, p.M, static_cast<uint64_t>(p.N) * sizeof(TY), 32, 32,
+                        sizeof(TY) == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B)))
     return cudaErrorInvalidValue;
-  if (half) return tma ? launch_tiles<TY, 128, true>(maps, p, s) : launch_tiles<TY, 128, false>(maps, p, s);
-  return tma ? launch_tiles<TY, 256, true>(maps, p, s) : launch_tiles<TY, 256, false>(maps, p, s);
-}
-
-template <typename TY, int kTok, int R, int kU>
-cudaError_t launch_few(const FewParams& p, cudaStream_t s) {
-  auto kernel = int8_few_kernel<TY, kTok, R, kU>;
-  constexpr size_t kPerWarp = static_cast<size_t>(16 * R) * 8 * kTok * sizeof(int);
-  static bool done[64] = {};
-  if (cudaError_t e = allow_smem(kernel, kPerWarp * kFewWarps, done); e != cudaSuccess) return e;
-  const int nb = (p.K + 63) / 64;
-  int warps = kFewWarps;
-  while (warps > 1 && 2 * warps > nb) warps /= 2;  // two blocks of K per warp at least
-  return launch_pdl(kernel, dim3((p.N + 16 * R - 1) / (16 * R)), dim3(32 * warps), kPerWarp * warps, s, p);
+  return tma ? launch_tiles<TY, BN, true>(maps, p, s) : launch_tiles<TY, BN, false>(maps, p, s);
 }
 
 template <typename TY>
-cudaError_t forward_few(const FewParams& p, cudaStream_t s) {
-  if (p.M <= 8) return launch_few<TY, 1, 1, 4>(p, s);
-  if (p.M <= 16) return launch_few<TY, 2, 1, 4>(p, s);
-  return launch_few<TY, 4, 1, 2>(p, s);
+cudaError_t forward_tiles(const int8_t* xq, const int8_t* wq, TileParams p, cudaStream_t s) {
+  p.tiles_m = (p.M + kRows - 1) / kRows;
+  // The tiles' width: the least time of the busiest pair, its tiles times a
+  // stage's MMAs (measured: 122 cycles for 128 columns, 168 for 256, so 76 + 0.36 a
+  // column) and the end of one tile.
+  const int pairs = device_sm_count() / 2, nkb = (p.K + kBlockK - 1) / kBlockK;
+  int best = 256;
+  int64_t least = INT64_MAX;
+  for (int bn = 256; bn >= 64; bn -= 32) {
+    const int64_t rounds = (static_cast<int64_t>(p.tiles_m) * ((p.N + bn - 1) / bn) + pairs - 1) / pairs;
+    const int64_t cost = rounds * nkb * (4 * (7600 + 36 * bn)) + 1000 * bn;
+    if (cost < least) best = bn, least = cost;
+  }
+  switch (best) {
+    case 64: return forward_tiles<TY, 64>(xq, wq, p, s);
+    case 96: return forward_tiles<TY, 96>(xq, wq, p, s);
+    case 128: return forward_tiles<TY, 128>(xq, wq, p, s);
+    case 160: return forward_tiles<TY, 160>(xq, wq, p, s);
+    case 192: return forward_tiles<TY, 192>(xq, wq, p, s);
+    case 224: return forward_tiles<TY, 224>(xq, wq, p, s);
+    default: return forward_tiles<TY, 256>(xq, wq, p, s);
+  }
+}
+
+template <typename TY, int kTok, int R>
+cudaError_t launch_few(const int8_t* xq, const int8_t* wq, FewParams p, cudaStream_t s) {
+  using G = Few<kTok, R>;
+  auto kernel = int8_few_kernel<TY, kTok, R>;
+  static bool done[64] = {};
+  if (cudaError_t e = allow_smem(kernel, G::kSmemBytes, done); e != cudaSuccess) return e;
+  CUtensorMap x, w;
+  if (!make_map(&x, xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, p.M, p.K, 128, G::kM) ||
+      !make_map(&w, wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, p.N, p.K, 128, G::kN))
+    return cudaErrorInvalidValue;
+  p.ntiles = (p.N + G::kN - 1) / G::kN;
+  const int most = 2 * device_sm_count();
+  return launch_pdl(kernel, dim3(p.ntiles < most ? p.ntiles : most), dim3(G::kThreads), G::kSmemBytes, s, x, w, p);
+}
+
+template <typename TY, int kTok>
+cudaError_t forward_few(const int8_t* xq, const int8_t* wq, const FewParams& p, cudaStream_t s) {
+  // the tiles' channels: those with the least to load (the channels' rows, and for
+  // each tile the tokens', from L2, so half of them) for the busiest SM and for
+  // the SMs at work on average
+  constexpr int kWidest = kTok == 4 ? 3 : 4;
+  const int sms = device_sm_count();
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int r = kWidest; r >= 1; --r) {
+    const int64_t tiles = (p.N + 16 * r - 1) / (16 * r), rows = 16 * r + 4 * kTok;
+    const int64_t cost = (tiles + sms - 1) / sms * rows * 16 + tiles * rows * 16 / (tiles < sms ? tiles : sms);
+    if (cost < least) best = r, least = cost;
+  }
+  switch (best) {
+    case 1: return launch_few<TY, kTok, 1>(xq, wq, p, s);
+    case 2: return launch_few<TY, kTok, 2>(xq, wq, p, s);
+    case 3: return launch_few<TY, kTok, 3>(xq, wq, p, s);
+    default: return launch_few<TY, kTok, kWidest>(xq, wq, p, s);
+  }
+}
+
+template <typename TY>
+cudaError_t forward_few(const int8_t* xq, const int8_t* wq, const FewParams& p, cudaStream_t s) {
+  if (p.M <= 8) return forward_few<TY, 1>(xq, wq, p, s);
+  return p.M <= 16 ? forward_few<TY, 2>(xq, wq, p, s) : forward_few<TY, 4>(xq, wq, p, s);
+}
+
+template <typename TY, int NT>
+cudaError_t launch_mid(const int8_t* xq, const int8_t* wq, MidParams p, cudaStream_t s) {
+  using G = Mid<NT>;
+  auto kernel = int8_mid_kernel<TY, NT>;
+  static bool done[64] = {};
+  if (cudaError_t e = allow_smem(kernel, G::kSmemBytes, done); e != cudaSuccess) return e;
+  CUtensorMap x, w;
+  if (!make_map(&x, xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, p.M, p.K, kBlockK, NT) ||
+      !make_map(&w, wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, p.N, p.K, kBlockK, 128))
+    return cudaErrorInvalidValue;
+  // as many CTAs per tile as leave each an SM and two stages
+  const int tiles = (p.N + 127) / 128, boxes = (p.K + kBlockK - 1) / kBlockK, sms = device_sm_count();
+  p.share = 1;
+  while (p.share < 8 && tiles * p.share * 2 <= sms && boxes >= p.share * 4) p.share *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(tiles * p.share);
+  cfg.blockDim = dim3(kMidThreads);
+  cfg.dynamicSmemBytes = G::kSmemBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.share;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, x, w, p);
+}
+
+template <typename TY>
+cudaError_t forward_mid(const int8_t* xq, const int8_t* wq, const MidParams& p, cudaStream_t s) {
+  if (p.M <= 32) return launch_mid<TY, 32>(xq, wq, p, s);
+  return launch_mid<TY, 64>(xq, wq, p, s);
 }
 
 size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -582,8 +936,12 @@ size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 cudaError_t launch_int8_forward(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw, int64_t M,
                                 int64_t N, int64_t K, void* y, int y_f32, int* err, cudaStream_t s) {
   if (M <= kFewMost) {
-    FewParams p{xq, sx, wq, sw, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), y};
-    return y_f32 ? forward_few<float>(p, s) : forward_few<__nv_bfloat16>(p, s);
+    const FewParams p{static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), 0, sx, sw, y, err};
+    return y_f32 ? forward_few<float>(xq, wq, p, s) : forward_few<__nv_bfloat16>(xq, wq, p, s);
+  }
+  if (M <= kMidMost) {
+    const MidParams p{static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), 1, sx, sw, y, err};
+    return y_f32 ? forward_mid<float>(xq, wq, p, s) : forward_mid<__nv_bfloat16>(xq, wq, p, s);
   }
   TileParams p{};
   p.M = static_cast<int>(M);
