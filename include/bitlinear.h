@@ -521,12 +521,13 @@ bl_status bl_swiglu_backward(const void* dy, const int8_t* gate_codes, const flo
  *   rstd[m]  = 1 / sqrt(sum_k sum[m,k]^2 / K + eps)      sums in fp32
  *   t[m,k]   = fp32(sum[m,k] * weight[k])
  *   a        = max(fp32(max_k |t[m,k]| * rstd[m]), 1e-5)
- *   xq[m,k]  = rint_half_even(fp32(t[m,k] * fp32(rstd[m] * fp32(127 / a))))   in [-127, 127]
+ *   xq[m,k]  = rint_half_even(t[m,k] * rstd[m] * 127 / a)      in [-127, 127]
  *   sx[m]    = fp32(a / 127)
  *
  * xq and sx are S2's form of y = sum * rstd * weight, which itself is not
  * rounded to a type of its own on the way (S2 takes a bf16 x): the operand of
- * bl_forward (K % 32 == 0) and of L1 (K % 16 == 0).
+ * bl_forward (K % 32 == 0) and of L1 (K % 16 == 0). The quotient's factor carries a
+ * few roundings in fp32: next to a tie a code may be another one, by one.
  * x [M,K] of x_dtype, residual and sum [M,K] of s_dtype (the stream's), weight
  * [K] of p_dtype or NULL (ones): BL_BF16 or BL_F32 each, not an fp32 x with a
  * bf16 stream. residual and sum both NULL: x is the stream itself (s_dtype is

@@ -161,11 +161,6 @@ cudaError_t launch_norm_backward(const void* dy, const void* x, const int8_t* co
                                  int64_t K, int rms, void* dx, void* dweight, void* dbias, int accumulate,
                                  void* workspace, cudaStream_t s);
 
-// dweight, dbias [K] (either may be null) from nparts (at most kPlanSms) partial
-// rows, parts [nparts][2][K], added in a fixed order (k_norm.cu).
-cudaError_t launch_norm_join(const float* parts, int nparts, int K, void* dweight, void* dbias, int p_f32,
-                             int accumulate, cudaStream_t s);
-
 // RMS norm with the residual's addition and an INT8 result (k_norm_quant.cu).
 // f32 flags: x, the residual stream, the gain, dy.
 constexpr int64_t kNormQuantMaxK = 8192;

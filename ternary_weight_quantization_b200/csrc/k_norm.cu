@@ -908,12 +908,6 @@ cudaError_t backward(NormBwdArgs p, int* nparts, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_norm_join(const float* parts, int nparts, int K, void* dweight, void* dbias, int p_f32,
-                             int accumulate, cudaStream_t s) {
-  return launch_pdl(norm_join_kernel, dim3(static_cast<unsigned>((K + 31) / 32)), dim3(1024), 0, s, parts, nparts, K,
-                    dweight, dbias, p_f32, accumulate);
-}
-
 size_t norm_backward_workspace_bytes(int64_t M, int64_t K) {
   const size_t parts = static_cast<size_t>(kMaxParts) * 2 * static_cast<size_t>(K) * 4;
   return parts + (K > kBwdMaxK ? static_cast<size_t>(M) * 8 : 0);
@@ -974,8 +968,8 @@ cudaError_t launch_norm_backward(const void* dy, const void* x, const int8_t* co
     e = f32 ? go(float{}) : go(__nv_bfloat16{});
   }
   if (e != cudaSuccess || !sums) return e;
-  return launch_norm_join(static_cast<const float*>(workspace), nparts, static_cast<int>(K), dweight, dbias, p_f32,
-                          accumulate, s);
+  return launch_pdl(norm_join_kernel, dim3(static_cast<unsigned>((K + 31) / 32)), dim3(1024), 0, s,
+                    static_cast<const float*>(workspace), nparts, static_cast<int>(K), dweight, dbias, p_f32, accumulate);
 }
 
 }  // namespace bl

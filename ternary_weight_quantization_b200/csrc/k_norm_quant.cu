@@ -5,7 +5,8 @@
 //   forward   r = rn(x + residual)          kept in the stream's type
 //             rstd = 1 / sqrt(mean(r^2) + eps)
 //             t = r w, a = max(max |t| rstd, 1e-5)
-//             xq = rint(t (rstd (127 / a))), sx = a / 127
+//             xq = rint(t (127 / max |t|))    (t rstd 127 / 1e-5 where a is that)
+//             sx = a / 127
 //   backward  n = r rstd, g = dy w          (the quantiser's Jacobian is 1)
 //             d = dsum + rstd (g - n mean(g n))
 //             dresidual, dx = d, dweight = sum over rows of dy n
@@ -52,27 +53,41 @@ struct FwdArgs {
   float* sx;
 };
 
-// v rounded to the stream's type, and stored there.
-__device__ __forceinline__ void keep8(__nv_bfloat16* p, f32x2 (&v)[4]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w[i] = pack_bf16x2(v[i]);
-    v[i] = pair2(bf16_lo(w[i]), bf16_hi(w[i]));
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void keep8(float* p, f32x2 (&v)[4]) { store8(p, v); }
-
-// Bits of the largest |v| (finite values and infinity in their order, NaN above).
-__device__ __forceinline__ uint32_t top_bits(const f32x2 (&v)[4], uint32_t m) {
+// The larger of m and the absolute values of v; a NaN if there is one.
+__device__ __forceinline__ float top_of(const f32x2 (&v)[4], float m) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float lo, hi;
     split2(v[i], lo, hi);
-    m = max(m, max(__float_as_uint(lo) & 0x7FFFFFFFu, __float_as_uint(hi) & 0x7FFFFFFFu));
+    asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(fabsf(lo)), "f"(fabsf(hi)));
   }
   return m;
+}
+
+// The sum of 8 values of x and of the residual, rounded to the stream's type and
+// stored. (Two bf16 numbers add exactly in fp32, or so far apart that the smaller
+// one is lost in bf16 all the same: the packed bf16 addition, rounded once, gives
+// what an fp32 addition and a rounding would.)
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void add_keep(const Raw8<__nv_bfloat16>& x, const Raw8<__nv_bfloat16>& r, __nv_bfloat16* to,
+                                         f32x2 (&v)[4]) {
+  Raw8<__nv_bfloat16> o;
+  o.a = make_uint4(add_bf16x2(x.a.x, r.a.x), add_bf16x2(x.a.y, r.a.y), add_bf16x2(x.a.z, r.a.z), add_bf16x2(x.a.w, r.a.w));
+  *reinterpret_cast<uint4*>(to) = o.a;
+  o.get(v);
+}
+template <typename TX>
+__device__ __forceinline__ void add_keep(const Raw8<TX>& x, const Raw8<float>& r, float* to, f32x2 (&v)[4]) {
+  f32x2 o[4];
+  x.get(v);
+  r.get(o);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = add2(v[i], o[i]);
+  store8(to, v);
 }
 
 constexpr int kFwdThreads = 512;  // most threads of a forward block
@@ -134,35 +149,33 @@ __global__ void __launch_bounds__(kFwdThreads, kVecs <= 2 ? 2 : 1) norm_quant_fo
   for (uint32_t slot = mine; rows > 0; --rows, row += step, at += step_k) {
     copy_async_wait<kDepth - 1>();
     f32x2 v[kVecs][4], q2 = 0;  // t, and the sum of r^2
-    uint32_t top = 0;
+    float most = 0.0f;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
       if (!live(j)) continue;
       const uint32_t from = slot + j * kPieces * stride;
       Raw8<TX> rx;
       read_raw(from, stride, rx);
-      rx.get(v[j]);
       if (added) {
         Raw8<TS> rs;
         read_raw(from + kPx * stride, stride, rs);
-        f32x2 o[4];
-        rs.get(o);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], o[i]);
-        keep8(static_cast<TS*>(p.sum) + at + j * cs, v[j]);
+        add_keep(rx, rs, static_cast<TS*>(p.sum) + at + j * cs, v[j]);
+      } else {
+        rx.get(v[j]);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         q2 = fma2(v[j][i], v[j][i], q2);
         v[j][i] = mul2(v[j][i], w[j][i]);
       }
-      top = top_bits(v[j], top);
+      most = top_of(v[j], most);
     }
     issue(slot);
     slot += row_stride;
     if (slot == end) slot = mine;
     float q = warp_sum(sum2(q2));
-    top = __reduce_max_sync(0xffffffffu, top);
+    // (as integers the bits of values from 0 on have the values' order, NaN last)
+    uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
     if constexpr (!kWarp) {
       // the buffers alternate, so one barrier per row is enough: a warp writes
       // one again only after a barrier that every reader of it has reached
@@ -180,13 +193,17 @@ __global__ void __launch_bounds__(kFwdThreads, kVecs <= 2 ? 2 : 1) norm_quant_fo
     }
     // a sum beyond fp32 (or a NaN) leaves NaN, not a row of zeros
     const float rstd = q < __uint_as_float(0x7F800000u) ? rsqrt_of(fmaf(q, p.inv_k, p.eps)) : __uint_as_float(0x7FC00000u);
-    const float a = max_nan(__fmul_rn(__uint_as_float(top), rstd), kQuantFloor);
-    const float f = __fmul_rn(rstd, __fdiv_rn(127.0f, a));
+    const float most_t = __uint_as_float(top), a = max_nan(__fmul_rn(most_t, rstd), kQuantFloor);
+    // 127 / a of y is 127 / max |t| of t, but where a is the floor: the reciprocal's
+    // approximation (an fp32 step off) and one product
+    float f;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(f) : "f"(most_t));
+    f = a > kQuantFloor ? f * 127.0f : rstd * (127.0f / kQuantFloor);
     if (t == 0) {
       p.rstd[row] = rstd;
       p.sx[row] = __fdiv_rn(a, 127.0f);
     }
-    // f is four roundings from 127 / max |t|, so |t f| ends below 127.5
+    // f is a few fp32 steps from 127 / max |t| at most, so |t f| ends below 127.5
 #pragma unroll
     for (int j = 0; j < kVecs; ++j)
       if (live(j)) *reinterpret_cast<uint2*>(p.xq + at + j * cs) = act8_codes8(v[j], f);
@@ -207,7 +224,7 @@ struct BwdArgs {
   float inv_k;
   void* dresidual;  // or null
   void* dx;         // or null
-  float* parts;     // [blocks][2][K], the first half used; or null
+  float* parts;     // [blocks][K], or null
 };
 
 constexpr int kBwdThreads = 512;  // of a block, one block per SM
@@ -232,7 +249,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_quant_backward_kernel(con
   auto live = [&](int j) { return kFull || c0 + j * cs < K; };
   const uint32_t stride = blockDim.x * 16, row_stride = kBwdVecs * kPieces * stride;
   const uint32_t mine = smem_u32(ring) + threadIdx.x * 16, end = mine + kDepth * row_stride;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * ngrp + grp;
+  // neighbouring rows to neighbouring blocks, so that the blocks' rows differ by one
+  const int64_t first = static_cast<int64_t>(grp) * gridDim.x + blockIdx.x;
   const int64_t step = static_cast<int64_t>(gridDim.x) * ngrp, step_k = step * K;
   int rows = first < p.M ? static_cast<int>((p.M - 1 - first) / step) + 1 : 0, left = rows;
   int64_t at = first * K + c0, next = at;  // the thread's place in this row, and in the row to load next
@@ -321,11 +339,49 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_quant_backward_kernel(con
 #pragma unroll
   for (int j = 0; j < kBwdVecs; ++j) store8(joint + grp * width + c0 + j * cs, dw[j]);
   __syncthreads();
-  float* part = p.parts + static_cast<int64_t>(blockIdx.x) * 2 * K;
+  float* part = p.parts + static_cast<int64_t>(blockIdx.x) * K;
   for (int c = threadIdx.x; c < K; c += blockDim.x) {
     float a = 0.0f;
     for (int i = 0; i < ngrp; ++i) a += joint[i * width + c];
     part[c] = a;
+  }
+}
+
+// dweight from the blocks' partial rows: 16 columns per block, the rows (at most
+// kPlanSms) spread over 32 threads of each, whose loads are all in flight at once.
+// (8 threads of each: 1.3 us more at 2560 columns.)
+constexpr int kJoinCols = 16, kJoinSplit = 32;
+
+__global__ void __launch_bounds__(kJoinCols* kJoinSplit)
+    norm_quant_join_kernel(const float* __restrict__ parts, int nparts, int K, void* dweight, int p_f32, int accumulate) {
+  __shared__ float sums[kJoinSplit][kJoinCols + 1];
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int x = threadIdx.x % kJoinCols, y = threadIdx.x / kJoinCols;
+  const int c = static_cast<int>(blockIdx.x) * kJoinCols + x;
+  constexpr int kMost = (kPlanSms + kJoinSplit - 1) / kJoinSplit;
+  float a = 0.0f;
+  if (c < K) {
+    float v[kMost];
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      const int r = y + i * kJoinSplit;
+      v[i] = r < nparts ? parts[static_cast<int64_t>(r) * K + c] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) a += v[i];
+  }
+  sums[y][x] = a;
+  __syncthreads();
+  if (y != 0 || c >= K) return;
+#pragma unroll
+  for (int i = 1; i < kJoinSplit; ++i) a += sums[i][x];
+  if (p_f32) {
+    float* o = static_cast<float*>(dweight) + c;
+    *o = accumulate ? a + *o : a;
+  } else {
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(dweight) + c;
+    *o = __float2bfloat16_rn(accumulate ? a + __bfloat162float(*o) : a);
   }
 }
 
@@ -397,7 +453,7 @@ cudaError_t backward(BwdArgs p, int* nparts, cudaStream_t s) {
 
 }  // namespace
 
-size_t norm_quant_backward_workspace_bytes(int64_t K) { return static_cast<size_t>(kPlanSms) * 2 * static_cast<size_t>(K) * 4; }
+size_t norm_quant_backward_workspace_bytes(int64_t K) { return static_cast<size_t>(kPlanSms) * static_cast<size_t>(K) * 4; }
 
 cudaError_t launch_norm_quant_forward(const void* x, int x_f32, const void* residual, int s_f32, const void* weight,
                                       int p_f32, int64_t M, int64_t K, float eps, void* sum, float* rstd, int8_t* xq,
@@ -449,8 +505,9 @@ cudaError_t launch_norm_quant_backward(const void* dy, int dy_f32, const void* d
     if (e != cudaSuccess) return e;
   }
   if (!dweight) return cudaSuccess;
-  return launch_norm_join(static_cast<const float*>(workspace), nparts, static_cast<int>(K), dweight, nullptr, p_f32,
-                          accumulate, s);
+  return launch_pdl(norm_quant_join_kernel, dim3(static_cast<unsigned>((K + kJoinCols - 1) / kJoinCols)),
+                    dim3(kJoinCols * kJoinSplit), 0, s, static_cast<const float*>(workspace), nparts, static_cast<int>(K),
+                    dweight, p_f32, accumulate);
 }
 
 }  // namespace bl

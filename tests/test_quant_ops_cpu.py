@@ -114,7 +114,7 @@ def test_empty_work_is_ok_without_gpu():
 
 
 def test_workspace_sizes():
-    assert bl.bl_norm_quant_backward_workspace_size(4096, 2560) == 148 * 2 * 2560 * 4
+    assert bl.bl_norm_quant_backward_workspace_size(4096, 2560) == 148 * 2560 * 4
     assert bl.bl_norm_quant_backward_workspace_size(1, 64) == bl.bl_norm_quant_backward_workspace_size(1 << 20, 64)
     assert bl.bl_norm_quant_backward_workspace_size(0, 64) == 0 and bl.bl_norm_quant_backward_workspace_size(4, 60) == 0
     assert bl.bl_grad_norm_workspace_size(0) == 0
