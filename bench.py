@@ -910,7 +910,9 @@ def run_lm(args, rank, world, local_rank):
     """Decoder-LM mode: the 4-layer LM of workloads/lm.py trained through the
     library (every projection a BitLinear call; the rest plain PyTorch in
     fp64, the precision the LM oracle keeps it in; with --lm-ops library the
-    norms, the gating and the head's loss are the library's too, in fp32) for
+    norms, the gating and the head's loss are the library's too, in fp32, with
+    --lm-ops fused also the residual's addition and the quantiser in one pass
+    with each norm) for
     its 50 steps on each rank (independent replicas). Reports tokens per
     second (batch x sequence per step over the mean device time of a step,
     the first step excluded) and the largest |loss - oracle loss| over the
@@ -921,8 +923,8 @@ def run_lm(args, rank, world, local_rank):
     dev = torch.device("cuda", local_rank)
     torch.cuda.set_device(dev)
     cfg = LM_CONFIG
-    library = args.lm_ops == "library"
-    how = {"dtype": torch.float32, "library_ops": True, "saved8": True} if library else {}
+    library, fused = args.lm_ops != "torch", args.lm_ops == "fused"
+    how = {"dtype": torch.float32, "library_ops": True, "saved8": not fused, "fused_norms": fused} if library else {}
     losses, ms = train_lm(lm_init(cfg, seed=0), lm_batches(cfg, seed=0), cfg, dev, timing=True, **how)
     job_ms = job_time_ms(ms, world, dev)
     worst = None
@@ -1002,9 +1004,10 @@ def main():
                     help="layer-stack mode (prints its own line instead of the single-layer one)")
     ap.add_argument("--lm", action="store_true",
                     help="decoder-LM training mode (prints its own line)")
-    ap.add_argument("--lm-ops", choices=["torch", "library"], default="torch",
+    ap.add_argument("--lm-ops", choices=["torch", "library", "fused"], default="torch",
                     help="the decoder LM's norms, gating and head loss: plain PyTorch in fp64, or the library's "
-                         "operators (fp32, activations kept in 8 bits)")
+                         "operators (fp32, activations kept in 8 bits), fused: the norms with the residual's addition and "
+                         "the quantiser in one pass")
     ap.add_argument("--signsgd", action="store_true",
                     help="sign-gradient data-parallel step mode (prints its own line)")
     ap.add_argument("--few-tokens", default=None,

@@ -33,6 +33,16 @@ for the backward, not in fp32) and the LM head with the cross-entropy
 (``bl_linear_xent_forward`` / ``bl_linear_xent_backward``: no logits). The head
 then takes the last norm's output and its weights in bf16, and a target outside
 the vocabulary leaves its token out of the mean.
+
+With ``fused_norms`` too, what lies between two blocks' projections is one pass
+(``bl_norm_quant_forward`` / ``bl_norm_quant_backward``): the last projection's
+output is added to the residual stream, the sum normed, and the norm's result
+quantised once for all projections that read it (q, k and v; gate and up). The
+norm's result is then not rounded to bf16 in front of the quantiser. ``head8``
+runs the head on 8-bit codes of the last norm's output and of the head's rows
+(``bl_int8_linear_forward`` / ``bl_int8_linear_backward``, straight-through
+gradients); its logits go through torch's cross-entropy. ``train_lm`` scales the
+gradients down to ``max_norm`` over all parameters (``bl_clip_grads``).
 """
 
 from __future__ import annotations
@@ -44,8 +54,8 @@ from torch.autograd.function import once_differentiable
 
 from . import bitlinear as b
 
-__all__ = ["BitLinearFunction", "RMSNormFunction", "SwigluFunction", "HeadLossFunction", "to_bf16_rn", "lm_loss",
-           "adamw_step", "train_lm"]
+__all__ = ["BitLinearFunction", "RMSNormFunction", "SwigluFunction", "HeadLossFunction", "NormProjectionsFunction",
+           "NormHead8Function", "to_bf16_rn", "lm_loss", "clip_gradients", "adamw_step", "train_lm"]
 
 _BF16_MIN_NORMAL = 2.0 ** -126
 
@@ -197,16 +207,120 @@ class HeadLossFunction(torch.autograd.Function):
         return (None if dH is None else dH.to(ctx.dtypes[0])), (None if dW is None else dW.to(ctx.dtypes[1])), None
 
 
+def _normed(x, residual, gain, eps):
+    """The stream x + residual [M, K] (fp32; x, in bf16, may be None), 1 / rms,
+    and the 8-bit form of its norm."""
+    M, K = residual.shape
+    stream, gain = _operand(residual), _operand(gain)
+    buf = b.NormQuantBuffers.allocate(M, K, torch.bfloat16, torch.float32, gain.dtype, backward=False, device=gain.device)
+    if x is None:
+        b.bl_norm_quant_forward(stream, None, gain, eps, None, buf.rstd, buf.xq, buf.sx)
+        buf.sum = stream
+    else:
+        b.bl_norm_quant_forward(_operand(x.to(torch.bfloat16)), stream, gain, eps, buf.sum, buf.rstd, buf.xq, buf.sx)
+    return gain, buf
+
+
+def _norm_gradients(dy, dsum, stream, gain, rstd, x_dtype):
+    """Gradients of x (None where there is none), of the residual and of the gain."""
+    dresidual, dgain = torch.empty_like(stream), torch.empty_like(gain)
+    dx = None if x_dtype is None else torch.empty(stream.shape, dtype=torch.bfloat16, device=stream.device)
+    ws = torch.empty(max(b.bl_norm_quant_backward_workspace_size(*stream.shape), 16), dtype=torch.uint8, device=stream.device)
+    b.bl_norm_quant_backward(dy, None if dsum is None else _operand(dsum), stream, gain, rstd, dx, dresidual, dgain, ws)
+    return (None if dx is None else dx.to(x_dtype)), dresidual, dgain
+
+
+class NormProjectionsFunction(torch.autograd.Function):
+    """(stream, y_1, ..., y_n): the stream x + residual [M, K] (fp32; x, the last
+    projection's output, in bf16 precision, or None: the stream is the residual),
+    and BitLinear of its RMS norm, quantised once, with each of the masters
+    weights [N_i, K]."""
+
+    @staticmethod
+    def forward(ctx, x, residual, gain, eps, *weights):
+        M, K = residual.shape
+        dev = residual.device
+        gain, buf = _normed(x, residual, gain, eps)
+        saved, outs = [], []
+        for w in weights:
+            N = w.shape[0]
+            w32 = _operand(w.detach().to(torch.float32))
+            packed = torch.empty((N, K // 4), dtype=torch.uint8, device=dev)
+            gamma = torch.empty(1, dtype=torch.float32, device=dev)
+            ws = torch.empty(max(b.bl_quantize_weight_workspace_size(N, K), 16), dtype=torch.uint8, device=dev)
+            y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+            b.bl_quantize_weight(w32, packed, gamma, ws)
+            b.bl_forward(buf.xq, buf.sx, packed, gamma, y)
+            saved += [packed, gamma]
+            outs.append(y.to(residual.dtype))
+        stream = buf.sum if x is not None else residual.clone()
+        ctx.save_for_backward(buf.sum, gain, buf.rstd, buf.xq, buf.sx, *saved)
+        ctx.x_dtype = None if x is None else x.dtype
+        ctx.w_dtypes = [w.dtype for w in weights]
+        return (stream, *outs)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dsum, *dys):
+        stream, gain, rstd, xq, sx, *saved = ctx.saved_tensors
+        M, K = xq.shape
+        dy, dws = None, []
+        for g, packed, gamma, dt in zip(dys, saved[::2], saved[1::2], ctx.w_dtypes):
+            N = packed.shape[0]
+            dX = torch.empty((M, K), dtype=torch.bfloat16, device=g.device)
+            dW = torch.empty((N, K), dtype=torch.float32, device=g.device)
+            ws = torch.empty(max(b.bl_backward_workspace_size(M, N, K), 16), dtype=torch.uint8, device=g.device)
+            b.bl_backward(_operand(to_bf16_rn(g)), xq, sx, packed, gamma, dX, dW, workspace=ws)
+            dy = dX.float() if dy is None else dy.add_(dX)
+            dws.append(dW.to(dt))
+        return (*_norm_gradients(dy, dsum, stream, gain, rstd, ctx.x_dtype), None, *dws)
+
+
+class NormHead8Function(torch.autograd.Function):
+    """Logits [M, V] (fp32) of a head [V, K] kept in 8 bits per row, from the RMS
+    norm of the stream x + residual (as in NormProjectionsFunction) in 8 bits per
+    token."""
+
+    @staticmethod
+    def forward(ctx, x, residual, gain, eps, head):
+        (M, K), V = residual.shape, head.shape[0]
+        gain, buf = _normed(x, residual, gain, eps)
+        wq = torch.empty((V, K), dtype=torch.int8, device=head.device)
+        sw = torch.empty(V, dtype=torch.float32, device=head.device)
+        b.bl_quantize_act(_operand(head.detach().to(torch.bfloat16)), wq, sw)
+        logits = torch.empty((M, V), dtype=torch.float32, device=head.device)
+        b.bl_int8_linear_forward(buf.xq, buf.sx, wq, sw, logits)
+        ctx.save_for_backward(buf.sum, gain, buf.rstd, buf.xq, buf.sx, wq, sw)
+        ctx.x_dtype = None if x is None else x.dtype
+        ctx.w_dtype = head.dtype
+        return logits
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        stream, gain, rstd, xq, sx, wq, sw = ctx.saved_tensors
+        (M, K), V = xq.shape, wq.shape[0]
+        dX = torch.empty((M, K), dtype=torch.bfloat16, device=g.device)
+        dW = torch.empty((V, K), dtype=torch.float32, device=g.device)
+        ws = torch.empty(max(b.bl_int8_linear_backward_workspace_size(M, V, K), 16), dtype=torch.uint8, device=g.device)
+        b.bl_int8_linear_backward(_operand(g.to(torch.bfloat16)), xq, sx, wq, sw, dX, dW, workspace=ws)
+        return (*_norm_gradients(dX, None, stream, gain, rstd, ctx.x_dtype), None, dW.to(ctx.w_dtype))
+
+
 def _rmsnorm(x, g, eps):
     return x / torch.sqrt(torch.mean(x * x, dim=-1, keepdim=True) + eps) * g
 
 
-def lm_loss(params: dict, ids: torch.Tensor, cfg, library_ops: bool = False, saved8: bool = False) -> torch.Tensor:
+def lm_loss(params: dict, ids: torch.Tensor, cfg, library_ops: bool = False, saved8: bool = False,
+            fused_norms: bool = False, head8: bool = False) -> torch.Tensor:
     """Mean next-token cross-entropy of ids [B, S + 1] (parameters of one float
     dtype; fp32 with library_ops: the norms, the gating and the head's loss by
-    the library, the norms' inputs kept in 8 bits with saved8)."""
+    the library, the norms' inputs kept in 8 bits with saved8). fused_norms, head8
+    (with library_ops, without saved8): the module's docstring."""
     if library_ops and params["embed"].dtype != torch.float32:
         raise ValueError(f"library_ops takes fp32 parameters, got {params['embed'].dtype}")
+    if (fused_norms or head8) and (not library_ops or saved8):
+        raise ValueError("fused_norms and head8 go with library_ops and without saved8")
 
     def norm(x, g):
         if library_ops:
@@ -225,21 +339,60 @@ def lm_loss(params: dict, ids: torch.Tensor, cfg, library_ops: bool = False, sav
     h = (one_hot @ embed).reshape(B, S, d)
     causal = torch.ones(S, S, dtype=torch.bool, device=ids.device).tril()
     bl = BitLinearFunction.apply
+    pending = None  # the last projection's output, still to be added to h (fused_norms)
+
+    def normed_projections(gain, weights):
+        """h with what is pending added, and the projections of its norm."""
+        if fused_norms:
+            stream, *ys = NormProjectionsFunction.apply(pending, h.reshape(-1, d), gain, cfg.norm_eps, *weights)
+            return stream.reshape(B, S, d), ys
+        a = norm(h, gain)
+        return h, [bl(a, w) for w in weights]
+
     for i in range(cfg.layers):
         def p(n):
             return params[f"layer{i}.{n}"]
-        a = norm(h, p("attn_norm"))
-        q, k, v = (bl(a, p(n)).reshape(B, S, H, dh).transpose(1, 2) for n in ("q", "k", "v"))
+        h, qkv = normed_projections(p("attn_norm"), [p(n) for n in ("q", "k", "v")])
+        q, k, v = (y.reshape(B, S, H, dh).transpose(1, 2) for y in qkv)
         scores = (q @ k.transpose(-1, -2)) / math.sqrt(dh)
         scores = scores.masked_fill(~causal, float("-inf"))
         o = (torch.softmax(scores, dim=-1) @ v).transpose(1, 2).reshape(B * S, d)
-        h = h + bl(o, p("o")).reshape(B, S, d)
-        m = norm(h, p("mlp_norm"))
-        h = h + bl(gated(bl(m, p("gate")), bl(m, p("up"))), p("down")).reshape(B, S, d)
+        pending = bl(o, p("o"))
+        if not fused_norms:
+            h = h + pending.reshape(B, S, d)
+        h, (gate, up) = normed_projections(p("mlp_norm"), [p("gate"), p("up")])
+        pending = bl(gated(gate, up), p("down"))
+        if not fused_norms:
+            h = h + pending.reshape(B, S, d)
+    if head8:
+        logits = NormHead8Function.apply(pending if fused_norms else None, h.reshape(-1, d), params["final_norm"],
+                                         cfg.norm_eps, params["head"])
+        return torch.nn.functional.cross_entropy(logits, y_ids.reshape(-1))
+    if fused_norms:
+        h = h + pending.reshape(B, S, d)
     last = norm(h, params["final_norm"])
     if library_ops:
         return HeadLossFunction.apply(last, params["head"], y_ids.reshape(-1))
     return torch.nn.functional.cross_entropy(last @ params["head"].T, y_ids.reshape(-1))
+
+
+def clip_gradients(grads, max_norm: float):
+    """The gradients (tensors, bf16 or fp32), scaled down in place to a norm over
+    all of them of max_norm at most, and that norm [1] before. A gradient that is
+    not contiguous, or that shares memory with one before it (autograd may hand
+    one tensor to two leaves), is replaced by a copy."""
+    out, seen = [], set()
+    for g in grads:
+        g = g.contiguous()
+        storage = g.untyped_storage().data_ptr()
+        if g.numel() and storage in seen:
+            g = g.clone()
+        seen.add(storage)
+        out.append(g)
+    norm = torch.empty(1, dtype=torch.float32, device=out[0].device)
+    ws = torch.empty(max(b.bl_grad_norm_workspace_size(len(out)), 16), dtype=torch.uint8, device=norm.device)
+    b.bl_clip_grads(out, max_norm, norm, ws)
+    return out, norm
 
 
 def adamw_step(params: dict, grads: dict, state: dict, step: int, cfg):
@@ -258,11 +411,15 @@ def adamw_step(params: dict, grads: dict, state: dict, step: int, cfg):
 
 
 def train_lm(init: dict, batches: torch.Tensor, cfg, device, steps: int | None = None, timing: bool = False,
-             dtype=torch.float64, library_ops: bool = False, saved8: bool = False):
+             dtype=torch.float64, library_ops: bool = False, saved8: bool = False, fused_norms: bool = False,
+             head8: bool = False, max_norm: float | None = None):
     """Losses of `steps` AdamW steps from `init` on `batches` (token ids), with
     everything outside the BitLinear calls in ``dtype``; with ``timing``, also
     the mean device time per step in ms (CUDA events, first step excluded).
-    library_ops, saved8: as lm_loss (with dtype fp32)."""
+    library_ops, saved8, fused_norms, head8: as lm_loss (with dtype fp32). max_norm
+    (dtype fp32): the gradients' norm over all parameters is cut to it before AdamW."""
+    if max_norm is not None and dtype != torch.float32:
+        raise ValueError(f"max_norm takes fp32 gradients, got {dtype}")
     params = {n: t.to(device=device, dtype=dtype).contiguous().requires_grad_(True) for n, t in init.items()}
     ids_all = batches.to(device)
     state: dict = {}
@@ -271,8 +428,10 @@ def train_lm(init: dict, batches: torch.Tensor, cfg, device, steps: int | None =
         if timing:
             s, e = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
             s.record()
-        loss = lm_loss(params, ids_all[t], cfg, library_ops, saved8)
+        loss = lm_loss(params, ids_all[t], cfg, library_ops, saved8, fused_norms, head8)
         grads = torch.autograd.grad(loss, list(params.values()))
+        if max_norm is not None:
+            grads, _ = clip_gradients(grads, max_norm)
         adamw_step(params, dict(zip(params.keys(), grads)), state, t + 1, cfg)
         if timing:
             e.record()
