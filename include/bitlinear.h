@@ -630,7 +630,7 @@ typedef struct bl_tensor {
  * each dense and aligned to its element (views into a packed buffer). host_out:
  * for each the memory for its clipped values, of the same type, or NULL for
  * clipping in place; an output is its own gradient's memory or shares memory
- * with nothing else. norm: one float (device).
+ * with nothing else. norm: one float (device), in none of them.
  * Squares are added in fp32 over up to 32 values, in fp64 beyond (wholly in fp64
  * where fp32 would overflow or vanish), always in the same order; norm is
  * rounded once, to infinity beyond fp32, with the factor still right. A norm that

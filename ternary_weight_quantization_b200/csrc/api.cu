@@ -128,6 +128,13 @@ bl_status clip(const bl_tensor* host_grads, void* const* host_out, int64_t count
   std::unique_ptr<Span[]> spans(new (std::nothrow) Span[write ? count + 1 : 1]);
   if (!list || !spans) return fail(BL_ERR_INVALID_ARG, "no host memory for a list of %lld", (long long)count);
   if (bl_status s = tensor_list(host_grads, host_out, count, write, list.get(), spans.get())) return s;
+  for (int64_t i = 0; i < count; ++i) {
+    const uintptr_t n = reinterpret_cast<uintptr_t>(norm), bytes = static_cast<uintptr_t>(list[i].n) * (list[i].f32 ? 4 : 2);
+    for (const void* t : {list[i].in, static_cast<const void*>(list[i].out)}) {
+      const uintptr_t b = reinterpret_cast<uintptr_t>(t);
+      if (t && b < n + 4 && n < b + bytes) return fail(BL_ERR_INVALID_ARG, "norm lies in tensor %lld", (long long)i);
+    }
+  }
   const size_t need = bl::grad_norm_workspace_bytes(count);
   if (count > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
     return fail(BL_ERR_WORKSPACE, "workspace needs %zu bytes, 16-byte aligned", need);

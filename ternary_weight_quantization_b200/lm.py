@@ -381,6 +381,8 @@ def clip_gradients(grads, max_norm: float):
     all of them of max_norm at most, and that norm [1] before. A gradient that is
     not contiguous, or that shares memory with one before it (autograd may hand
     one tensor to two leaves), is replaced by a copy."""
+    if not grads:
+        raise ValueError("no gradients")
     out, seen = [], set()
     for g in grads:
         g = g.contiguous()

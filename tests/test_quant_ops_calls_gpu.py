@@ -230,6 +230,24 @@ def test_int8_linear_past_32_bit_offsets(M, N, K):
     assert not bool(y[0, :-300].any()) and not bool(y[-1, :-300].any())
 
 
+def test_int8_linear_gradient_over_many_channels():
+    """Above 131072 channels dX is a sum of fp32 partial sums even where it has
+    tiles enough without: sampled rows."""
+    M, N, K = 1200, 140000, 4096
+    wq, sw, dY = codes(N, K), scales(N, 1), rnd(M, N, seed=2, dtype=BF)
+    xq, sx = codes(M, K, seed=3), scales(M)
+    b = bl.Int8LinearBuffers.allocate(M, N, K)
+    b.workspace.fill_(255)
+    bl.bl_int8_linear_backward(dY, xq, sx, wq, sw, b.dX, None, workspace=b.workspace)
+    ok()
+    rows = torch.tensor([0, 255, 256, 700, M - 1], device="cuda")
+    w, d = (wq.float() * sw[:, None]).to(BF).double(), dY[rows].double()
+    close(b.dX[rows], d @ w, (131072 / 16 + 64) * 2 * U * (d.abs() @ w.abs()), "dX")
+    # the sums lose nothing to one side: the errors' mean is far below that bound
+    err = (b.dX[rows].double() - d @ w) / (d.abs() @ w.abs())
+    assert abs(float(err.mean())) <= 2.0 ** -12
+
+
 def test_clip_past_32_bit_offsets():
     n = (1 << 31) + 12345
     g = torch.zeros(n, dtype=BF, device="cuda")
@@ -404,6 +422,26 @@ def test_training_with_everything_runs_and_repeats():
     assert runs[0] == runs[1] and all(math.isfinite(x) for x in runs[0])
     # a zero head: every probability is 1 / V
     assert abs(runs[0][0] - math.log(LM_TINY.vocab)) <= 16 * 2.0 ** -23 * math.log(LM_TINY.vocab)
+
+
+def test_clip_of_many_tensors_in_a_graph():
+    """A list of more tensors than one launch takes, captured and replayed."""
+    grads = tensors([37] * 1500)
+    norm, ws = torch.zeros(1, device="cuda"), workspace(len(grads))
+    out = [torch.empty_like(g) for g in grads]
+    bl.bl_clip_grads(grads, 0.5, norm, ws, out=out)
+    ok()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        bl.bl_clip_grads(grads, 0.5, norm, ws, out=out)
+    for t in grads:
+        t.mul_(3)
+    g.replay()
+    ok()
+    want = norm64(grads)
+    assert abs(float(norm) - want) <= 7 * U * want
+    for t, o in zip(grads, out):
+        close(o, t.double() * 0.5 / want, 9 * U * t.double().abs() * 0.5 / want, "clipped")
 
 
 def test_clip_gradients_copies_what_is_not_dense_or_shared():

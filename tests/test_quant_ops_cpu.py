@@ -14,6 +14,7 @@ from tests.test_train_ops_cpu import _Fake
 
 F = ctypes.c_void_p(0x10000)        # never dereferenced: validation fails first
 G = ctypes.c_void_p(0x20000)
+NORM = ctypes.c_void_p(0x50000)
 MIS = ctypes.c_void_p(0x10008)
 BIG = 1 << 50
 INF, NAN = float("inf"), float("nan")
@@ -45,11 +46,11 @@ def _list(items):
 TWO = ((0x10000, 100, 0), (0x20000, 7, 1))
 
 
-def _gn(items=TWO, count=None, norm=F, ws=F, n=BIG):
+def _gn(items=TWO, count=None, norm=NORM, ws=F, n=BIG):
     return lambda L: L.bl_grad_norm(_list(items), len(items) if count is None else count, norm, ws, n, None)
 
 
-def _gc(items=TWO, out=None, most=1.0, norm=F, ws=F, n=BIG, count=None):
+def _gc(items=TWO, out=None, most=1.0, norm=NORM, ws=F, n=BIG, count=None):
     def call(L):
         to = None if out is None else (ctypes.c_void_p * len(out))(*out)
         return L.bl_clip_grads(_list(items), to, len(items) if count is None else count, most, norm, ws, n, None)
@@ -76,7 +77,8 @@ def _gc(items=TWO, out=None, most=1.0, norm=F, ws=F, n=BIG, count=None):
     (_gn(items=((None, 4, 0),)), 1), (_gn(items=((0x10001, 4, 0),)), 4), (_gn(items=((0x10002, 4, 1),)), 4),
     (_gn(ws=None), 8), (_gn(ws=MIS), 8), (_gn(n=16), 8), (_gn(norm=ctypes.c_void_p(0x10002)), 4),
     (_gn(items=((0x10000, (1 << 40) + 1, 0),)), 2), (_gn(items=((0x10000, 1 << 39, 0),) * 3), 2),
-    (lambda L: L.bl_grad_norm(None, 3, F, F, BIG, None), 1), (lambda L: L.bl_grad_norm(_list(TWO), (1 << 20) + 1, F, F, BIG, None), 2),
+    (lambda L: L.bl_grad_norm(None, 3, NORM, F, BIG, None), 1),
+    (lambda L: L.bl_grad_norm(_list(TWO), (1 << 20) + 1, NORM, F, BIG, None), 2),
     (_gc(most=NAN), 1), (_gc(most=-1.0), 1), (_gc(norm=None), 1), (_gc(ws=None), 8), (_gc(n=16), 8),
     (_gc(items=TWO + ((0x10000, 4, 0),)), 1),                       # one tensor twice, in place
     (_gc(items=((0x10000, 100, 0), (0x100C0, 100, 0))), 1),         # two that overlap
@@ -85,7 +87,8 @@ def _gc(items=TWO, out=None, most=1.0, norm=F, ws=F, n=BIG, count=None):
     (_gc(out=(0x30000, 0x10000 + 196)), 1),                         # an output in another's input
     (_gc(out=(0x10000 + 4, 0x40000)), 1),                           # an output in its own input, at another place
     (_gc(out=(0x20000, 0x10000)), 1),                               # outputs that change places
-    (_gc(out=(None, 0x40000)), 1), (_gc(out=(0x30001, 0x40000)), 4), (_gc(out=(0x30000, 0x40002)), 4),
+    (_gc(norm=ctypes.c_void_p(0x10000 + 196)), 1), (_gn(norm=ctypes.c_void_p(0x20000 + 24)), 1),   # norm in a tensor
+    (_gc(out=(0x30000, 0x40000), norm=ctypes.c_void_p(0x30000)), 1), (_gc(out=(None, 0x40000)), 1), (_gc(out=(0x30001, 0x40000)), 4), (_gc(out=(0x30000, 0x40002)), 4),
 ])
 def test_host_validation_without_gpu(call, expect):
     lib = b.load_library()
