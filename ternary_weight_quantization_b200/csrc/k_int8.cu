@@ -87,6 +87,24 @@ __device__ __forceinline__ uint32_t box_piece(uint32_t box, int row, int j) {
   return box + static_cast<uint32_t>(row) * (32 * kEsize) + (static_cast<uint32_t>(j ^ turn) << 4);
 }
 
+// Element e of row `row` of an output box, in the low bits.
+template <int kEsize>
+__device__ __forceinline__ uint32_t box_element(uint32_t box, int row, int e) {
+  constexpr int kV = 16 / kEsize;
+  const uint32_t at = box_piece<kEsize>(box, row, e / kV) + (e & (kV - 1)) * kEsize;
+  uint32_t w;
+  if constexpr (kEsize == 4) {
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at));
+  } else {
+    uint16_t h;
+    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(h) : "r"(at));
+    w = h;
+  }
+  return w;
+}
+__device__ __forceinline__ void store_element(float* p, uint32_t w) { *reinterpret_cast<uint32_t*>(p) = w; }
+__device__ __forceinline__ void store_element(__nv_bfloat16* p, uint32_t w) { *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w); }
+
 // TY: type of y. kTma: y's rows start on 16-byte boundaries, so a box leaves by
 // one TMA store; else the warp writes it row by row.
 template <typename TY, int BN, bool kTma>
@@ -314,20 +332,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
           }
         } else {
           __syncwarp();
-          const int rows = col + lane < p.N ? p.M - row0 : 0;
-          const uint32_t in = (lane * kEsize) & 15;
+          const int rows = p.M - row0;
           TY* to = static_cast<TY*>(p.y) + static_cast<int64_t>(row0) * p.N + col + lane;
 #pragma unroll 16
           for (int i = 0; i < 32; ++i, to += p.N) {
-            if constexpr (kEsize == 4) {
-              uint32_t w;
-              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(box_piece<4>(box, i, lane / 4) + in));
-              if (i < rows) *reinterpret_cast<uint32_t*>(to) = w;
-            } else {
-              uint16_t w;
-              asm volatile("ld.shared.b16 %0, [%1];" : "=h"(w) : "r"(box_piece<2>(box, i, lane / 8) + in));
-              if (i < rows) *reinterpret_cast<uint16_t*>(to) = w;
-            }
+            const uint32_t w = box_element<kEsize>(box, i, lane);
+            if (i < rows && col + lane < p.N) store_element(to, w);
           }
         }
         tmem_ld_wait();
@@ -360,7 +370,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
 // warp takes one group of 16 channels and every S-th stage, mma.sync.m16n8k32 on
 // operands that ldmatrix brings in the instruction's order; the S warps' INT32
 // sums are added in shared memory (exact in any order).
-constexpr int64_t kFewMost = 16;   // most tokens
+constexpr int64_t kFewMost = 16;   // most tokens, with weights of any size
+constexpr int64_t kFewWeights = int64_t(1) << 22;  // most weights with up to 32
 constexpr int kFewSmem = 114688;   // of a CTA: half an SM's
 
 struct FewParams {
@@ -537,7 +548,7 @@ __global__ void __launch_bounds__(Few<kTok, R>::kThreads, 2)
 }
 
 // ---------------------------------------------------------------- tens of tokens
-// D = W x^T: 128 channels of one CTA by all tokens (32 or 64 columns),
+// D = W x^T: 128 channels of one CTA by 32 or 64 tokens,
 // tcgen05.mma kind::i8 (cta_group::1). There are few such tiles, so the CTAs of a
 // cluster share one: each sums its part of K, leaves its INT32 sums in its shared
 // memory, and turns its share of the tokens into y from all CTAs' sums. A thread
@@ -546,11 +557,12 @@ __global__ void __launch_bounds__(Few<kTok, R>::kThreads, 2)
 // Roles (192 threads): warp 0 loads, warp 1 issues the MMAs, warps 2..5 are the
 // epilogue. Waits are bounded as in the tiles' kernel; every thread reaches the
 // cluster's barriers whatever happened before.
-constexpr int64_t kMidMost = 64;  // most tokens
+constexpr int64_t kMidMost = 64;  // most tokens of a tile
 constexpr int kMidThreads = 192;
 
 struct MidParams {
-  int M, N, K, share;  // CTAs per tile
+  int M, N, K;
+  int tiles_n, share;  // tiles over the channels; CTAs per tile
   const float* sx;
   const float* sw;
   void* y;
@@ -587,7 +599,8 @@ __global__ void __launch_bounds__(kMidThreads)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank()), share = p.share;
-  const int n0 = static_cast<int>(blockIdx.x) / share * 128;
+  const int tile = static_cast<int>(blockIdx.x) / share;
+  const int n0 = tile % p.tiles_n * 128, t0 = tile / p.tiles_n * NT, M = p.M - t0 < NT ? p.M - t0 : NT;  // tokens t0 .. t0 + M - 1
   const int boxes = (p.K + kBlockK - 1) / kBlockK;
   const int kb0 = boxes * rank / share, nkb = boxes * (rank + 1) / share - kb0;
   if (threadIdx.x == 0) {
@@ -620,7 +633,7 @@ __global__ void __launch_bounds__(kMidThreads)
         mbar_arrive_expect_tx(&full[s], G::kStageBytes);
         uint8_t* at = smem + s * G::kStageBytes;
         tma_load_2d(&map_w, &full[s], at, (kb0 + kb) * kBlockK, n0);
-        tma_load_2d(&map_x, &full[s], at + G::kW, (kb0 + kb) * kBlockK, 0);
+        tma_load_2d(&map_x, &full[s], at + G::kW, (kb0 + kb) * kBlockK, t0);
       }
       if (kb < nkb || *abort_flag) {
         const unsigned long long deadline = globaltimer_ns() + kWaitLimitNs;
@@ -649,12 +662,12 @@ __global__ void __launch_bounds__(kMidThreads)
   const int q = warp & 3, row = q * 32 + lane, n = n0 + row;
   const float4* sx = reinterpret_cast<const float4*>(smem + G::kOffSx);
   if (warp >= 2) {
-    if (row < NT) reinterpret_cast<float*>(smem + G::kOffSx)[row] = row < p.M ? __ldg(p.sx + row) : 0.0f;
+    if (row < NT) reinterpret_cast<float*>(smem + G::kOffSx)[row] = row < M ? __ldg(p.sx + t0 + row) : 0.0f;
     asm volatile("bar.sync 1, 128;" ::: "memory");
   }
   const float sw = warp >= 2 && n < p.N ? __ldg(p.sw + n) : 0.0f;
   bool ok = true;
-  TY* y = static_cast<TY*>(p.y) + n;
+  TY* y = static_cast<TY*>(p.y) + static_cast<int64_t>(t0) * p.N + n;
   if (warp >= 2) {
     ok = mbar_wait(done, 0, abort_flag, p.err);
     tc_fence_after();
@@ -666,7 +679,7 @@ __global__ void __launch_bounds__(kMidThreads)
   if (warp >= 2 && ok) {
     const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll 1
-    for (int c = 0; c < NT && c < p.M; c += 32) {
+    for (int c = 0; c < M; c += 32) {
       uint32_t r[32];
       tmem_ld_32x32b_x32(base + c, r);
       tmem_ld_wait();
@@ -681,7 +694,7 @@ __global__ void __launch_bounds__(kMidThreads)
           const float s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (c + j + i < p.M)
+            if (c + j + i < M)
               store1(y + static_cast<int64_t>(c + j + i) * p.N, __int2float_rn(static_cast<int>(r[j + i])) * __fmul_rn(s[i], sw));
         }
       }
@@ -690,7 +703,7 @@ __global__ void __launch_bounds__(kMidThreads)
   if (share > 1) {
     cluster_sync_all();
     if (warp >= 2 && ok && n < p.N) {
-      const int m0 = p.M * rank / share, m1 = p.M * (rank + 1) / share;
+      const int m0 = M * rank / share, m1 = M * (rank + 1) / share;
       constexpr int kU = 16;  // tokens in flight per thread
       const uint32_t at = smem_u32(sums + row);
       for (int m = m0; m < m1; m += kU) {
@@ -825,21 +838,28 @@ cudaError_t forward_tiles(const int8_t* xq, const int8_t* wq, TileParams p, cuda
   return tma ? launch_tiles<TY, BN, true>(maps, p, s) : launch_tiles<TY, BN, false>(maps, p, s);
 }
 
-template <typename TY>
-cudaError_t forward_tiles(const int8_t* xq, const int8_t* wq, TileParams p, cudaStream_t s) {
-  p.tiles_m = (p.M + kRows - 1) / kRows;
-  // The tiles' width: the least time of the busiest pair, its tiles times a
-  // stage's MMAs (measured: 122 cycles for 128 columns, 168 for 256, so 76 + 0.36 a
-  // column) and the end of one tile.
-  const int pairs = device_sm_count() / 2, nkb = (p.K + kBlockK - 1) / kBlockK;
-  int best = 256;
-  int64_t least = INT64_MAX;
+// The tiles' width: the least time of the busiest pair, its tiles times a stage's
+// MMAs (measured: 122 cycles for 32 of K with 128 columns, 168 with 256, so 76 +
+// 0.36 a column) and the end of one tile.
+struct TilePlan {
+  int columns;
+  int64_t cycles;
+};
+TilePlan tile_plan(int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles_m = (M + kRows - 1) / kRows, pairs = device_sm_count() / 2, nkb = (K + kBlockK - 1) / kBlockK;
+  TilePlan best{256, INT64_MAX};
   for (int bn = 256; bn >= 64; bn -= 32) {
-    const int64_t rounds = (static_cast<int64_t>(p.tiles_m) * ((p.N + bn - 1) / bn) + pairs - 1) / pairs;
-    const int64_t cost = rounds * nkb * (4 * (7600 + 36 * bn)) + 1000 * bn;
-    if (cost < least) best = bn, least = cost;
+    const int64_t rounds = (tiles_m * ((N + bn - 1) / bn) + pairs - 1) / pairs;
+    const int64_t cycles = (rounds * nkb * 4 * (7600 + 36 * bn) + 1000 * bn) / 100;
+    if (cycles < best.cycles) best = {bn, cycles};
   }
-  switch (best) {
+  return best;
+}
+
+template <typename TY>
+cudaError_t forward_tiles(const int8_t* xq, const int8_t* wq, TileParams p, int columns, cudaStream_t s) {
+  p.tiles_m = (p.M + kRows - 1) / kRows;
+  switch (columns) {
     case 64: return forward_tiles<TY, 64>(xq, wq, p, s);
     case 96: return forward_tiles<TY, 96>(xq, wq, p, s);
     case 128: return forward_tiles<TY, 128>(xq, wq, p, s);
@@ -893,6 +913,24 @@ cudaError_t forward_few(const int8_t* xq, const int8_t* wq, const FewParams& p, 
   return p.M <= 16 ? forward_few<TY, 2>(xq, wq, p, s) : forward_few<TY, 4>(xq, wq, p, s);
 }
 
+// CTAs per tile, a power of two that leaves each an SM, and the nanoseconds that
+// follow from it: 280 per stage of a CTA, 1600 for a join, 2500 for one of 8 (40 x
+// 145 x 400, 4 stages: 4.6 us alone and 5.7 over 2 CTAs; 40 x 512 x 1408, 11 stages:
+// 6.8 us over 2, 5.9 over 4, 6.5 over 8).
+struct MidPlan {
+  int share;
+  int64_t ns;
+};
+MidPlan mid_plan(int64_t tiles, int64_t K) {
+  const int64_t boxes = (K + kBlockK - 1) / kBlockK;
+  MidPlan best{1, boxes * 280};
+  for (int share = 2; share <= 8 && tiles * share <= device_sm_count() && share <= boxes; share *= 2) {
+    const int64_t ns = (boxes + share - 1) / share * 280 + (share < 8 ? 1600 : 2500);
+    if (ns < best.ns) best = {share, ns};
+  }
+  return best;
+}
+
 template <typename TY, int NT>
 cudaError_t launch_mid(const int8_t* xq, const int8_t* wq, MidParams p, cudaStream_t s) {
   using G = Mid<NT>;
@@ -903,10 +941,8 @@ cudaError_t launch_mid(const int8_t* xq, const int8_t* wq, MidParams p, cudaStre
   if (!make_map(&x, xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, p.M, p.K, kBlockK, NT) ||
       !make_map(&w, wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, p.N, p.K, kBlockK, 128))
     return cudaErrorInvalidValue;
-  // as many CTAs per tile as leave each an SM and two stages
-  const int tiles = (p.N + 127) / 128, boxes = (p.K + kBlockK - 1) / kBlockK, sms = device_sm_count();
-  p.share = 1;
-  while (p.share < 8 && tiles * p.share * 2 <= sms && boxes >= p.share * 4) p.share *= 2;
+  p.tiles_n = (p.N + 127) / 128;
+  const int tiles = p.tiles_n * ((p.M + NT - 1) / NT);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(tiles * p.share);
   cfg.blockDim = dim3(kMidThreads);
@@ -925,8 +961,7 @@ cudaError_t launch_mid(const int8_t* xq, const int8_t* wq, MidParams p, cudaStre
 
 template <typename TY>
 cudaError_t forward_mid(const int8_t* xq, const int8_t* wq, const MidParams& p, cudaStream_t s) {
-  if (p.M <= 32) return launch_mid<TY, 32>(xq, wq, p, s);
-  return launch_mid<TY, 64>(xq, wq, p, s);
+  return p.M <= 32 ? launch_mid<TY, 32>(xq, wq, p, s) : launch_mid<TY, 64>(xq, wq, p, s);
 }
 
 size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -935,12 +970,21 @@ size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
 cudaError_t launch_int8_forward(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw, int64_t M,
                                 int64_t N, int64_t K, void* y, int y_f32, int* err, cudaStream_t s) {
-  if (M <= kFewMost) {
+  // Up to 16 tokens stream the weights through mma.sync, up to 32 where the weights
+  // are small: its MMAs are a few times slower than tcgen05's, its start 2 us shorter.
+  if (M <= kFewMost || (M <= 32 && N * K <= kFewWeights)) {
     const FewParams p{static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), 0, sx, sw, y, err};
     return y_f32 ? forward_few<float>(xq, wq, p, s) : forward_few<__nv_bfloat16>(xq, wq, p, s);
   }
-  if (M <= kMidMost) {
-    const MidParams p{static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), 1, sx, sw, y, err};
+  const TilePlan wide = tile_plan(M, N, K);
+  // More tokens than one narrow tile has take the wide tiles, but where those are few
+  // and K is long, so that splitting K over narrow ones is worth its join (at 1.9
+  // cycles a nanosecond; 65 x 120 x 5824: 8.3 us for 15.8 in wide tiles, 412 x 332 x
+  // 3200 7.9 for 10.2).
+  const int64_t columns = M <= 32 ? 32 : kMidMost, tiles = (N + 127) / 128 * ((M + columns - 1) / columns);
+  const MidPlan narrow = mid_plan(tiles, K);
+  if (M <= kMidMost || (tiles * narrow.share <= device_sm_count() && narrow.ns + 400 < wide.cycles * 10 / 19)) {
+    const MidParams p{static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), 0, narrow.share, sx, sw, y, err};
     return y_f32 ? forward_mid<float>(xq, wq, p, s) : forward_mid<__nv_bfloat16>(xq, wq, p, s);
   }
   TileParams p{};
@@ -951,7 +995,7 @@ cudaError_t launch_int8_forward(const int8_t* xq, const float* sx, const int8_t*
   p.sw = sw;
   p.y = y;
   p.err = err;
-  return y_f32 ? forward_tiles<float>(xq, wq, p, s) : forward_tiles<__nv_bfloat16>(xq, wq, p, s);
+  return y_f32 ? forward_tiles<float>(xq, wq, p, wide.columns, s) : forward_tiles<__nv_bfloat16>(xq, wq, p, wide.columns, s);
 }
 
 // The values of x and of w in bf16, the factor 1, dX's partial sums.
