@@ -16,6 +16,12 @@
 // other's loads, 8.7 us for 6.9 over 9 MB in 28 tensors), and the second launch
 // walks its runs backwards, from what the first read last and L2 still holds.
 //
+// Measured on B200 (in a graph, gradients from HBM): 1279 MB of bf16 in 57 tensors:
+// norm 215 us (0.91 of the copy rate), clipped copies 655 (0.9 of what the two
+// launches move, 0.6 of reading once and writing once: a second reading is the price
+// of a norm that has to be known first); 85 MB of fp32 in 39: 17.4 and 40.4; 9 MB in
+// 30: 5.7 and 9.4 (two launches of 1.5 to 2 us, one HBM latency each).
+//
 // Sums: the squares of up to 32 values are added in fp32, such sums in fp64. A
 // sum that leaves fp32's range (values around 1e19 and beyond, or so small that
 // their squares vanish) is formed again in fp64, so the norm of any finite

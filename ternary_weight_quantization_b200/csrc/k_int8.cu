@@ -13,6 +13,18 @@
 //                     is split over a cluster
 //   int8_values_kernel  rn_bf16(code * scale) of both operands, for the gradients'
 //                     products (k_xent.cu)
+//
+// Measured on B200 (a call among others in a graph, inputs from HBM; the floor is
+// the bytes at the copy rate or the operations at twice the bf16 rate):
+//   tokens x channels x K    kernel   us      floor   bound by
+//   1 x 6912 x 2560          few      6.0     2.7     the start (2.2) and one HBM latency
+//   16 x 32000 x 2560, fp32  few      16.9    12.8    HBM (5.0 TB/s)
+//   64 x 32000 x 2560        mid      17.7    13.2    HBM
+//   64 x 6912 x 2560         mid      10.4    2.9     108 CTAs with 10 stages each, and their join
+//   333 x 5001 x 1040        tiles    8.5     1.4     one tile per pair: set-up, 9 stages, its end
+//   2048 x 8192 x 512        tiles    12.7    5.9     the epilogue
+//   4096 x 6912 x 2560       tiles    49.5    44.4    tensor cores (ncu: 76 % of the cycles; 5.84 rounds as 6)
+//   4096 x 32000 x 2560      tiles    217     205     tensor cores
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -734,45 +746,47 @@ __global__ void __launch_bounds__(kMidThreads)
 }
 
 // ---------------------------------------------------------------- values for the gradients
+// The two operands' chunks of 8 codes are one range, cut evenly.
 struct ValuesParams {
-  const uint2* q[2];      // codes of the two operands (null: not wanted)
+  const uint2* q[2];
   const float* scale[2];
   uint4* out[2];
-  int64_t chunks[2];      // of 8 codes
+  int64_t first, chunks;  // of the first operand, and of both (either may have none)
   int per_row;
   float* one;
 };
 
+constexpr int kValuesU = 4;  // chunks in flight per thread
+
 __global__ void __launch_bounds__(256) int8_values_kernel(const ValuesParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
-  constexpr int kU = 4;
   const int64_t T = static_cast<int64_t>(gridDim.x) * 256, t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (t == 0) *p.one = 1.0f;
+  const bool narrow = p.chunks <= 0xFFFFFFFFll;  // the row by a 32-bit division
+  for (int64_t i0 = t; i0 < p.chunks; i0 += kValuesU * T) {
+    uint2 c[kValuesU];
+    float s[kValuesU];
 #pragma unroll
-  for (int o = 0; o < 2; ++o) {
-    const int64_t n = p.chunks[o];
-    const bool narrow = n <= 0xFFFFFFFFll;  // the row by a 32-bit division
-    for (int64_t i0 = t; i0 < n; i0 += kU * T) {
-      uint2 c[kU];
-      float s[kU];
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int64_t i = i0 + u * T;
-        if (i < n) {
-          c[u] = __ldg(p.q[o] + i);
-          s[u] = __ldg(p.scale[o] + (narrow ? static_cast<int64_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(p.per_row))
-                                            : i / p.per_row));
-        }
+    for (int u = 0; u < kValuesU; ++u) {
+      const int64_t at = i0 + u * T;
+      if (at < p.chunks) {
+        const bool second = at >= p.first;
+        const int64_t i = second ? at - p.first : at;
+        c[u] = __ldg((second ? p.q[1] : p.q[0]) + i);
+        s[u] = __ldg((second ? p.scale[1] : p.scale[0]) +
+                     (narrow ? static_cast<int64_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(p.per_row)) : i / p.per_row));
       }
+    }
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int64_t i = i0 + u * T;
-        if (i < n) {
-          f32x2 v[4];
-          act8_values8(c[u], s[u], v);
-          p.out[o][i] = make_uint4(pack_bf16x2(v[0]), pack_bf16x2(v[1]), pack_bf16x2(v[2]), pack_bf16x2(v[3]));
-        }
+    for (int u = 0; u < kValuesU; ++u) {
+      const int64_t at = i0 + u * T;
+      if (at < p.chunks) {
+        f32x2 v[4];
+        act8_values8(c[u], s[u], v);
+        const bool second = at >= p.first;
+        (second ? p.out[1] : p.out[0])[second ? at - p.first : at] =
+            make_uint4(pack_bf16x2(v[0]), pack_bf16x2(v[1]), pack_bf16x2(v[2]), pack_bf16x2(v[3]));
       }
     }
   }
@@ -1022,13 +1036,14 @@ cudaError_t launch_int8_backward(const void* dY, const int8_t* xq, const float* 
   v.scale[1] = sw;
   v.out[0] = reinterpret_cast<uint4*>(x);
   v.out[1] = reinterpret_cast<uint4*>(w);
-  v.chunks[0] = dW ? M * K / 8 : 0;
-  v.chunks[1] = dX ? N * K / 8 : 0;
+  v.first = dW ? M * K / 8 : 0;
+  v.chunks = v.first + (dX ? N * K / 8 : 0);
   v.per_row = static_cast<int>(K / 8);
   v.one = one;
-  const int64_t most = v.chunks[0] > v.chunks[1] ? v.chunks[0] : v.chunks[1];
-  const int64_t want = (most + 1023) / 1024, cap = static_cast<int64_t>(8) * device_sm_count();
-  if (cudaError_t e = launch_pdl(int8_values_kernel, dim3(static_cast<unsigned>(want < cap ? want : cap)), dim3(256), 0, s, v);
+  // as many rounds as fill the SMs, and a grid that fills the rounds
+  const int64_t most = static_cast<int64_t>(8) * device_sm_count(), per = 256 * kValuesU;
+  const int64_t rounds = (v.chunks + most * per - 1) / (most * per), grid = (v.chunks + rounds * per - 1) / (rounds * per);
+  if (cudaError_t e = launch_pdl(int8_values_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, v);
       e != cudaSuccess)
     return e;
   return launch_linear_grads(dY, x, w, M, N, K, dX, dW, dw_is_f32, accumulate, one,

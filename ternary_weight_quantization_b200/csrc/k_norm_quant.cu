@@ -24,6 +24,13 @@
 // for narrow rows, a warp) per row. Backward: one block per SM, columns' sums of
 // dweight in registers over all of its rows, joined per block and then by a
 // second launch in a fixed order.
+//
+// Measured on B200 (in a graph, inputs from HBM), with the share of the copy rate:
+// bf16, 4096 x 2560: forward 13.8 us (0.81), backward 18.9 (0.68, of which some 6 are
+// its start, the blocks' joins and the second launch); 16384 x 2560: 53.0 (0.85) and
+// 53.3 (0.96). bf16 onto an fp32 stream, 4096 x 2560: 21.1 (0.83) and 31.3 (0.82). One
+// token: 2.0 and 5.3 (launches). The forward issues 0.53 instructions a cycle and
+// scheduler (ncu): next to HBM that is what it is short of.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
