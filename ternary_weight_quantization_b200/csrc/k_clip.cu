@@ -189,7 +189,7 @@ struct Run {
 template <int kCap>
 __global__ void __launch_bounds__(kThreads, 2) grad_sum_kernel(const __grid_constant__ Table<kCap> t, double* parts) {
   __shared__ double buf[kWarps];
-  Run x;
+  Run x{};
   x.begin<false>(t);
   pdl_wait_primary();
   pdl_launch_dependents();
@@ -278,7 +278,7 @@ template <int kCap>
 __global__ void __launch_bounds__(kThreads, 2) grad_scale_kernel(const __grid_constant__ Table<kCap> t, const double* parts,
                                                                  int nparts, double most, int in_place, float* norm) {
   __shared__ double buf[kWarps];
-  Run x;
+  Run x{};
   x.begin<true>(t);
   pdl_wait_primary();
   pdl_launch_dependents();
