@@ -712,6 +712,13 @@ __global__ void __launch_bounds__(kMidThreads)
       }
     }
   }
+  // freed in front of the cluster's barriers: a CTA that holds TMEM waits for no other
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_one(tmem, NT);
+  }
   if (share > 1) {
     cluster_sync_all();
     if (warp >= 2 && ok && n < p.N) {
@@ -735,13 +742,6 @@ __global__ void __launch_bounds__(kMidThreads)
       }
     }
     cluster_sync_all();  // a CTA's sums stay until all have read them
-  } else {
-    tc_fence_before();
-    __syncthreads();
-  }
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc_one(tmem, NT);
   }
 }
 
