@@ -20,7 +20,8 @@
 //   1 x 6912 x 2560          few      6.0     2.7     the start (2.2) and one HBM latency
 //   16 x 32000 x 2560, fp32  few      16.9    12.8    HBM (5.0 TB/s)
 //   64 x 32000 x 2560        mid      17.7    13.2    HBM
-//   64 x 6912 x 2560         mid      10.4    2.9     108 CTAs with 10 stages each, and their join
+//   64 x 6912 x 2560         mid      9.2     2.9     108 CTAs with 10 stages each (280 ns a stage), and their join
+//   64 x 2560 x 6912         mid      9.1     2.8     120 CTAs (6 per tile), 9 stages each
 //   333 x 5001 x 1040        tiles    8.5     1.4     one tile per pair: set-up, 9 stages, its end
 //   2048 x 8192 x 512        tiles    12.7    5.9     the epilogue
 //   4096 x 6912 x 2560       tiles    49.5    44.4    tensor cores (ncu: 76 % of the cycles; 5.84 rounds as 6)
@@ -31,6 +32,7 @@
 #include <cudaTypedefs.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "bl_act8.cuh"
 #include "bl_device.cuh"
@@ -563,14 +565,19 @@ __global__ void __launch_bounds__(Few<kTok, R>::kThreads, 2)
 // D = W x^T: 128 channels of one CTA by 32 or 64 tokens,
 // tcgen05.mma kind::i8 (cta_group::1). There are few such tiles, so the CTAs of a
 // cluster share one: each sums its part of K, leaves its INT32 sums in its shared
-// memory, and turns its share of the tokens into y from all CTAs' sums. A thread
-// has a channel, so a warp writes 32 channels of a token at once, whatever N.
+// memory, and turns its share of the tokens into y from all CTAs' sums. A warp reads
+// 128 channels of a token at once from each CTA, 16 bytes a lane, and everything it
+// needs before it adds (4 bytes a lane and one CTA after another: 1 us more over 2 or
+// 4 CTAs, 2 over 8; 16 bytes a lane of one channel's tokens, so with the lanes apart:
+// the same 1 to 2). A tile that is not shared goes from TMEM to y, a thread for each
+// channel, so a warp writes 32 channels of a token at once, whatever N.
 //
 // Roles (192 threads): warp 0 loads, warp 1 issues the MMAs, warps 2..5 are the
 // epilogue. Waits are bounded as in the tiles' kernel; every thread reaches the
 // cluster's barriers whatever happened before.
 constexpr int64_t kMidMost = 64;  // most tokens of a tile
 constexpr int kMidThreads = 192;
+constexpr int kMidShare = 8;  // most CTAs of a cluster
 
 struct MidParams {
   int M, N, K;
@@ -591,10 +598,20 @@ struct Mid {
   static_assert(kSmemBytes <= 232448 && NT * 512 <= kOffBar, "the sums fit in the ring");
 };
 
-__device__ __forceinline__ int ld_cluster(uint32_t addr) {
-  int v;
-  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ int4 ld_cluster_v4(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
+}
+
+__device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(pair2(v[0], v[1])), pack_bf16x2(pair2(v[2], v[3])));
 }
 
 template <typename TY, int NT>
@@ -672,14 +689,14 @@ __global__ void __launch_bounds__(kMidThreads)
   }
   __syncwarp();
   const int q = warp & 3, row = q * 32 + lane, n = n0 + row;
-  const float4* sx = reinterpret_cast<const float4*>(smem + G::kOffSx);
+  float* sx = reinterpret_cast<float*>(smem + G::kOffSx);
   if (warp >= 2) {
-    if (row < NT) reinterpret_cast<float*>(smem + G::kOffSx)[row] = row < M ? __ldg(p.sx + t0 + row) : 0.0f;
+    if (row < NT) sx[row] = row < M ? __ldg(p.sx + t0 + row) : 0.0f;
     asm volatile("bar.sync 1, 128;" ::: "memory");
   }
   const float sw = warp >= 2 && n < p.N ? __ldg(p.sw + n) : 0.0f;
   bool ok = true;
-  TY* y = static_cast<TY*>(p.y) + static_cast<int64_t>(t0) * p.N + n;
+  TY* y = static_cast<TY*>(p.y) + static_cast<int64_t>(t0) * p.N;
   if (warp >= 2) {
     ok = mbar_wait(done, 0, abort_flag, p.err);
     tc_fence_after();
@@ -702,12 +719,12 @@ __global__ void __launch_bounds__(kMidThreads)
       } else if (n < p.N) {
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
-          const float4 s4 = sx[(c + j) / 4];
+          const float4 s4 = *reinterpret_cast<const float4*>(sx + c + j);
           const float s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (c + j + i < M)
-              store1(y + static_cast<int64_t>(c + j + i) * p.N, __int2float_rn(static_cast<int>(r[j + i])) * __fmul_rn(s[i], sw));
+              store1(y + static_cast<int64_t>(c + j + i) * p.N + n, __int2float_rn(static_cast<int>(r[j + i])) * __fmul_rn(s[i], sw));
         }
       }
     }
@@ -721,24 +738,48 @@ __global__ void __launch_bounds__(kMidThreads)
   }
   if (share > 1) {
     cluster_sync_all();
-    if (warp >= 2 && ok && n < p.N) {
-      const int m0 = M * rank / share, m1 = M * (rank + 1) / share;
-      constexpr int kU = 16;  // tokens in flight per thread
-      const uint32_t at = smem_u32(sums + row);
-      for (int m = m0; m < m1; m += kU) {
-        int v[kU] = {};
-        for (int k = 0; k < share; ++k) {
-          const uint32_t from = map_to_rank(at + m * 512, k);
-          int t[kU];
+    if (warp >= 2 && ok) {
+      // a warp takes every fourth token of the CTA's share, a lane 4 of the channels;
+      // all CTAs' sums of them are requested at once
+      const int m0 = M * rank / share + q, m1 = M * (rank + 1) / share, c0 = n0 + 4 * lane;
+      const uint32_t at = smem_u32(sums + m0 * 128 + 4 * lane);
+      float w[4];
 #pragma unroll
-          for (int i = 0; i < kU; ++i) t[i] = m + i < m1 ? ld_cluster(from + i * 512) : 0;
+      for (int h = 0; h < 4; ++h) w[h] = c0 + h < p.N ? __ldg(p.sw + c0 + h) : 0.0f;
+      auto join = [&](auto ctas) {
+        constexpr int kShare = decltype(ctas)::value, kU = (NT + 4 * kShare - 1) / (4 * kShare);
+        int4 t[kU][kShare];
 #pragma unroll
-          for (int i = 0; i < kU; ++i) v[i] += t[i];
+        for (int i = 0; i < kU; ++i) {
+          if (m0 + 4 * i >= m1) break;
+#pragma unroll
+          for (int k = 0; k < kShare; ++k) t[i][k] = ld_cluster_v4(map_to_rank(at, k) + i * 2048);
         }
 #pragma unroll
-        for (int i = 0; i < kU; ++i)
-          if (m + i < m1)
-            store1(y + static_cast<int64_t>(m + i) * p.N, __int2float_rn(v[i]) * __fmul_rn(reinterpret_cast<const float*>(sx)[m + i], sw));
+        for (int i = 0; i < kU; ++i) {
+          const int m = m0 + 4 * i;
+          if (m >= m1) break;
+          int4 v = t[i][0];
+#pragma unroll
+          for (int k = 1; k < kShare; ++k) v.x += t[i][k].x, v.y += t[i][k].y, v.z += t[i][k].z, v.w += t[i][k].w;
+          const float s = sx[m];
+          const float o[4] = {__int2float_rn(v.x) * __fmul_rn(s, w[0]), __int2float_rn(v.y) * __fmul_rn(s, w[1]),
+                              __int2float_rn(v.z) * __fmul_rn(s, w[2]), __int2float_rn(v.w) * __fmul_rn(s, w[3])};
+          TY* to = y + static_cast<int64_t>(m) * p.N + c0;
+          if ((p.N & 3) == 0) {
+            if (c0 < p.N) store4(to, o);
+          } else {
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+              if (c0 + h < p.N) store1(to + h, o[h]);
+          }
+        }
+      };
+      switch (share) {
+        case 2: join(std::integral_constant<int, 2>{}); break;
+        case 4: join(std::integral_constant<int, 4>{}); break;
+        case 6: join(std::integral_constant<int, 6>{}); break;
+        default: join(std::integral_constant<int, 8>{});
       }
     }
     cluster_sync_all();  // a CTA's sums stay until all have read them
@@ -927,19 +968,51 @@ cudaError_t forward_few(const int8_t* xq, const int8_t* wq, const FewParams& p, 
   return p.M <= 16 ? forward_few<TY, 2>(xq, wq, p, s) : forward_few<TY, 4>(xq, wq, p, s);
 }
 
-// CTAs per tile, a power of two that leaves each an SM, and the nanoseconds that
-// follow from it: 280 per stage of a CTA, 1600 for a join, 2500 for one of 8 (40 x
-// 145 x 400, 4 stages: 4.6 us alone and 5.7 over 2 CTAs; 40 x 512 x 1408, 11 stages:
-// 6.8 us over 2, 5.9 over 4, 6.5 over 8).
+// Clusters of `share` CTAs that fit at once with an SM for each CTA (a cluster lies
+// within one GPC: 15 of 8, 33 of 4).
+int clusters_at_once(int share) {
+  static int known[64][kMidShare + 1] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const bool keep = dev >= 0 && dev < 64;
+  if (keep && known[dev][share]) return known[dev][share];
+  constexpr int kOne = 128 * 1024;  // shared memory of which an SM holds one CTA's
+  static bool done[64] = {};
+  auto kernel = int8_mid_kernel<__nv_bfloat16, 64>;
+  int clusters = 0;
+  if (allow_smem(kernel, kOne, done) == cudaSuccess) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(share * device_sm_count()));
+    cfg.blockDim = dim3(kMidThreads);
+    cfg.dynamicSmemBytes = kOne;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = share;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess) clusters = 0;
+  }
+  cudaGetLastError();
+  if (clusters <= 0) clusters = device_sm_count() / share;
+  if (keep) known[dev][share] = clusters;
+  return clusters;
+}
+
+// CTAs per tile (1 or even: 3, 5 and 7 measured 0.25 us more than their stages say), and
+// the nanoseconds that follow from it: 280 per stage of a CTA, 550 + 75 per CTA for a
+// join, 1300 where the clusters do not fit one CTA to an SM (64 tokens, 17 tiles, 32
+// stages: 13.5 us alone, 9.8 over 2 CTAs, 7.9 over 4, 7.5 over 6, 8.5 over 8; 15 tiles:
+// 7.3 over 8).
 struct MidPlan {
   int share;
   int64_t ns;
 };
 MidPlan mid_plan(int64_t tiles, int64_t K) {
-  const int64_t boxes = (K + kBlockK - 1) / kBlockK;
+  const int64_t boxes = (K + kBlockK - 1) / kBlockK, most = device_sm_count() * 5 / 4;
   MidPlan best{1, boxes * 280};
-  for (int share = 2; share <= 8 && tiles * share <= device_sm_count() && share <= boxes; share *= 2) {
-    const int64_t ns = (boxes + share - 1) / share * 280 + (share < 8 ? 1600 : 2500);
+  for (int share = 2; share <= kMidShare && tiles * share <= most && share <= boxes; share += 2) {
+    const int64_t ns = (boxes + share - 1) / share * 280 + 550 + 75 * share + (tiles > clusters_at_once(share) ? 1300 : 0);
     if (ns < best.ns) best = {share, ns};
   }
   return best;
@@ -993,11 +1066,11 @@ cudaError_t launch_int8_forward(const int8_t* xq, const float* sx, const int8_t*
   const TilePlan wide = tile_plan(M, N, K);
   // More tokens than one narrow tile has take the wide tiles, but where those are few
   // and K is long, so that splitting K over narrow ones is worth its join (at 1.9
-  // cycles a nanosecond; 65 x 120 x 5824: 8.3 us for 15.8 in wide tiles, 412 x 332 x
-  // 3200 7.9 for 10.2).
+  // cycles a nanosecond; 65 x 120 x 5824: 6.1 us for 15.6 in wide tiles, 412 x 332 x
+  // 3200 6.2 for 10.1).
   const int64_t columns = M <= 32 ? 32 : kMidMost, tiles = (N + 127) / 128 * ((M + columns - 1) / columns);
   const MidPlan narrow = mid_plan(tiles, K);
-  if (M <= kMidMost || (tiles * narrow.share <= device_sm_count() && narrow.ns + 400 < wide.cycles * 10 / 19)) {
+  if (M <= kMidMost || (tiles * narrow.share <= device_sm_count() * 5 / 4 && narrow.ns + 400 < wide.cycles * 10 / 19)) {
     const MidParams p{static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), 0, narrow.share, sx, sw, y, err};
     return y_f32 ? forward_mid<float>(xq, wq, p, s) : forward_mid<__nv_bfloat16>(xq, wq, p, s);
   }

@@ -279,6 +279,24 @@ def test_int8_linear(M, N, K, dtype):
     assert torch.equal(y, product(xq, sx, wq, sw, dtype))
 
 
+# tens of tokens, K split over 2 to 8 CTAs: more and fewer tiles than clusters fit at
+# once, N that ends anywhere in a tile and in a group of four channels
+SPLIT = [(64, 6912, 2560), (33, 7001, 2576), (40, 3001, 1504), (64, 5600, 4096), (33, 2040, 4096), (200, 130, 6000),
+         (63, 1000, 8208), (17, 1803, 2576), (32, 2560, 6912), (100, 129, 16384), (35, 1030, 256)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M,N,K", SPLIT)
+def test_int8_linear_split_over_a_cluster(M, N, K, dtype):
+    xq, wq, sx, sw = codes(M, K, seed=M), codes(N, K, seed=N), scales(M, 1), scales(N, 2)
+    hold = torch.full((M * N + 64,), 7.0, dtype=dtype, device="cuda")
+    y = hold[32 : 32 + M * N].view(M, N)
+    bl.bl_int8_linear_forward(xq, sx, wq, sw, y)
+    ok()
+    assert torch.equal(y, product(xq, sx, wq, sw, dtype))
+    assert bool((hold[:32] == 7).all()) and bool((hold[32 + M * N :] == 7).all())
+
+
 @pytest.mark.parametrize("M", [1, 20, 300])
 def test_int8_linear_largest_sums(M):
     """K at its limit with the largest codes: 65536 * 128^2 = 2^30, and sums that
