@@ -57,9 +57,13 @@ constexpr int kBlockK = 128;           // K per stage
 constexpr int kABytes = 128 * kBlockK; // one CTA's tokens of a stage
 constexpr uint32_t kTmemCols = 512;    // two accumulators
 constexpr int kEpiWarps = 8, kWarpEpi0 = 2, kTileThreads = 32 * (kWarpEpi0 + kEpiWarps);
-template <typename TY, int BN>
+constexpr int kBoxPitch = 176;
+template <typename TY, int BN, bool kTma>
 struct Geo {
-  static constexpr int kBox = 32 * 32 * sizeof(TY);  // an epilogue warp's output box, 32 rows x 32 columns
+  // an epilogue warp's output box, 32 rows of 32 columns; or of 128 bytes, where the
+  // warp writes them itself, with 32 bytes in front and 16 behind that part the banks
+  static constexpr int kBoxRow = kTma ? 32 * sizeof(TY) : kBoxPitch;
+  static constexpr int kBox = 32 * kBoxRow;
   static constexpr int kBBytes = BN / 2 * kBlockK;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kStages = (232448 - 1280 - kEpiWarps * (kBox + 128)) / kStageBytes;
@@ -101,23 +105,47 @@ __device__ __forceinline__ uint32_t box_piece(uint32_t box, int row, int j) {
   return box + static_cast<uint32_t>(row) * (32 * kEsize) + (static_cast<uint32_t>(j ^ turn) << 4);
 }
 
-// Element e of row `row` of an output box, in the low bits.
-template <int kEsize>
-__device__ __forceinline__ uint32_t box_element(uint32_t box, int row, int e) {
-  constexpr int kV = 16 / kEsize;
-  const uint32_t at = box_piece<kEsize>(box, row, e / kV) + (e & (kV - 1)) * kEsize;
-  uint32_t w;
-  if constexpr (kEsize == 4) {
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at));
-  } else {
-    uint16_t h;
-    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(h) : "r"(at));
-    w = h;
-  }
-  return w;
+__device__ __forceinline__ void store_word_if(bool yes, char* to, uint32_t w) {
+  asm volatile("{\n.reg .pred q;\nsetp.ne.b32 q, %2, 0;\n@q st.global.b32 [%0], %1;\n}" ::"l"(to), "r"(w), "r"(static_cast<int>(yes)) : "memory");
 }
-__device__ __forceinline__ void store_element(float* p, uint32_t w) { *reinterpret_cast<uint32_t*>(p) = w; }
-__device__ __forceinline__ void store_element(__nv_bfloat16* p, uint32_t w) { *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w); }
+
+// A warp's 32 rows, of which 128 bytes from column col on stand in the box behind the
+// 32 bytes in front of them, go to y in runs that start and end on its 32-byte sectors:
+// of each row, from the last sector boundary up to col to the last one up to the end
+// of the 128 bytes (kEnd: from there to col alone). A row whose columns do not start on
+// a word's boundary stands a column further on in the box, so that its words are y's.
+// Only words within columns lo .. hi - 1 and the first `rows` rows are written.
+// (Runs that start where the 32 columns do: 139 us for 80 at 7788 x 10233 x 384
+// fp32, for partly written sectors; the loop unrolled in full: 100, for instructions
+// that no cache holds; branches around the stores: twice the time.)
+template <typename TY, bool kEnd>
+__device__ __forceinline__ void store_rows(uint32_t box, TY* y, int row0, int rows, int col, int lo, int hi, int N, int lane) {
+  constexpr int kEsize = sizeof(TY), kPer = 4 / kEsize;        // elements of a word
+  constexpr int kLanes = kEnd ? 8 : 32, kStep = 32 / kLanes;   // of a row; rows at once
+  constexpr int kU = 8;                                        // words in flight
+  const int r0 = lane / kLanes, l = lane % kLanes;
+  const uintptr_t start = reinterpret_cast<uintptr_t>(y + static_cast<int64_t>(row0) * N + col);
+  char* to = reinterpret_cast<char*>(start & ~uintptr_t(31)) + 4 * l;
+  const uint32_t step = static_cast<uint32_t>(kStep * kEsize) * static_cast<uint32_t>(N);
+  uint32_t rel = static_cast<uint32_t>(start & 31) + static_cast<uint32_t>(r0 * kEsize) * static_cast<uint32_t>(N);  // of the row
+  uint32_t from = box + r0 * kBoxPitch + 32 + 4 * l;
+#pragma unroll 1
+  for (int r = r0; r < 32; r += kU * kStep) {
+    uint32_t w[kU], at[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      at[u] = rel;
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[u]) : "r"(from + u * kStep * kBoxPitch - (rel & 28)));
+      rel += step;
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int c = col + l * kPer - static_cast<int>((at[u] & 31) / kEsize);
+      store_word_if(r + u * kStep < rows && c >= lo && c + kPer <= hi, to + (at[u] & ~31u), w[u]);
+    }
+    from += kU * kStep * kBoxPitch;
+  }
+}
 
 // TY: type of y. kTma: y's rows start on 16-byte boundaries, so a box leaves by
 // one TMA store; else the warp writes it row by row.
@@ -125,7 +153,7 @@ template <typename TY, int BN, bool kTma>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     int8_tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                      const __grid_constant__ CUtensorMap map_y, const __grid_constant__ TileParams p) {
-  using G = Geo<TY, BN>;
+  using G = Geo<TY, BN, kTma>;
   constexpr int kStages = G::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -299,6 +327,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         if (lane == 0) mbar_arrive_cluster(lead(&tmem_empty[buf]));
       };
       if (live == 0) release();
+      uint32_t last[8], word = 0;  // of the chunk before: a row's last 32 bytes as the box had them; its last word
       uint32_t r[2][32];
       if (live > 0) {
         tmem_ld_32x32b_x32(tbase, r[0]);
@@ -326,18 +355,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         }
         if (kTma && lane == 0) bulk_wait_group_read<0>();
         __syncwarp();
+        uint32_t out[8 * kEsize];
         if constexpr (kEsize == 4) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(box_piece<4>(box, lane, j)), "l"(v[2 * j]), "l"(v[2 * j + 1])
-                         : "memory");
+          for (int j = 0; j < 16; ++j) {
+            float lo, hi;
+            split2(v[j], lo, hi);
+            out[2 * j] = __float_as_uint(lo), out[2 * j + 1] = __float_as_uint(hi);
+          }
         } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            st_shared_v4(box_piece<2>(box, lane, j), pack_bf16x2(v[4 * j]), pack_bf16x2(v[4 * j + 1]),
-                         pack_bf16x2(v[4 * j + 2]), pack_bf16x2(v[4 * j + 3]));
+          for (int j = 0; j < 16; ++j) out[j] = pack_bf16x2(v[j]);
         }
         if constexpr (kTma) {
+#pragma unroll
+          for (int j = 0; j < 2 * kEsize; ++j)
+            st_shared_v4(box_piece<kEsize>(box, lane, j), out[4 * j], out[4 * j + 1], out[4 * j + 2], out[4 * j + 3]);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -345,13 +378,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             bulk_commit_group();
           }
         } else {
-          __syncwarp();
+          // 128 bytes of each row at a time (part h of them now)
+          constexpr int kParts = 4 / kEsize;
+          const int h = c % kParts, left = col - 32 * h, hi = col + 32 < p.N ? col + 32 : p.N;
+          const bool end = c + 1 == live, whole = h == kParts - 1;
+          const uint32_t to = box + lane * kBoxPitch;
+          TY* y = static_cast<TY*>(p.y);
           const int rows = p.M - row0;
-          TY* to = static_cast<TY*>(p.y) + static_cast<int64_t>(row0) * p.N + col + lane;
-#pragma unroll 16
-          for (int i = 0; i < 32; ++i, to += p.N) {
-            const uint32_t w = box_element<kEsize>(box, i, lane);
-            if (i < rows && col + lane < p.N) store_element(to, w);
+          auto front = [&] {
+            st_shared_v4(to, last[0], last[1], last[2], last[3]);
+            st_shared_v4(to + 16, last[4], last[5], last[6], last[7]);
+          };
+          if (h == 0 && c > 0) front();
+          const uint32_t first = out[0], tail = out[8 * kEsize - 1];
+          const bool odd = kEsize == 2 && (lane & p.N & 1);  // the row starts in the middle of a word
+          if constexpr (kEsize == 2) {
+            // (the word in front of the first one is written by nobody here)
+            const uint32_t pick = odd ? 0x5432u : 0x7654u;
+            uint32_t before = c > 0 ? word : 0u;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const uint32_t w = out[j];
+              out[j] = __byte_perm(before, w, pick);
+              before = w;
+            }
+            word = tail;
+          }
+#pragma unroll
+          for (int j = 0; j < 2 * kEsize; ++j)
+            st_shared_v4(to + 32 + h * 64 + 16 * j, out[4 * j], out[4 * j + 1], out[4 * j + 2], out[4 * j + 3]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) last[j] = out[8 * kEsize - 8 + j];
+          if constexpr (kEsize == 2) {
+            // a row's first and last element, where they share their words with columns of others
+            TY* line = y + static_cast<int64_t>(row0 + lane) * p.N;
+            if (c == 0 && odd && lane < rows) *reinterpret_cast<uint16_t*>(line + col) = static_cast<uint16_t>(first);
+            if (end && (odd != ((hi & 1) != 0)) && lane < rows) {
+              uint16_t w = static_cast<uint16_t>(tail >> 16);
+              if (hi < col + 32) asm volatile("ld.shared.b16 %0, [%1];" : "=h"(w) : "r"(to + 32 + 2 * (hi - 1 - left) + 2 * odd) : "memory");
+              *reinterpret_cast<uint16_t*>(line + hi - 1) = w;
+            }
+          }
+          if (whole || end) {
+            __syncwarp();
+            store_rows<TY, false>(box, y, row0, rows, left, col0, hi, p.N, lane);
+            if (whole && end) {
+              __syncwarp();
+              front();
+              __syncwarp();
+              store_rows<TY, true>(box, y, row0, rows, col + 32, col0, hi, p.N, lane);
+            }
           }
         }
         tmem_ld_wait();
@@ -856,7 +932,7 @@ bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType type, uint64
 template <typename TY, int BN, bool kTma>
 cudaError_t launch_tiles(const CUtensorMap (&maps)[3], const TileParams& p, cudaStream_t s) {
   auto kernel = int8_tile_kernel<TY, BN, kTma>;
-  constexpr int kSmem = Geo<TY, BN>::kSmemBytes;
+  constexpr int kSmem = Geo<TY, BN, kTma>::kSmemBytes;
   static int pairs_of[64] = {};  // pairs resident at once, by device
   int dev = 0;
   cudaGetDevice(&dev);
