@@ -147,6 +147,17 @@ __device__ __forceinline__ void store_rows(uint32_t box, TY* y, int row0, int ro
   }
 }
 
+// One lane of the (converged) warp. The loops that load and multiply run in all lanes
+// and this one issues: code after elect.sync keeps an instruction's descriptors in
+// uniform registers (under `lane == 0` each tcgen05.mma took 63 cycles to issue, a
+// stage of four and its waits 530, for 512 of the tensor cores': 36.7 us for 28.8 at 2048 x
+// 2560 x 6912).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n.reg .pred q;\nelect.sync _|q, 0xffffffff;\nselp.b32 %0, 1, 0, q;\n}" : "=r"(yes));
+  return yes != 0;
+}
+
 // TY: type of y. kTma: y's rows start on 16-byte boundaries, so a box leaves by
 // one TMA store; else the warp writes it row by row.
 template <typename TY, int BN, bool kTma>
@@ -204,6 +215,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     st_cluster_u32(map_to_rank(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u), 1u);
     return false;
   };
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };  // a warp's
   auto lead = [&](uint64_t* bar) -> uint32_t { return map_to_rank(smem_u32(bar), 0); };
   const int nkb = (p.K + kBlockK - 1) / kBlockK;
   // tokens fastest: the pairs at work share few tiles of the weights
@@ -211,40 +223,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   auto tile_col = [&](int u) { return u / p.tiles_m * BN; };
 
   if (warp == 0) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, issued = 0;  // stages requested so far
-      const uint32_t bars = lead(full), smem0 = smem_u32(smem);
-      bool ok = true;
-      for (int u = pair; ok && u < p.ntiles; u += npairs) {
-        const int a0 = tile_row(u), b0 = tile_col(u) + static_cast<int>(rank) * (BN / 2);
-        for (int kb = 0; kb < nkb; ++kb) {
-          if (!wait(&empty[stage], phase ^ 1)) {
-            ok = false;
-            break;
-          }
+    const bool one = elect_one();
+    int stage = 0;
+    uint32_t phase = 0, issued = 0;  // stages requested so far
+    const uint32_t bars = lead(full), smem0 = smem_u32(smem);
+    bool ok = true;
+    for (int u = pair; ok && u < p.ntiles; u += npairs) {
+      const int a0 = tile_row(u), b0 = tile_col(u) + static_cast<int>(rank) * (BN / 2);
+      for (int kb = 0; kb < nkb; ++kb) {
+        if (!wait_all(&empty[stage], phase ^ 1)) {
+          ok = false;
+          break;
+        }
+        if (one) {
           // both CTAs' boxes arrive on the leader's barrier
           if (leader) mbar_arrive_expect_tx(&full[stage], 2 * G::kStageBytes);
           const uint32_t at = smem0 + stage * G::kStageBytes, bar = bars + 8 * stage;
           load_pair(&map_x, bar, at, kb * kBlockK, a0);
           load_pair(&map_w, bar, at + kABytes, kb * kBlockK, b0);
-          ++issued;
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1;
-          }
+        }
+        __syncwarp();
+        ++issued;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
         }
       }
-      if (leader && (!ok || *abort_flag)) {
-        // let every copy already issued land before the pair exits
-        const unsigned long long deadline = globaltimer_ns() + kWaitLimitNs;
-        for (uint32_t s = 0; s < kStages && s < issued; ++s)
-          mbar_drain_until(&full[s], (issued - s - 1) / kStages & 1, deadline);
-      }
+    }
+    if (one && leader && (!ok || *abort_flag)) {
+      // let every copy already issued land before the pair exits
+      const unsigned long long deadline = globaltimer_ns() + kWaitLimitNs;
+      for (uint32_t s = 0; s < kStages && s < issued; ++s)
+        mbar_drain_until(&full[s], (issued - s - 1) / kStages & 1, deadline);
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (leader && lane == 0) {
+    if (leader) {
+      const bool one = elect_one();
       constexpr uint32_t kIdesc = make_idesc(2 /*s32*/, 1 /*s8*/, 0, 0, kRows, BN);
       const uint32_t s0 = smem_u32(smem);
       const uint64_t ad0 = smem_desc_sw128(s0, 16, 1024), bd0 = smem_desc_sw128(s0 + kABytes, 16, 1024);
@@ -252,32 +267,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       uint32_t phase = 0, buf_phase = 0;
       bool ok = true;
       for (int u = pair; ok && u < p.ntiles; u += npairs) {
-        if (!wait(&tmem_empty[buf], buf_phase ^ 1)) break;
+        if (!wait_all(&tmem_empty[buf], buf_phase ^ 1)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * 256);
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!wait(&full[stage], phase)) {
+          if (!wait_all(&full[stage], phase)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint64_t at = static_cast<uint64_t>(stage) * (G::kStageBytes >> 4);
+          if (one) {
 #pragma unroll
-          for (int kk = 0; kk < kBlockK / 32; ++kk)
-            mma_i8_pair(d_tmem, ad0 + at + kk * 2, bd0 + at + kk * 2, kIdesc, (kb | kk) != 0);
-          mma_commit_pair(&empty[stage], 0x3);
+            for (int kk = 0; kk < kBlockK / 32; ++kk)
+              mma_i8_pair(d_tmem, ad0 + at + kk * 2, bd0 + at + kk * 2, kIdesc, (kb | kk) != 0);
+            mma_commit_pair(&empty[stage], 0x3);
+          }
+          __syncwarp();
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
           }
         }
-        if (ok) mma_commit_pair(&tmem_full[buf], 0x3);
+        if (ok && one) mma_commit_pair(&tmem_full[buf], 0x3);
+        __syncwarp();
         if (++buf == 2) {
           buf = 0;
           buf_phase ^= 1;
         }
       }
-      mma_commit_pair(done_bar, 0x3);
+      if (one) mma_commit_pair(done_bar, 0x3);
+      __syncwarp();
     }
     if (lane == 0) mbar_drain(done_bar, 0);
     __syncwarp();
@@ -460,8 +480,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
 // warp takes one group of 16 channels and every S-th stage, mma.sync.m16n8k32 on
 // operands that ldmatrix brings in the instruction's order; the S warps' INT32
 // sums are added in shared memory (exact in any order).
-constexpr int64_t kFewMost = 16;   // most tokens, with weights of any size
-constexpr int64_t kFewWeights = int64_t(1) << 22;  // most weights with up to 32
+constexpr int64_t kFewMost = 16;   // most tokens, with weights of any shape
 constexpr int kFewSmem = 114688;   // of a CTA: half an SM's
 
 struct FewParams {
@@ -540,16 +559,17 @@ __global__ void __launch_bounds__(Few<kTok, R>::kThreads, 2)
   pdl_wait_primary();
   pdl_launch_dependents();
   if (warp < G::kLoaders) {
-    if (lane == 0) {
-      const int mine = ((p.ntiles - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1) * nst;  // the CTA's stages
-      int it = warp, st = warp % nst, u = blockIdx.x + warp / nst * gridDim.x;
-      bool ok = true;
-      for (; it < mine; it += G::kLoaders) {
-        const int stage = it % kStages;
-        if (!mbar_wait(&empty[stage], (it / kStages & 1) ^ 1, abort_flag, p.err)) {
-          ok = false;
-          break;
-        }
+    const bool one = elect_one();
+    const int mine = ((p.ntiles - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1) * nst;  // the CTA's stages
+    int it = warp, st = warp % nst, u = blockIdx.x + warp / nst * gridDim.x;
+    bool ok = true;
+    for (; it < mine; it += G::kLoaders) {
+      const int stage = it % kStages;
+      if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], (it / kStages & 1) ^ 1, abort_flag, p.err))) {
+        ok = false;
+        break;
+      }
+      if (one) {
         const bool two = 2 * st + 1 < boxes;
         mbar_arrive_expect_tx(&full[stage], two ? G::kStageBytes : G::kStageBytes / 2);
         uint8_t* at = smem + stage * G::kStageBytes;
@@ -559,14 +579,15 @@ __global__ void __launch_bounds__(Few<kTok, R>::kThreads, 2)
           tma_load_2d(&map_w, &full[stage], at + h * G::kBoxW, (2 * st + h) * 128, u * kN);
           tma_load_2d(&map_x, &full[stage], at + 2 * G::kBoxW + h * G::kBoxX, (2 * st + h) * 128, 0);
         }
-        for (st += G::kLoaders; st >= nst; st -= nst) u += gridDim.x;
       }
-      // an early end: let this thread's copies land before the CTA exits
-      if (!ok || *abort_flag) {
-        const unsigned long long deadline = globaltimer_ns() + kWaitLimitNs;
-        for (int i = it - G::kLoaders, n = 0; i >= 0 && n < kStages; i -= G::kLoaders, n += G::kLoaders)
-          mbar_drain_until(&full[i % kStages], i / kStages & 1, deadline);
-      }
+      __syncwarp();
+      for (st += G::kLoaders; st >= nst; st -= nst) u += gridDim.x;
+    }
+    // an early end: let this warp's copies land before the CTA exits
+    if (one && (!ok || *abort_flag)) {
+      const unsigned long long deadline = globaltimer_ns() + kWaitLimitNs;
+      for (int i = it - G::kLoaders, n = 0; i >= 0 && n < kStages; i -= G::kLoaders, n += G::kLoaders)
+        mbar_drain_until(&full[i % kStages], i / kStages & 1, deadline);
     }
     return;
   }
@@ -690,6 +711,18 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(pair2(v[0], v[1])), pack_bf16x2(pair2(v[2], v[3])));
 }
 
+// Channels n .. n + 3 (n a multiple of 4) of a token, those that there are.
+template <typename TY>
+__device__ __forceinline__ void store_channels(TY* to, const float (&v)[4], int n, int N) {
+  if ((N & 3) == 0) {
+    if (n < N) store4(to, v);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+      if (n + h < N) store1(to + h, v[h]);
+  }
+}
+
 template <typename TY, int NT>
 __global__ void __launch_bounds__(kMidThreads)
     int8_mid_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const MidParams p) {
@@ -730,38 +763,42 @@ __global__ void __launch_bounds__(kMidThreads)
   pdl_wait_primary();
   pdl_launch_dependents();  // (after the allocation: a dependent's must not come first)
   if (warp == 0) {
-    if (lane == 0) {
-      int kb = 0;
-      for (; kb < nkb; ++kb) {
-        const int s = kb % kStages;
-        if (!mbar_wait(&empty[s], (kb / kStages & 1) ^ 1, abort_flag, p.err)) break;
+    const bool one = elect_one();
+    int kb = 0;
+    for (; kb < nkb; ++kb) {
+      const int s = kb % kStages;
+      if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], (kb / kStages & 1) ^ 1, abort_flag, p.err))) break;
+      if (one) {
         mbar_arrive_expect_tx(&full[s], G::kStageBytes);
         uint8_t* at = smem + s * G::kStageBytes;
         tma_load_2d(&map_w, &full[s], at, (kb0 + kb) * kBlockK, n0);
         tma_load_2d(&map_x, &full[s], at + G::kW, (kb0 + kb) * kBlockK, t0);
       }
-      if (kb < nkb || *abort_flag) {
-        const unsigned long long deadline = globaltimer_ns() + kWaitLimitNs;
-        for (int i = kb - 1; i >= 0 && i >= kb - kStages; --i)
-          mbar_drain_until(&full[i % kStages], i / kStages & 1, deadline);
-      }
+      __syncwarp();
+    }
+    if (one && (kb < nkb || *abort_flag)) {
+      const unsigned long long deadline = globaltimer_ns() + kWaitLimitNs;
+      for (int i = kb - 1; i >= 0 && i >= kb - kStages; --i)
+        mbar_drain_until(&full[i % kStages], i / kStages & 1, deadline);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t kIdesc = make_idesc(2 /*s32*/, 1 /*s8*/, 0, 0, 128, NT);
-      const uint32_t s0 = smem_u32(smem);
-      const uint64_t ad0 = smem_desc_sw128(s0, 16, 1024), bd0 = smem_desc_sw128(s0 + G::kW, 16, 1024);
-      for (int kb = 0; kb < nkb; ++kb) {
-        const int s = kb % kStages;
-        if (!mbar_wait(&full[s], kb / kStages & 1, abort_flag, p.err)) break;
-        tc_fence_after();
-        const uint64_t at = static_cast<uint64_t>(s) * (G::kStageBytes >> 4);
+    const bool one = elect_one();
+    constexpr uint32_t kIdesc = make_idesc(2 /*s32*/, 1 /*s8*/, 0, 0, 128, NT);
+    const uint32_t s0 = smem_u32(smem);
+    const uint64_t ad0 = smem_desc_sw128(s0, 16, 1024), bd0 = smem_desc_sw128(s0 + G::kW, 16, 1024);
+    for (int kb = 0; kb < nkb; ++kb) {
+      const int s = kb % kStages;
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[s], kb / kStages & 1, abort_flag, p.err))) break;
+      tc_fence_after();
+      const uint64_t at = static_cast<uint64_t>(s) * (G::kStageBytes >> 4);
+      if (one) {
 #pragma unroll
         for (int kk = 0; kk < kBlockK / 32; ++kk) mma_i8_one(tmem, ad0 + at + kk * 2, bd0 + at + kk * 2, kIdesc, (kb | kk) != 0);
         mma_commit_one(&empty[s]);
       }
-      mma_commit_one(done);
+      __syncwarp();
     }
+    if (one) mma_commit_one(done);
   }
   __syncwarp();
   const int q = warp & 3, row = q * 32 + lane, n = n0 + row;
@@ -841,14 +878,7 @@ __global__ void __launch_bounds__(kMidThreads)
           const float s = sx[m];
           const float o[4] = {__int2float_rn(v.x) * __fmul_rn(s, w[0]), __int2float_rn(v.y) * __fmul_rn(s, w[1]),
                               __int2float_rn(v.z) * __fmul_rn(s, w[2]), __int2float_rn(v.w) * __fmul_rn(s, w[3])};
-          TY* to = y + static_cast<int64_t>(m) * p.N + c0;
-          if ((p.N & 3) == 0) {
-            if (c0 < p.N) store4(to, o);
-          } else {
-#pragma unroll
-            for (int h = 0; h < 4; ++h)
-              if (c0 + h < p.N) store1(to + h, o[h]);
-          }
+          store_channels(y + static_cast<int64_t>(m) * p.N + c0, o, c0, p.N);
         }
       };
       switch (share) {
@@ -970,8 +1000,9 @@ cudaError_t forward_tiles(const int8_t* xq, const int8_t* wq, TileParams p, cuda
 }
 
 // The tiles' width: the least time of the busiest pair, its tiles times a stage's
-// MMAs (measured: 122 cycles for 32 of K with 128 columns, 168 with 256, so 76 +
-// 0.36 a column) and the end of one tile.
+// MMAs (measured with all SMs at work, in cycles of 1.9 GHz: 88 for 32 of K with 64
+// columns, 109 with 128, 136 with 192, 183 with 256; so 45 + 0.5 a column) and 300 for
+// each tile, and the end of one tile.
 struct TilePlan {
   int columns;
   int64_t cycles;
@@ -981,7 +1012,7 @@ TilePlan tile_plan(int64_t M, int64_t N, int64_t K) {
   TilePlan best{256, INT64_MAX};
   for (int bn = 256; bn >= 64; bn -= 32) {
     const int64_t rounds = (tiles_m * ((N + bn - 1) / bn) + pairs - 1) / pairs;
-    const int64_t cycles = (rounds * nkb * 4 * (7600 + 36 * bn) + 1000 * bn) / 100;
+    const int64_t cycles = rounds * (nkb * (180 + 2 * bn) + 300) + 10 * bn;
     if (cycles < best.cycles) best = {bn, cycles};
   }
   return best;
@@ -1076,7 +1107,7 @@ int clusters_at_once(int share) {
 }
 
 // CTAs per tile (1 or even: 3, 5 and 7 measured 0.25 us more than their stages say), and
-// the nanoseconds that follow from it: 280 per stage of a CTA, 550 + 75 per CTA for a
+// the nanoseconds that follow from it: 260 per stage of a CTA, 550 + 75 per CTA for a
 // join, 1300 where the clusters do not fit one CTA to an SM (64 tokens, 17 tiles, 32
 // stages: 13.5 us alone, 9.8 over 2 CTAs, 7.9 over 4, 7.5 over 6, 8.5 over 8; 15 tiles:
 // 7.3 over 8).
@@ -1086,12 +1117,31 @@ struct MidPlan {
 };
 MidPlan mid_plan(int64_t tiles, int64_t K) {
   const int64_t boxes = (K + kBlockK - 1) / kBlockK, most = device_sm_count() * 5 / 4;
-  MidPlan best{1, boxes * 280};
+  MidPlan best{1, boxes * 260};
   for (int share = 2; share <= kMidShare && tiles * share <= most && share <= boxes; share += 2) {
-    const int64_t ns = (boxes + share - 1) / share * 280 + 550 + 75 * share + (tiles > clusters_at_once(share) ? 1300 : 0);
+    const int64_t ns = (boxes + share - 1) / share * 260 + 550 + 75 * share + (tiles > clusters_at_once(share) ? 1300 : 0);
     if (ns < best.ns) best = {share, ns};
   }
   return best;
+}
+
+// A programmatic dependent launch of clusters of `cluster` CTAs.
+template <typename... Params, typename... Args>
+cudaError_t launch_clusters(void (*kernel)(Params...), int grid, int cluster, int threads, int smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <typename TY, int NT>
@@ -1106,20 +1156,7 @@ cudaError_t launch_mid(const int8_t* xq, const int8_t* wq, MidParams p, cudaStre
     return cudaErrorInvalidValue;
   p.tiles_n = (p.N + 127) / 128;
   const int tiles = p.tiles_n * ((p.M + NT - 1) / NT);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(tiles * p.share);
-  cfg.blockDim = dim3(kMidThreads);
-  cfg.dynamicSmemBytes = G::kSmemBytes;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = p.share;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, x, w, p);
+  return launch_clusters(kernel, tiles * p.share, p.share, kMidThreads, G::kSmemBytes, s, x, w, p);
 }
 
 template <typename TY>
@@ -1133,17 +1170,19 @@ size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
 cudaError_t launch_int8_forward(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw, int64_t M,
                                 int64_t N, int64_t K, void* y, int y_f32, int* err, cudaStream_t s) {
-  // Up to 16 tokens stream the weights through mma.sync, up to 32 where the weights
-  // are small: its MMAs are a few times slower than tcgen05's, its start 2 us shorter.
-  if (M <= kFewMost || (M <= 32 && N * K <= kFewWeights)) {
+  // Up to 16 tokens stream the weights through mma.sync, up to 32 where K and the
+  // weights are of middling size: its start is 0.5 us shorter, its stages are slower (17
+  // to 32 tokens: 1000 x 768 3.1 us for 3.6, 2048 x 1024 3.3 for 3.7; 2560 x 2560 6.7
+  // for 5.3, 8192 x 512 4.0 for 3.3).
+  if (M <= kFewMost || (M <= 32 && K >= 512 && K <= 2048 && N <= 4096 && N * K <= int64_t(1) << 22)) {
     const FewParams p{static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), 0, sx, sw, y, err};
     return y_f32 ? forward_few<float>(xq, wq, p, s) : forward_few<__nv_bfloat16>(xq, wq, p, s);
   }
   const TilePlan wide = tile_plan(M, N, K);
   // More tokens than one narrow tile has take the wide tiles, but where those are few
   // and K is long, so that splitting K over narrow ones is worth its join (at 1.9
-  // cycles a nanosecond; 65 x 120 x 5824: 6.1 us for 15.6 in wide tiles, 412 x 332 x
-  // 3200 6.2 for 10.1).
+  // cycles a nanosecond; 65 x 120 x 5824: 5.5 us for 10.3 in wide tiles, 412 x 332 x
+  // 3200 5.6 for 7.6).
   const int64_t columns = M <= 32 ? 32 : kMidMost, tiles = (N + 127) / 128 * ((M + columns - 1) / columns);
   const MidPlan narrow = mid_plan(tiles, K);
   if (M <= kMidMost || (tiles * narrow.share <= device_sm_count() * 5 / 4 && narrow.ns + 400 < wide.cycles * 10 / 19)) {
