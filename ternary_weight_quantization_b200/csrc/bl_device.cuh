@@ -234,6 +234,16 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
+// One lane of the (converged) warp. A loop that loads or multiplies runs in all lanes of
+// its warp and this one issues: code after elect.sync keeps the instructions' descriptors
+// in uniform registers. (Under `lane == 0` each tcgen05.mma took 63 cycles to issue, a
+// stage of four and its waits 530, for 512 of the tensor cores'.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.b32 %0, 1, 0, q;\n\t}" : "=r"(yes));
+  return yes != 0;
+}
+
 // Pair MMA (issued by one thread of the leader CTA): A rows split across the
 // two CTAs' shared memory, B rows split likewise, D rows split across the two
 // CTAs' TMEM.

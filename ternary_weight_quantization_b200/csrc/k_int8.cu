@@ -147,17 +147,6 @@ __device__ __forceinline__ void store_rows(uint32_t box, TY* y, int row0, int ro
   }
 }
 
-// One lane of the (converged) warp. The loops that load and multiply run in all lanes
-// and this one issues: code after elect.sync keeps an instruction's descriptors in
-// uniform registers (under `lane == 0` each tcgen05.mma took 63 cycles to issue, a
-// stage of four and its waits 530, for 512 of the tensor cores': 36.7 us for 28.8 at 2048 x
-// 2560 x 6912).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t yes;
-  asm volatile("{\n.reg .pred q;\nelect.sync _|q, 0xffffffff;\nselp.b32 %0, 1, 0, q;\n}" : "=r"(yes));
-  return yes != 0;
-}
-
 // TY: type of y. kTma: y's rows start on 16-byte boundaries, so a box leaves by
 // one TMA store; else the warp writes it row by row.
 template <typename TY, int BN, bool kTma>

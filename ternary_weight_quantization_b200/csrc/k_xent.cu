@@ -376,106 +376,110 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
     st_cluster_u32(map_to_rank(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u), 1u);
     return false;
   };
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };  // a warp's
   auto lead = [&](uint64_t* bar) -> uint32_t { return map_to_rank(smem_u32(bar), 0); };
 
   if (warp == kWarpLoad) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, issued = 0;  // stages requested so far
-      const uint32_t bars = lead(full), smem0 = smem_u32(smem);
-      bool ok = true;
-      int u;
-      for (int i = 0; ok && next_tile(p, pair, npairs, i, u); ++i) {
-        const Tile t = decode<P, BN>(p, u);
-        const int a0 = t.a0 + static_cast<int>(rank) * 128, b0 = t.b0 + static_cast<int>(rank) * (BN / 2);
-        // both CTAs' boxes arrive on the leader's barrier
-        uint32_t bytes = 2 * kStageBytes;
-        int na = 2, nb = 2;
-        if constexpr (P != Phase::Grad) {
-          const CtaBoxes<BN> first(p, t, 0), second(p, t, 1);
-          na = leader ? first.a : second.a;
-          nb = leader ? first.b : second.b;
-          bytes = kBox * (first.a + first.b + second.a + second.b);
-        }
-        // one loop per kind of tile: a stage must be requested in the few hundred
-        // cycles that the tensor cores take for one
-        auto each = [&](int n, auto load) {
-          for (int kb = 0; kb < n; ++kb) {
-            if (!wait(&empty[stage], phase ^ 1)) {
-              ok = false;
-              return;
-            }
+    const bool one = elect_one();
+    int stage = 0;
+    uint32_t phase = 0, issued = 0;  // stages requested so far
+    const uint32_t bars = lead(full), smem0 = smem_u32(smem);
+    bool ok = true;
+    int u;
+    for (int i = 0; ok && next_tile(p, pair, npairs, i, u); ++i) {
+      const Tile t = decode<P, BN>(p, u);
+      const int a0 = t.a0 + static_cast<int>(rank) * 128, b0 = t.b0 + static_cast<int>(rank) * (BN / 2);
+      // both CTAs' boxes arrive on the leader's barrier
+      uint32_t bytes = 2 * kStageBytes;
+      int na = 2, nb = 2;
+      if constexpr (P != Phase::Grad) {
+        const CtaBoxes<BN> first(p, t, 0), second(p, t, 1);
+        na = leader ? first.a : second.a;
+        nb = leader ? first.b : second.b;
+        bytes = kBox * (first.a + first.b + second.a + second.b);
+      }
+      // one loop per kind of tile: a stage must be requested in the few hundred
+      // cycles that the tensor cores take for one
+      auto each = [&](int n, auto load) {
+        for (int kb = 0; kb < n; ++kb) {
+          if (!wait_all(&empty[stage], phase ^ 1)) {
+            ok = false;
+            return;
+          }
+          if (one) {
             if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
             load(kb, bars + 8 * stage, smem0 + stage * kStageBytes);
-            ++issued;
-            if (++stage == kStages) {
-              stage = 0;
-              phase ^= 1;
-            }
           }
-        };
-        // K-major: (reduction, row); MN-major: (row, reduction)
-        if constexpr (P != Phase::Grad) {
-          const int w0 = p.v0 + b0;
-          if (na == 2 && nb == BN / 128) {
-            each(t.nkb, [&](int kb, uint32_t bar, uint32_t sa) {
-              const int k0 = kb * kBlockR;
-#pragma unroll
-              for (int j = 0; j < 2; ++j) load_pair(&map_h, bar, sa + j * kBox, k0, a0 + 64 * j);
-#pragma unroll
-              for (int j = 0; j < BN / 128; ++j) load_pair(&map_w, bar, sa + (2 + j) * kBox, k0, w0 + 64 * j);
-            });
-          } else {
-            each(t.nkb, [&](int kb, uint32_t bar, uint32_t sa) {
-              const int k0 = kb * kBlockR;
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-                if (j < na) load_pair(&map_h, bar, sa + j * kBox, k0, a0 + 64 * j);
-#pragma unroll
-              for (int j = 0; j < BN / 128; ++j)
-                if (j < nb) load_pair(&map_w, bar, sa + (2 + j) * kBox, k0, w0 + 64 * j);
-            });
-          }
-        } else if (t.cls == 0) {
-          const int v0 = t.kb0 * kBlockR;
-          each(t.nkb, [&](int kb, uint32_t bar, uint32_t sa) {
-            const int v = v0 + kb * kBlockR;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              load_pair(&map_dz, bar, sa + j * kBox, v, a0 + 64 * j);
-              load_pair(&map_w, bar, sa + (2 + j) * kBox, b0 + 64 * j, p.v0 + v);
-            }
-          });
-        } else {
-          auto of = [&](const CUtensorMap* dz) {
-            return [&, dz](int kb, uint32_t bar, uint32_t sa) {
-              const int m = p.t0 + kb * kBlockR;
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                load_pair(dz, bar, sa + j * kBox, a0 + 64 * j, m);
-                load_pair(&map_h, bar, sa + (2 + j) * kBox, b0 + 64 * j, m);
-              }
-            };
-          };
-          if (p.split) {
-            each(t.nkb >> 1, of(&map_dz_lo));
-            if (ok) each(t.nkb >> 1, of(&map_dz));
-          } else {
-            each(t.nkb, of(&map_dz));
+          __syncwarp();
+          ++issued;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
           }
         }
+      };
+      // K-major: (reduction, row); MN-major: (row, reduction)
+      if constexpr (P != Phase::Grad) {
+        const int w0 = p.v0 + b0;
+        if (na == 2 && nb == BN / 128) {
+          each(t.nkb, [&](int kb, uint32_t bar, uint32_t sa) {
+            const int k0 = kb * kBlockR;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) load_pair(&map_h, bar, sa + j * kBox, k0, a0 + 64 * j);
+#pragma unroll
+            for (int j = 0; j < BN / 128; ++j) load_pair(&map_w, bar, sa + (2 + j) * kBox, k0, w0 + 64 * j);
+          });
+        } else {
+          each(t.nkb, [&](int kb, uint32_t bar, uint32_t sa) {
+            const int k0 = kb * kBlockR;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (j < na) load_pair(&map_h, bar, sa + j * kBox, k0, a0 + 64 * j);
+#pragma unroll
+            for (int j = 0; j < BN / 128; ++j)
+              if (j < nb) load_pair(&map_w, bar, sa + (2 + j) * kBox, k0, w0 + 64 * j);
+          });
+        }
+      } else if (t.cls == 0) {
+        const int v0 = t.kb0 * kBlockR;
+        each(t.nkb, [&](int kb, uint32_t bar, uint32_t sa) {
+          const int v = v0 + kb * kBlockR;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            load_pair(&map_dz, bar, sa + j * kBox, v, a0 + 64 * j);
+            load_pair(&map_w, bar, sa + (2 + j) * kBox, b0 + 64 * j, p.v0 + v);
+          }
+        });
+      } else {
+        auto of = [&](const CUtensorMap* dz) {
+          return [&, dz](int kb, uint32_t bar, uint32_t sa) {
+            const int m = p.t0 + kb * kBlockR;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              load_pair(dz, bar, sa + j * kBox, a0 + 64 * j, m);
+              load_pair(&map_h, bar, sa + (2 + j) * kBox, b0 + 64 * j, m);
+            }
+          };
+        };
+        if (p.split) {
+          each(t.nkb >> 1, of(&map_dz_lo));
+          if (ok) each(t.nkb >> 1, of(&map_dz));
+        } else {
+          each(t.nkb, of(&map_dz));
+        }
       }
-      if (leader && (!ok || *abort_flag)) {
-        // let every copy already issued land before the pair exits: the last
-        // request of each stage that was requested at all
-        const unsigned long long deadline = globaltimer_ns() + kWaitLimitNs;
-        for (uint32_t s = 0; s < kStages && s < issued; ++s)
-          mbar_drain_until(&full[s], (issued - s - 1) / kStages & 1, deadline);
-      }
+    }
+    if (one && leader && (!ok || *abort_flag)) {
+      // let every copy already issued land before the pair exits: the last
+      // request of each stage that was requested at all
+      const unsigned long long deadline = globaltimer_ns() + kWaitLimitNs;
+      for (uint32_t s = 0; s < kStages && s < issued; ++s)
+        mbar_drain_until(&full[s], (issued - s - 1) / kStages & 1, deadline);
     }
     __syncwarp();
   } else if (warp == kWarpMma) {
-    if (leader && lane == 0) {
+    if (leader) {
+      const bool one = elect_one();
       const uint32_t s0 = smem_u32(smem);
       int stage = 0, buf = 0;
       uint32_t phase = 0, buf_phase = 0;
@@ -484,27 +488,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
       for (int i = 0; ok && next_tile(p, pair, npairs, i, u); ++i) {
         const Tile t = decode<P, BN>(p, u);
         if (t.nkb == 0) continue;
-        if (!wait(&tmem_empty[buf], buf_phase ^ 1)) break;
+        if (!wait_all(&tmem_empty[buf], buf_phase ^ 1)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * kTile);
         auto each = [&](auto a_mn, auto b_mn) {
           constexpr bool kAMn = decltype(a_mn)::value, kBMn = decltype(b_mn)::value;
           const uint64_t ad0 = operand_desc(s0, kAMn), bd0 = operand_desc(s0 + 2 * kBox, kBMn);
           for (int kb = 0; kb < t.nkb; ++kb) {
-            if (!wait(&full[stage], phase)) {
+            if (!wait_all(&full[stage], phase)) {
               ok = false;
               return;
             }
             tc_fence_after();
             const uint64_t at = static_cast<uint64_t>(stage) * (kStageBytes >> 4);
-            mma_stage<kAMn, kBMn, BN>(d_tmem, ad0 + at, bd0 + at, kb);
-            mma_commit_pair(&empty[stage], 0x3);
+            if (one) {
+              mma_stage<kAMn, kBMn, BN>(d_tmem, ad0 + at, bd0 + at, kb);
+              mma_commit_pair(&empty[stage], 0x3);
+            }
+            __syncwarp();
             if (++stage == kStages) {
               stage = 0;
               phase ^= 1;
             }
           }
-          mma_commit_pair(&tmem_full[buf], 0x3);
+          if (one) mma_commit_pair(&tmem_full[buf], 0x3);
+          __syncwarp();
         };
         using K = std::false_type;
         using MN = std::true_type;
@@ -516,7 +524,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
           buf_phase ^= 1;
         }
       }
-      mma_commit_pair(done_bar, 0x3);
+      if (one) mma_commit_pair(done_bar, 0x3);
+      __syncwarp();
     }
     if (lane == 0) mbar_drain(done_bar, 0);
     __syncwarp();
