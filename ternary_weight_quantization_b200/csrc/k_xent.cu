@@ -127,6 +127,7 @@ struct XentParams {
   int h_add;             // ... and is added to them (later pieces)
   int t0, tcount;        // tokens of this launch's share of dW
   int w_f32, w_add;      // dW is fp32; dW adds to its contents
+  int w_slices, w_rows;  // the reduction of dW is split over this many fp32 partial sums (1: none), rows between them
   void* dW;              // for the bf16 sums that read dW back
 };
 
@@ -178,9 +179,16 @@ __device__ __forceinline__ Tile decode(const XentParams& p, int u) {
   } else {
     u -= p.ntiles_h;
     t.cls = 1;
+    t.nkb = (p.tcount + kBlockR - 1) / kBlockR;
+    if (p.w_slices > 1) {
+      const int per = (p.vcount + kTile - 1) / kTile * p.tiles_k, nkb = t.nkb;
+      t.slice = u / per;
+      u -= t.slice * per;
+      t.kb0 = static_cast<int>(static_cast<int64_t>(nkb) * t.slice / p.w_slices);
+      t.nkb = static_cast<int>(static_cast<int64_t>(nkb) * (t.slice + 1) / p.w_slices) - t.kb0;
+    }
     t.a0 = (u / p.tiles_k) * kTile;
     t.b0 = (u % p.tiles_k) * kTile;
-    t.nkb = (p.tcount + kBlockR - 1) / kBlockR;
     if (p.split) t.nkb *= 2;  // the remainders first, while the sums are small
   }
   return t;
@@ -453,7 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
       } else {
         auto of = [&](const CUtensorMap* dz) {
           return [&, dz](int kb, uint32_t bar, uint32_t sa) {
-            const int m = p.t0 + kb * kBlockR;
+            const int m = p.t0 + (t.kb0 + kb) * kBlockR;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               load_pair(dz, bar, sa + j * kBox, a0 + 64 * j, m);
@@ -709,13 +717,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
           if (col >= p.K) return;
 #pragma unroll
           for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * scale);
-          const bool f32 = t.cls == 0 ? p.h_f32 != 0 : p.w_f32 != 0;
+          const bool f32 = t.cls == 0 ? p.h_f32 != 0 : p.w_f32 != 0 || p.w_slices > 1;
           if (f32) {
             box = st.next();
 #pragma unroll
             for (int j = 0; j < 8; ++j) st_shared_v4(box_chunk(box, lane, j), r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
             if (t.cls == 0) st.store(&out0, box, col, t.slice * p.rows_pad + row0, p.h_add != 0);
-            else st.store(&out1, box, col, p.v0 + row0, p.w_add != 0);
+            else st.store(&out1, box, col, p.v0 + t.slice * p.w_rows + row0, p.w_add != 0);
           } else {
             if (t.cls == 1 && p.w_add && row < p.vcount) {
               // one rounding: the bf16 contents are added to the fp32 sum
@@ -1035,9 +1043,9 @@ Plan make_plan(int64_t M, int64_t V, int64_t K, bool f32) {
 // Tiles of a Grad launch and their costs, from the vocabulary and the tokens set.
 void grad_tiles(XentParams& p, bool dh, bool dw) {
   p.ntiles_h = dh ? p.slices * p.tiles_m * p.tiles_k : 0;
-  const int ntiles_w = dw ? tiles_of(p.vcount) * p.tiles_k : 0;
+  const int ntiles_w = dw ? p.w_slices * tiles_of(p.vcount) * p.tiles_k : 0;
   const int cost_h = (p.vcount + kBlockR - 1) / kBlockR / p.slices;
-  const int cost_w = (p.tcount + kBlockR - 1) / kBlockR * (p.split ? 2 : 1);
+  const int cost_w = (p.tcount + kBlockR - 1) / kBlockR * (p.split ? 2 : 1) / p.w_slices;
   p.dw_first = cost_w > cost_h || p.ntiles_h == 0;
   p.ntiles_a = p.dw_first ? ntiles_w : p.ntiles_h;
   p.ntiles_b = p.dw_first ? p.ntiles_h : ntiles_w;
@@ -1193,6 +1201,7 @@ cudaError_t launch_xent_backward(const void* h, const void* W, const int64_t* ta
   p.rows_pad = static_cast<int>(q.rows_pad);
   p.h_f32 = q.sums;
   p.w_f32 = f32;
+  p.w_slices = 1;
   p.dW = dW;
 
   CUtensorMap zm[6] = {}, gm[6] = {};  // maps of Dz and of Grad
@@ -1246,6 +1255,49 @@ cudaError_t launch_xent_backward(const void* h, const void* W, const int64_t* ta
 // the place of dz, x of h and w of the head
 namespace {
 
+// The fp32 partial sums of dX and of dW joined, each in order: to bf16 or fp32, and
+// with `add` to what is there (one rounding to bf16). The first blocks take dX's.
+struct JoinPart {
+  const float4* sums;
+  void* out;
+  int64_t slice_vecs, vecs;  // from a slice to the next; outputs, in fours
+  int slices, f32, add, blocks;
+};
+
+__device__ __forceinline__ void join_sums(const JoinPart& p, int block) {
+  const int64_t T = static_cast<int64_t>(p.blocks) * 256;
+  for (int64_t i = static_cast<int64_t>(block) * 256 + threadIdx.x; i < p.vecs; i += T) {
+    float4 v = p.sums[i];
+    for (int s = 1; s < p.slices; ++s) {
+      const float4 w = p.sums[s * p.slice_vecs + i];
+      v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+    }
+    if (p.f32) {
+      float4* to = static_cast<float4*>(p.out) + i;
+      if (p.add) {
+        const float4 o = *to;
+        v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+      }
+      *to = v;
+    } else {
+      uint2* to = static_cast<uint2*>(p.out) + i;
+      if (p.add) {
+        const uint2 o = *to;
+        v.x += bf16_lo(o.x), v.y += bf16_hi(o.x), v.z += bf16_lo(o.y), v.w += bf16_hi(o.y);
+      }
+      *to = make_uint2(pack_bf16x2(v.y, v.x), pack_bf16x2(v.w, v.z));
+    }
+  }
+}
+
+__global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ JoinPart first, const __grid_constant__ JoinPart second) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int block = static_cast<int>(blockIdx.x);
+  if (block < first.blocks) join_sums(first, block);
+  else join_sums(second, block - first.blocks);
+}
+
 // Slices of dX's reduction: as of dH, and each at most 131072 columns (the
 // tensor cores' sums lose up to a step of fp32 per 16 terms).
 int linear_slices(int64_t M, int64_t N, int64_t K) {
@@ -1254,12 +1306,33 @@ int linear_slices(int64_t M, int64_t N, int64_t K) {
 }
 int64_t pad_rows(int64_t M) { return (M + kTile - 1) / kTile * kTile; }
 
+// Slices of dW's reduction over the tokens, where its tiles are few: parts of at most
+// two thirds of a pair's even share of all k-blocks, as of dH (4096 tokens, 512
+// channels, K 2560: 20 tiles of 64 k-blocks next to dX's 160 of 8); an fp32 dW
+// takes at most 1024 tokens in each, or, where those sums are too many, one launch
+// for each 1024 tokens. 1: none. (As many without dX: dW is the same then.)
+int linear_w_slices(int64_t M, int64_t N, int64_t K, bool f32) {
+  const int64_t tiles = static_cast<int64_t>(tiles_of(N)) * tiles_of(K), nkb = (M + kBlockR - 1) / kBlockR;
+  if (tiles >= kPlanPairs) return 1;
+  const int64_t others = static_cast<int64_t>(tiles_of(M)) * tiles_of(K) * ((N + kBlockR - 1) / kBlockR + 8);
+  const int64_t share = (tiles * nkb + others) / kPlanPairs + 8, most = (3 * kPlanPairs + 2 * tiles - 1) / (2 * tiles);
+  int64_t slices = (3 * nkb + 2 * share - 1) / (2 * share);
+  if (f32 && slices < (M + kF32Tokens - 1) / kF32Tokens) slices = (M + kF32Tokens - 1) / kF32Tokens;
+  if (slices > 32 || slices > most || slices > nkb) {
+    slices = most < nkb ? most : nkb;
+    if (slices > 32) slices = 32;
+    if (f32 && slices * kF32Tokens < M) return 1;
+  }
+  return slices < 1 ? 1 : static_cast<int>(slices);
+}
+
 }  // namespace
 
 // Never shrinks as tokens are added, as the sizes of the head's backward: for
 // every smaller number of token tiles a bound on its slices, those of
 // make_plan's comment (up to kPlanPairs / tiles and a half, 32, and k-blocks).
-size_t linear_grad_sum_bytes(int64_t M, int64_t N, int64_t K) {
+// dW's slices are at most ceil(1.5 kPlanPairs / tiles), 32, and k-blocks.
+static size_t linear_x_sum_bytes(int64_t M, int64_t N, int64_t K) {
   const int64_t tm = tiles_of(M), tk = tiles_of(K), nkb = (N + kBlockR - 1) / kBlockR, least = (N + 131071) / 131072;
   int64_t rows = least > 1 ? tm * least : 0;  // of the partial sums, in tiles
   for (int64_t m = 1; m <= tm && m * tk < kPlanPairs; ++m) {
@@ -1269,6 +1342,14 @@ size_t linear_grad_sum_bytes(int64_t M, int64_t N, int64_t K) {
     if (slices > 1 && m * slices > rows) rows = m * slices;
   }
   return static_cast<size_t>(rows) * kTile * K * 4;
+}
+
+size_t linear_grad_sum_bytes(int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = static_cast<int64_t>(tiles_of(N)) * tiles_of(K), nkb = (M + kBlockR - 1) / kBlockR;
+  int64_t slices = tiles < kPlanPairs ? (3 * kPlanPairs + 2 * tiles - 1) / (2 * tiles) : 0;
+  slices = slices > 32 ? 32 : slices;
+  slices = slices > nkb ? nkb : slices;
+  return linear_x_sum_bytes(M, N, K) + (slices > 1 ? static_cast<size_t>(slices * pad_rows(N)) * K * 4 : 0);
 }
 
 cudaError_t launch_linear_grads(const void* dY, const void* x, const void* w, int64_t M, int64_t N, int64_t K, void* dX,
@@ -1289,10 +1370,15 @@ cudaError_t launch_linear_grads(const void* dY, const void* x, const void* w, in
   p.h_f32 = p.slices > 1;
   p.w_f32 = f32;
   p.dW = dW;
+  p.w_slices = dW ? linear_w_slices(M, N, K, f32) : 1;
+  p.w_rows = static_cast<int>(pad_rows(N));
+  const bool split = p.w_slices > 1;
+  float* w_sums = sums + linear_x_sum_bytes(M, N, K) / 4;
   CUtensorMap gm[6] = {};
   if (!make_map(&gm[2], dY, false, N, M, N * 2, 64, 64)) return cudaErrorInvalidValue;
   if (dW && (!make_map(&gm[0], x, false, K, M, K * 2, 64, 64) ||
-             !make_map(&gm[5], dW, f32, K, N, K * (f32 ? 4 : 2), f32 ? 32 : 64, 32)))
+             !(split ? make_map(&gm[5], w_sums, true, K, static_cast<uint64_t>(p.w_slices) * p.w_rows, K * 4, 32, 32)
+                     : make_map(&gm[5], dW, f32, K, N, K * (f32 ? 4 : 2), f32 ? 32 : 64, 32))))
     return cudaErrorInvalidValue;
   if (dX && (!make_map(&gm[1], w, false, K, N, K * 2, 64, 64) ||
              !(p.h_f32 ? make_map(&gm[4], sums, true, K, static_cast<uint64_t>(p.slices) * p.rows_pad, K * 4, 32, 32)
@@ -1301,16 +1387,27 @@ cudaError_t launch_linear_grads(const void* dY, const void* x, const void* w, in
   // maps that no tile uses are prefetched all the same
   for (int i : {0, 1, 3, 4, 5})
     if ((i == 3) || (!dW && (i == 0 || i == 5)) || (!dX && (i == 1 || i == 4))) gm[i] = gm[2];
-  const int step = f32 ? kF32Tokens : p.M;
+  const int step = f32 && !split ? kF32Tokens : p.M;
   for (int t0 = 0; t0 < p.M; t0 += step) {
     p.t0 = t0;
     p.tcount = p.M - t0 < step ? p.M - t0 : step;
-    p.w_add = accumulate || t0 > 0;
+    p.w_add = !split && (accumulate || t0 > 0);
     grad_tiles(p, dX && t0 == 0, dW != nullptr);
     if (cudaError_t e = launch_phase<Phase::Grad, 256>(gm, p, s); e != cudaSuccess) return e;
     if (!dW) break;
   }
-  return dX && p.h_f32 ? join_dh(sums, p.rows_pad, p.slices, M, K, dX, s) : cudaSuccess;
+  JoinPart parts[2] = {};
+  if (dX && p.h_f32)
+    parts[0] = {reinterpret_cast<const float4*>(sums), dX, static_cast<int64_t>(p.rows_pad) * K / 4, M * K / 4, p.slices, 0, 0, 0};
+  if (split)
+    parts[1] = {reinterpret_cast<const float4*>(w_sums), dW, static_cast<int64_t>(p.w_rows) * K / 4, N * K / 4, p.w_slices, f32, accumulate, 0};
+  for (JoinPart& part : parts) {
+    const int64_t want = (part.vecs + 255) / 256, cap = static_cast<int64_t>(8) * device_sm_count();
+    part.blocks = static_cast<int>(want < cap ? want : cap);
+  }
+  const int blocks = parts[0].blocks + parts[1].blocks;
+  if (blocks == 0) return cudaSuccess;
+  return launch_pdl(linear_join_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, parts[0], parts[1]);
 }
 
 }  // namespace bl

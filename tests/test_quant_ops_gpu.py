@@ -342,7 +342,9 @@ def test_int8_linear_scales_that_are_not_finite_stay_with_their_token_and_channe
 
 
 GRADS = [(1, 8, 16), (3, 64, 48), (16, 256, 512), (33, 1000, 128), (100, 136, 272), (257, 5000, 144), (700, 1408, 512),
-         (64, 32000, 80), (1030, 264, 400), (2048, 512, 1408)]
+         (64, 32000, 80), (1030, 264, 400), (2048, 512, 1408),
+         # dW's tokens in slices; more than 1024 tokens into an fp32 dW whose sums would be too many
+         (4200, 136, 272), (2100, 72, 2096), (4099, 520, 1552), (2500, 4992, 528)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
