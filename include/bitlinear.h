@@ -599,11 +599,11 @@ bl_status bl_int8_linear_forward(const int8_t* xq, const float* sx, const int8_t
  *
  * dY [M,N] bf16, N a multiple of 8. dX [M,K] bf16 or NULL (skipped); dW [N,K] of
  * dw_dtype (BL_BF16 or BL_F32) or NULL (skipped). Sums in fp32, always added in
- * the same order; dW in fp32 joins partial sums of 1024 tokens. M == 0 writes
+ * the same order; dW in fp32 joins partial sums of at most 1024 tokens. M == 0 writes
  * dW = 0 (leaves it as it is with accumulate_dW).
  * workspace: at least bl_int8_linear_backward_workspace_size(M,N,K) bytes,
  * 16-byte aligned, no initialisation, one call at a time per workspace: x_hat and
- * w_hat, and fp32 parts of dX where its sums are split.
+ * w_hat, and fp32 parts of dX and of dW where their sums are split.
  * Errors: as L1, plus BL_ERR_WORKSPACE.
  */
 size_t bl_int8_linear_backward_workspace_size(int64_t M, int64_t N, int64_t K);

@@ -266,7 +266,7 @@ def product(xq, sx, wq, sw, dtype):
 MNK = [(1, 1, 16), (1, 6912, 2560), (2, 17, 48), (7, 100, 64), (8, 256, 80), (9, 33, 144), (16, 5001, 1040), (17, 16, 16),
        (31, 130, 4096), (32, 1000, 528), (33, 8, 16), (33, 1000, 128), (64, 129, 144), (100, 5001, 1040), (128, 128, 256),
        (129, 512, 272), (255, 257, 400), (256, 256, 128), (257, 24, 2560), (300, 6912, 512), (513, 1001, 896), (1000, 3, 32),
-       (2048, 1408, 512), (700, 9999, 240)]
+       (2048, 1408, 512), (700, 9999, 240), (2100, 8004, 64)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
