@@ -175,8 +175,8 @@ cudaError_t launch_norm_quant_backward(const void* dy, int dy_f32, const void* d
 
 // Product of INT8 operands with a scale per token and channel (k_int8.cu), and
 // its straight-through gradients. The backward's workspace holds both
-// operands' values in bf16, a factor of 1 and, where dX's sums are split, their
-// fp32 parts.
+// operands' values in bf16, a factor of 1 and, where dX's or dW's sums are split,
+// their fp32 parts.
 cudaError_t launch_int8_forward(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw, int64_t M,
                                 int64_t N, int64_t K, void* y, int y_f32, int* err, cudaStream_t s);
 size_t int8_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);

@@ -18,14 +18,16 @@
 // the bytes at the copy rate or the operations at twice the bf16 rate):
 //   tokens x channels x K    kernel   us      floor   bound by
 //   1 x 6912 x 2560          few      6.0     2.7     the start (2.2) and one HBM latency
-//   16 x 32000 x 2560, fp32  few      16.9    12.8    HBM (5.0 TB/s)
-//   64 x 32000 x 2560        mid      17.7    13.2    HBM
-//   64 x 6912 x 2560         mid      9.2     2.9     108 CTAs with 10 stages each (280 ns a stage), and their join
-//   64 x 2560 x 6912         mid      9.1     2.8     120 CTAs (6 per tile), 9 stages each
-//   333 x 5001 x 1040        tiles    8.5     1.4     one tile per pair: set-up, 9 stages, its end
-//   2048 x 8192 x 512        tiles    12.7    5.9     the epilogue
-//   4096 x 6912 x 2560       tiles    49.5    44.4    tensor cores (ncu: 76 % of the cycles; 5.84 rounds as 6)
-//   4096 x 32000 x 2560      tiles    217     205     tensor cores
+//   16 x 32000 x 2560, fp32  few      17.0    12.8    HBM (4.9 TB/s)
+//   64 x 32000 x 2560        mid      17.4    13.2    HBM
+//   64 x 6912 x 2560         mid      8.6     2.9     108 CTAs with 10 stages each (260 ns a stage: 4 in flight), their join
+//   64 x 2560 x 6912         mid      8.6     2.8     120 CTAs (6 per tile), 9 stages each
+//   333 x 5001 x 1040        tiles    8.3     1.4     one tile per pair: set-up, 9 stages, its end
+//   512 x 2560 x 6912        tiles    13.9    5.7     54 pairs with 54 stages each (165 ns a stage, of the loads)
+//   2048 x 2560 x 6912       tiles    26.5    22.2    tensor cores (two rounds of tiles as 1.73)
+//   2048 x 8192 x 512        tiles    12.2    5.9     the epilogue
+//   4096 x 6912 x 2560       tiles    47.9    44.4    tensor cores (5.84 rounds as 6)
+//   4096 x 32000 x 2560      tiles    208     205     tensor cores
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -977,11 +979,12 @@ cudaError_t launch_tiles(const CUtensorMap (&maps)[3], const TileParams& p, cuda
 template <typename TY, int BN>
 cudaError_t forward_tiles(const int8_t* xq, const int8_t* wq, TileParams p, cudaStream_t s) {
   p.ntiles = p.tiles_m * ((p.N + BN - 1) / BN);
-  // Boxes leave by TMA where rows start on 16 bytes; but of a large fp32 y whose rows do
-  // not start on 32 (1024 x 32004 x 1024: 46.2 us by TMA, 43.3 in whole sectors; 7788 x
-  // 10236 x 384: 99.8 and 81; 609 x 9652 x 208: 10.4 and 12.4).
+  // Boxes leave by TMA where rows start on 16 bytes, but not those of a y beyond some
+  // half of L2 (fp32; bf16: all of it) whose rows do not start on 32 (7788 x 10236 x 384
+  // fp32: 99.8 us by TMA, 77.7 in whole sectors; bf16, 10232: 63.4 and 56.9, and 16.6 and
+  // 18.2 at 3809 x 4520 x 336).
   const int64_t row = static_cast<int64_t>(p.N) * sizeof(TY);
-  const bool tma = row % 16 == 0 && (sizeof(TY) == 2 || row % 32 == 0 || p.M * row < int64_t(1) << 26);
+  const bool tma = row % 16 == 0 && (row % 32 == 0 || p.M * row < int64_t(1) << (sizeof(TY) == 4 ? 26 : 27));
   CUtensorMap maps[3] = {};
   if (!make_map(&maps[0], xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, p.M, p.K, kBlockK, 128) ||
       !make_map(&maps[1], wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, p.N, p.K, kBlockK, BN / 2) ||
@@ -1193,7 +1196,7 @@ cudaError_t launch_int8_forward(const int8_t* xq, const float* sx, const int8_t*
   return y_f32 ? forward_tiles<float>(xq, wq, p, wide.columns, s) : forward_tiles<__nv_bfloat16>(xq, wq, p, wide.columns, s);
 }
 
-// The values of x and of w in bf16, the factor 1, dX's partial sums.
+// The values of x and of w in bf16, the factor 1, dX's and dW's partial sums.
 size_t int8_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   return align256(static_cast<size_t>(M) * K * 2) + align256(static_cast<size_t>(N) * K * 2) + 256 +
          linear_grad_sum_bytes(M, N, K);

@@ -11,7 +11,7 @@
 //   Lse          tokens x vocab     h  K-major   W  K-major   K          max and sum of exp of the tile's columns, per token
 //   Dz           tokens x vocab     h  K-major   W  K-major   K          dz of a vocabulary piece, bf16 (two terms for fp32 dW)
 //   Grad: dH     tokens x K         dz K-major   W  MN-major  vocab      bf16, or fp32 partial sums over pieces and slices
-//   Grad: dW     vocab x K          dz MN-major  h  MN-major  tokens     bf16 or fp32
+//   Grad: dW     vocab x K          dz MN-major  h  MN-major  tokens     bf16 or fp32; of a linear with few tiles, fp32 sums over slices
 //
 // The backward walks the vocabulary in pieces: Dz forms the piece's logits
 // again and leaves its dz in the workspace (128 MiB at most), Grad multiplies it
