@@ -1212,6 +1212,8 @@ cudaError_t launch_int8_backward(const void* dY, const int8_t* xq, const float* 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   uint8_t* x = ws;
   uint8_t* w = x + align256(static_cast<size_t>(M) * K * 2);
+  if (M <= kInt8FewGrads)
+    return launch_int8_few_grads(dY, xq, sx, wq, sw, M, N, K, dX, dW, dw_is_f32, accumulate, reinterpret_cast<float*>(w), s);
   float* one = reinterpret_cast<float*>(w + align256(static_cast<size_t>(N) * K * 2));
   ValuesParams v{};
   v.q[0] = reinterpret_cast<const uint2*>(xq);

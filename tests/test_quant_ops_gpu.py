@@ -344,7 +344,9 @@ def test_int8_linear_scales_that_are_not_finite_stay_with_their_token_and_channe
 GRADS = [(1, 8, 16), (3, 64, 48), (16, 256, 512), (33, 1000, 128), (100, 136, 272), (257, 5000, 144), (700, 1408, 512),
          (64, 32000, 80), (1030, 264, 400), (2048, 512, 1408),
          # dW's tokens in slices; more than 1024 tokens into an fp32 dW whose sums would be too many
-         (4200, 136, 272), (2100, 72, 2096), (4099, 520, 1552), (2500, 4992, 528)]
+         (4200, 136, 272), (2100, 72, 2096), (4099, 520, 1552), (2500, 4992, 528),
+         # a few tokens: the codes' own kernel, one or more slices, ends inside its tiles
+         (2, 8, 2576), (7, 24, 16), (17, 40, 32), (32, 1000, 144), (31, 2056, 1040), (5, 11976, 272), (20, 6912, 2560)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -373,6 +375,26 @@ def test_int8_linear_gradients(M, N, K, dtype):
     bl.bl_int8_linear_backward(dY, xq, sx, wq, sw, None, alone.dW, accumulate_dW=True, workspace=alone.workspace)
     ok()
     close(alone.dW, d.t() @ x + start.double(), tol * (d.abs().t() @ x.abs() + start.double().abs()), "dW added")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M,N,K", [(5, 264, 48), (20, 1032, 80), (70, 136, 48), (2100, 72, 272)])
+def test_int8_linear_gradients_leave_the_neighbours_alone(M, N, K, dtype):
+    xq, wq, sx, sw = codes(M, K, seed=M), codes(N, K, seed=N), scales(M, 1), scales(N, 2)
+    dY = rnd(M, N, seed=3, dtype=BF)
+    n = bl.bl_int8_linear_backward_workspace_size(M, N, K)
+    hx = torch.full((M * K + 64,), 7.0, dtype=BF, device="cuda")
+    hw = torch.full((N * K + 64,), 7.0, dtype=dtype, device="cuda")
+    ws = torch.full((n + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+    dX, dW = hx[32 : 32 + M * K].view(M, K), hw[32 : 32 + N * K].view(N, K)
+    bl.bl_int8_linear_backward(dY, xq, sx, wq, sw, dX, dW, workspace=ws[256 : 256 + n])
+    ok()
+    x, w, d = (xq.float() * sx[:, None]).to(BF).double(), (wq.float() * sw[:, None]).to(BF).double(), dY.double()
+    close(dX, d @ w, (N / 16 + 64) * 2 * U * (d.abs() @ w.abs()), "dX")
+    close(dW, d.t() @ x, (M / 16 + 64) * 2 * U * (d.abs().t() @ x.abs()), "dW")
+    for hold, size in ((hx, M * K), (hw, N * K)):
+        assert bool((hold[:32] == 7).all()) and bool((hold[32 + size :] == 7).all())
+    assert bool((ws[:256] == 0xA5).all()) and bool((ws[256 + n :] == 0xA5).all())
 
 
 def test_int8_linear_gradient_against_differences():
