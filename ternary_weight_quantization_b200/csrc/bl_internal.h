@@ -191,12 +191,8 @@ size_t linear_grad_sum_bytes(int64_t M, int64_t N, int64_t K);
 cudaError_t launch_linear_grads(const void* dY, const void* x, const void* w, int64_t M, int64_t N, int64_t K, void* dX,
                                 void* dW, int dw_is_f32, int accumulate, float* one, float* sums, int* err,
                                 cudaStream_t s);
-// [M,K] in bf16 from fp32 partial sums of `rows` rows each, added in order.
-cudaError_t launch_join_sums(const float* sums, int64_t rows, int slices, int64_t M, int64_t K, void* out, cudaStream_t s);
 
-// The same gradients for up to kInt8FewGrads tokens, from the codes (k_int8_grad.cu).
-// sums: 2 N K bytes.
-constexpr int64_t kInt8FewGrads = 32;
+// The same gradients for up to 64 tokens, from the codes (k_int8_grad.cu). sums: 2 N K bytes.
 cudaError_t launch_int8_few_grads(const void* dY, const int8_t* xq, const float* sx, const int8_t* wq, const float* sw,
                                   int64_t M, int64_t N, int64_t K, void* dX, void* dW, int dw_is_f32, int accumulate,
                                   float* sums, cudaStream_t s);

@@ -1212,7 +1212,10 @@ cudaError_t launch_int8_backward(const void* dY, const int8_t* xq, const float* 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   uint8_t* x = ws;
   uint8_t* w = x + align256(static_cast<size_t>(M) * K * 2);
-  if (M <= kInt8FewGrads)
+  // Few tokens take the codes' own kernel: up to 32 in any case (32 x 6912 x 2560: 23.8 us
+  // for 30.0 by values in bf16), up to 64 where it is the launches that count (64 tokens, 512
+  // x 512: 6.0 for 9.7; 1000 x 2560: 12.2 for 13.2; 2560 x 2560: 21.5 for 17.9).
+  if (M <= 32 || (M <= 64 && N * K <= int64_t(5) << 19))
     return launch_int8_few_grads(dY, xq, sx, wq, sw, M, N, K, dX, dW, dw_is_f32, accumulate, reinterpret_cast<float*>(w), s);
   float* one = reinterpret_cast<float*>(w + align256(static_cast<size_t>(N) * K * 2));
   ValuesParams v{};

@@ -21,9 +21,11 @@
 // graph, inputs from HBM; floor by bytes; before: by values written in bf16 and the
 // products of k_xent.cu, which more tokens take):
 //   tokens x channels x K   us      floor   before
-//   1 x 6912 x 2560         17.1    8.1     31.4
-//   16 x 6912 x 2560        18.7    8.2     29.9
-//   32 x 6912 x 2560        24.3    8.2     29.9    (64: 45.8 for 31.1)
+//   1 x 6912 x 2560         16.3    8.1     31.5
+//   16 x 6912 x 2560        18.1    8.2     29.9
+//   32 x 6912 x 2560        23.8    8.2     30.0    (64: 45.8 for 31.1)
+//   2 x 25128 x 208         13.0    2.4     19.2    (its 148 slices joined by one thread a place: 22.4)
+//   64 x 512 x 512          6.0     0.2     9.7
 //   5 x 11976 x 2704        26      14.9    54.1
 //   16 x 32000 x 2560       102     62.7    134     (dW in fp32)
 //   13 x 368 x 1984         6.5     0.4     8.6
@@ -92,6 +94,10 @@ __device__ __forceinline__ void load_words(const int8_t* p, uint32_t (&w)[4]) {
 __device__ __forceinline__ void load_words(const int8_t* p, uint32_t (&w)[2]) {
   const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
   w[0] = v.x, w[1] = v.y;
+}
+
+__device__ __forceinline__ void load_words(const int8_t* p, uint32_t (&w)[1]) {
+  w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
 }
 
 // Eight columns of a channel of dW.
@@ -261,6 +267,35 @@ __global__ void __launch_bounds__(kGradThreads, 2) int8_few_grad_kernel(const Fe
   }
 }
 
+// dX from its slices. There may be few outputs of many slices, so 8 warps share 32
+// places (of 4 columns): each adds every eighth slice, and the first one their sums.
+__global__ void __launch_bounds__(256) int8_few_join_kernel(const float4* __restrict__ sums, int64_t vecs, int slices,
+                                                            uint2* __restrict__ dX) {
+  __shared__ float4 sh[8][32];
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + x;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (i < vecs) {
+    constexpr int kU = 4;
+    for (int s = y; s < slices; s += 8 * kU) {
+      float4 w[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        w[u] = s + 8 * u < slices ? sums[(s + 8 * u) * vecs + i] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int u = 0; u < kU; ++u) v.x += w[u].x, v.y += w[u].y, v.z += w[u].z, v.w += w[u].w;
+    }
+  }
+  sh[y][x] = v;
+  __syncthreads();
+  if (y > 0 || i >= vecs) return;
+#pragma unroll
+  for (int u = 1; u < 8; ++u) v.x += sh[u][x].x, v.y += sh[u][x].y, v.z += sh[u][x].z, v.w += sh[u][x].w;
+  dX[i] = make_uint2(pack_bf16x2(v.y, v.x), pack_bf16x2(v.w, v.z));
+}
+
 template <int kTok, typename TW>
 cudaError_t launch_few(FewGradParams p, cudaStream_t s) {
   using G = FewGrad<kTok>;
@@ -286,7 +321,7 @@ cudaError_t launch_int8_few_grads(const void* dY, const int8_t* xq, const float*
   p.K = static_cast<int>(K);
   p.dW = dW;
   p.accumulate = accumulate;
-  const int tok = M <= 16 ? 1 : 2, cols = 128 / tok;
+  const int tok = M <= 16 ? 1 : M <= 32 ? 2 : 4, cols = 128 / tok;
   p.tiles_k = static_cast<int>((K + cols - 1) / cols);
   // slices of the channels: two blocks per SM, 16 channels per warp at least, and
   // no more than the sums have room for (2 bytes per weight)
@@ -301,9 +336,12 @@ cudaError_t launch_int8_few_grads(const void* dY, const int8_t* xq, const float*
   }
   cudaError_t e;
   if (tok == 1) e = dw_is_f32 ? launch_few<1, float>(p, s) : launch_few<1, __nv_bfloat16>(p, s);
-  else e = dw_is_f32 ? launch_few<2, float>(p, s) : launch_few<2, __nv_bfloat16>(p, s);
+  else if (tok == 2) e = dw_is_f32 ? launch_few<2, float>(p, s) : launch_few<2, __nv_bfloat16>(p, s);
+  else e = dw_is_f32 ? launch_few<4, float>(p, s) : launch_few<4, __nv_bfloat16>(p, s);
   if (e != cudaSuccess || !p.sums) return e;
-  return launch_join_sums(sums, M, p.slices, M, K, dX, s);
+  const int64_t vecs = M * K / 4;
+  return launch_pdl(int8_few_join_kernel, dim3(static_cast<unsigned>((vecs + 31) / 32)), dim3(256), 0, s,
+                    reinterpret_cast<const float4*>(sums), vecs, p.slices, static_cast<uint2*>(dX));
 }
 
 }  // namespace bl

@@ -1251,10 +1251,6 @@ cudaError_t launch_xent_backward(const void* h, const void* W, const int64_t* ta
   return join_dh(sum, q.rows_pad, q.slices, M, K, dH, s);
 }
 
-cudaError_t launch_join_sums(const float* sums, int64_t rows, int slices, int64_t M, int64_t K, void* out, cudaStream_t s) {
-  return join_dh(sums, rows, slices, M, K, out, s);
-}
-
 // ---- the gradients of y = x w^T from operands in bf16: Grad alone, with dY in
 // the place of dz, x of h and w of the head
 namespace {

@@ -346,7 +346,8 @@ GRADS = [(1, 8, 16), (3, 64, 48), (16, 256, 512), (33, 1000, 128), (100, 136, 27
          # dW's tokens in slices; more than 1024 tokens into an fp32 dW whose sums would be too many
          (4200, 136, 272), (2100, 72, 2096), (4099, 520, 1552), (2500, 4992, 528),
          # a few tokens: the codes' own kernel, one or more slices, ends inside its tiles
-         (2, 8, 2576), (7, 24, 16), (17, 40, 32), (32, 1000, 144), (31, 2056, 1040), (5, 11976, 272), (20, 6912, 2560)]
+         (2, 8, 2576), (7, 24, 16), (17, 40, 32), (32, 1000, 144), (31, 2056, 1040), (5, 11976, 272), (20, 6912, 2560),
+         (33, 24, 48), (64, 1000, 2560), (50, 2056, 80), (64, 2568, 1040)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
