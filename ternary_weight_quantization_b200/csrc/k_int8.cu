@@ -946,8 +946,10 @@ bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType type, uint64
   if (!encode) return false;
   const cuuint64_t dims[2] = {inner, outer}, strides[1] = {row_bytes};
   const cuuint32_t box[2] = {box_inner, box_outer}, steps[2] = {1, 1};
+  // (Lines of 128 bytes, not pairs of them: where K is no multiple of 128 a box's rows lie
+  // on two lines each, 12 x 3149 x 6672 11.3 us for 13.1; else the same.)
   return encode(m, type, 2, const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename TY, int BN, bool kTma>
