@@ -1082,10 +1082,10 @@ int clusters_at_once(int share) {
   const bool keep = dev >= 0 && dev < 64;
   if (keep && known[dev][share]) return known[dev][share];
   constexpr int kOne = 128 * 1024;  // shared memory of which an SM holds one CTA's
-  static bool done[64] = {};
   auto kernel = int8_mid_kernel<__nv_bfloat16, 64>;
   int clusters = 0;
-  if (allow_smem(kernel, kOne, done) == cudaSuccess) {
+  // (each time: a launch sets the kernel's own size again)
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kOne) == cudaSuccess) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(share * device_sm_count()));
     cfg.blockDim = dim3(kMidThreads);
