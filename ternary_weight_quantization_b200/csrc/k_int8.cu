@@ -463,10 +463,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
 // ---------------------------------------------------------------- a few tokens
 // The weights are read once and hardly used: what counts is bytes in flight. A CTA
 // (two fit on an SM, of this kernel or of the next one, whose first loads then
-// overlap this one's end) takes tiles of 16 R channels in turn; up to four threads,
+// overlap this one's end) takes tiles of 16 R channels in turn; up to four warps,
 // each with every fourth stage, keep a ring of stages (256 of K: the channels' rows
 // and the tokens', 128-byte swizzled boxes) filled by TMA, across the ends of
-// tiles (one thread takes some 250 cycles for a stage's requests, which a CTA's
+// tiles (one of them takes some 250 cycles for a stage's requests, which a CTA's
 // share of HBM fills in fewer). R x S consumer warps: a
 // warp takes one group of 16 channels and every S-th stage, mma.sync.m16n8k32 on
 // operands that ldmatrix brings in the instruction's order; the S warps' INT32
