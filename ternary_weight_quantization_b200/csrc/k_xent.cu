@@ -62,6 +62,7 @@
 #include "bl_act8.cuh"
 #include "bl_device.cuh"
 #include "bl_internal.h"
+#include "bl_mma.cuh"
 
 namespace bl {
 namespace {
