@@ -47,6 +47,7 @@ gradients down to ``max_norm`` over all parameters (``bl_clip_grads``).
 
 from __future__ import annotations
 
+import bisect
 import math
 
 import torch
@@ -383,13 +384,18 @@ def clip_gradients(grads, max_norm: float):
     one tensor to two leaves), is replaced by a copy."""
     if not grads:
         raise ValueError("no gradients")
-    out, seen = [], set()
+    out, begins, ends = [], [], []  # and the memory of those so far, by address
     for g in grads:
         g = g.contiguous()
-        storage = g.untyped_storage().data_ptr()
-        if g.numel() and storage in seen:
-            g = g.clone()
-        seen.add(storage)
+        if g.numel():
+            begin = g.data_ptr()
+            i = bisect.bisect_right(ends, begin)
+            if i < len(begins) and begins[i] < begin + g.numel() * g.element_size():
+                g = g.clone()
+                begin = g.data_ptr()
+                i = bisect.bisect_right(ends, begin)
+            begins.insert(i, begin)
+            ends.insert(i, begin + g.numel() * g.element_size())
         out.append(g)
     norm = torch.empty(1, dtype=torch.float32, device=out[0].device)
     ws = torch.empty(max(b.bl_grad_norm_workspace_size(len(out)), 16), dtype=torch.uint8, device=norm.device)
