@@ -41,8 +41,9 @@ quantised once for all projections that read it (q, k and v; gate and up). The
 norm's result is then not rounded to bf16 in front of the quantiser. ``head8``
 runs the head on 8-bit codes of the last norm's output and of the head's rows
 (``bl_int8_linear_forward`` / ``bl_int8_linear_backward``, straight-through
-gradients); its logits go through torch's cross-entropy. ``train_lm`` scales the
-gradients down to ``max_norm`` over all parameters (``bl_clip_grads``).
+gradients); its logits go through torch's cross-entropy, under the same rule for
+targets outside the vocabulary. ``train_lm`` scales the gradients down to
+``max_norm`` over all parameters (``bl_clip_grads``).
 """
 
 from __future__ import annotations
@@ -308,6 +309,13 @@ class NormHead8Function(torch.autograd.Function):
         return (*_norm_gradients(dX, None, stream, gain, rstd, ctx.x_dtype), None, dW.to(ctx.w_dtype))
 
 
+def _mean_loss(logits, targets):
+    """Mean cross-entropy of logits [M, V] at targets [M], as HeadLossFunction's."""
+    held = (targets >= 0) & (targets < logits.shape[1])
+    total = torch.nn.functional.cross_entropy(logits, torch.where(held, targets, -100), ignore_index=-100, reduction="sum")
+    return total / held.sum().clamp(min=1)
+
+
 def _rmsnorm(x, g, eps):
     return x / torch.sqrt(torch.mean(x * x, dim=-1, keepdim=True) + eps) * g
 
@@ -368,7 +376,7 @@ def lm_loss(params: dict, ids: torch.Tensor, cfg, library_ops: bool = False, sav
     if head8:
         logits = NormHead8Function.apply(pending if fused_norms else None, h.reshape(-1, d), params["final_norm"],
                                          cfg.norm_eps, params["head"])
-        return torch.nn.functional.cross_entropy(logits, y_ids.reshape(-1))
+        return _mean_loss(logits, y_ids.reshape(-1))
     if fused_norms:
         h = h + pending.reshape(B, S, d)
     last = norm(h, params["final_norm"])
