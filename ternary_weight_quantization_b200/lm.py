@@ -281,17 +281,21 @@ class NormProjectionsFunction(torch.autograd.Function):
 class NormHead8Function(torch.autograd.Function):
     """Logits [M, V] (fp32) of a head [V, K] kept in 8 bits per row, from the RMS
     norm of the stream x + residual (as in NormProjectionsFunction) in 8 bits per
-    token."""
+    token. The gradients' call takes a multiple of 8 channels: rows of zeros fill
+    the head's codes up to that."""
 
     @staticmethod
     def forward(ctx, x, residual, gain, eps, head):
         (M, K), V = residual.shape, head.shape[0]
         gain, buf = _normed(x, residual, gain, eps)
-        wq = torch.empty((V, K), dtype=torch.int8, device=head.device)
-        sw = torch.empty(V, dtype=torch.float32, device=head.device)
-        b.bl_quantize_act(_operand(head.detach().to(torch.bfloat16)), wq, sw)
+        wq = torch.empty((-(-V // 8) * 8, K), dtype=torch.int8, device=head.device)
+        sw = torch.empty(wq.shape[0], dtype=torch.float32, device=head.device)
+        b.bl_quantize_act(_operand(head.detach().to(torch.bfloat16)), wq[:V], sw[:V])
+        if len(wq) > V:
+            wq[V:] = 0
+            sw[V:] = 0
         logits = torch.empty((M, V), dtype=torch.float32, device=head.device)
-        b.bl_int8_linear_forward(buf.xq, buf.sx, wq, sw, logits)
+        b.bl_int8_linear_forward(buf.xq, buf.sx, wq[:V], sw[:V], logits)
         ctx.save_for_backward(buf.sum, gain, buf.rstd, buf.xq, buf.sx, wq, sw)
         ctx.x_dtype = None if x is None else x.dtype
         ctx.w_dtype = head.dtype
@@ -301,12 +305,15 @@ class NormHead8Function(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, g):
         stream, gain, rstd, xq, sx, wq, sw = ctx.saved_tensors
-        (M, K), V = xq.shape, wq.shape[0]
+        (M, K), V, V8 = xq.shape, g.shape[1], wq.shape[0]
         dX = torch.empty((M, K), dtype=torch.bfloat16, device=g.device)
-        dW = torch.empty((V, K), dtype=torch.float32, device=g.device)
-        ws = torch.empty(max(b.bl_int8_linear_backward_workspace_size(M, V, K), 16), dtype=torch.uint8, device=g.device)
-        b.bl_int8_linear_backward(_operand(g.to(torch.bfloat16)), xq, sx, wq, sw, dX, dW, workspace=ws)
-        return (*_norm_gradients(dX, None, stream, gain, rstd, ctx.x_dtype), None, dW.to(ctx.w_dtype))
+        dW = torch.empty((V8, K), dtype=torch.float32, device=g.device)
+        ws = torch.empty(max(b.bl_int8_linear_backward_workspace_size(M, V8, K), 16), dtype=torch.uint8, device=g.device)
+        dY = g.to(torch.bfloat16)
+        if V8 > V:
+            dY = torch.nn.functional.pad(dY, (0, V8 - V))
+        b.bl_int8_linear_backward(_operand(dY), xq, sx, wq, sw, dX, dW, workspace=ws)
+        return (*_norm_gradients(dX, None, stream, gain, rstd, ctx.x_dtype), None, dW[:V].to(ctx.w_dtype))
 
 
 def _mean_loss(logits, targets):

@@ -1,5 +1,5 @@
 """The decoder LM with an 8-bit head, with the library's calls replaced by plain ones:
-targets outside the vocabulary."""
+targets outside the vocabulary, and vocabularies of any size."""
 
 import dataclasses
 import math
@@ -79,3 +79,41 @@ def test_mean_over_the_targets_inside():
     # fp32: a log-sum-exp of 33 terms and a sum of at most 40 losses; e^z's relative error is that of z
     assert abs(float(loss.detach()) - float(want)) <= (40 + 33 + 8) * 2.0 ** -24 * float(z.abs().amax() + math.log(33))
     assert bool(((d.double() - grad).abs() <= (33 + 16 * 4) * 2.0 ** -24 / n).all())
+
+
+@pytest.mark.parametrize("vocab", [97, 103, 121, 128])
+def test_a_vocabulary_of_any_size_has_gradients(vocab):
+    cfg = dataclasses.replace(LM_TINY, vocab=vocab)
+    ids = lm_batches(cfg, seed=3)[0]
+    loss, grads = model(cfg, ids, head8=True)
+    other, want = model(cfg, ids)
+    assert abs(float(loss.detach()) - float(other.detach())) <= NEAR
+    assert grads["head"].shape == (vocab, cfg.d)
+    # dW = dz^T x_hat: x_hat is off by 4 / 254 of its norm at most, dz by exp(NEAR) - 1 of
+    # each probability, so of a row's norm of about 1 by that times sqrt(1 / vocab), 0.02
+    assert float((grads["head"] - want["head"]).norm()) <= 0.04 * float(want["head"].norm())
+
+
+@pytest.mark.parametrize("V", [97, 100, 104])
+def test_norm_head8_gradients_are_the_products(V):
+    """NormHead8Function against the formula on the same codes."""
+    M, K = 10, 64
+    g = torch.Generator().manual_seed(V)
+    x, r = torch.randn(M, K, generator=g).to(torch.bfloat16).float(), torch.randn(M, K, generator=g)
+    gain, head = 1 + 0.2 * torch.randn(K, generator=g), 0.1 * torch.randn(V, K, generator=g)
+    leaves = [t.requires_grad_(True) for t in (x, r, gain, head)]
+    logits = plm.NormHead8Function.apply(*leaves[:3], 1e-6, head)
+    assert logits.shape == (M, V)
+    dy = torch.randn(M, V, generator=g).to(torch.bfloat16).float()
+    got = torch.autograd.grad(logits, leaves, dy)
+    total = (x + r).detach().double()
+    rstd = torch.rsqrt(total.square().mean(1, keepdim=True) + 1e-6)
+    y = total * rstd * gain.detach().double()
+    a = y.abs().amax(1, keepdim=True)
+    x_hat = torch.round(y * 127 / a) * (a / 127)
+    assert got[3].shape == (V, K)
+    # x_hat in bf16 once, and a code next to a tie that fp32 leaves elsewhere
+    size = dy.double().abs().t() @ x_hat.abs()
+    step = dy.double().abs().t() @ (a / 127).expand(M, K)
+    assert bool(((got[3].double() - dy.double().t() @ x_hat).abs() <= 1.01 * 2.0 ** -8 * size + 0.02 * step).all())
+    assert all(bool(t.isfinite().all()) and bool(t.any()) for t in got)
