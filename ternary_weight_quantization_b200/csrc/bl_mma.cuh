@@ -18,6 +18,13 @@ __device__ __forceinline__ bool elect_one() {
   return yes != 0;
 }
 
+// A bounded wait of a whole (converged) warp, decided by all of its lanes: where the wait
+// runs out, or another warp gives up, between two lanes' looks at the barrier, no lane
+// goes on alone to an instruction that takes the whole warp.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err));
+}
+
 // Single-CTA (cta_group::1) forms.
 __device__ __forceinline__ void tmem_alloc_one(uint32_t* dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)), "r"(ncols)

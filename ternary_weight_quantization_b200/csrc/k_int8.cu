@@ -202,12 +202,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   pdl_wait_primary();
   pdl_launch_dependents();
 
+  // a warp's; a failed wait also stops the peer CTA's
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (mbar_wait(bar, parity, abort_flag, p.err)) return true;
+    if (mbar_wait_warp(bar, parity, abort_flag, p.err)) return true;
     st_cluster_u32(map_to_rank(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u), 1u);
     return false;
   };
-  auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };  // a warp's
   auto lead = [&](uint64_t* bar) -> uint32_t { return map_to_rank(smem_u32(bar), 0); };
   const int nkb = (p.K + kBlockK - 1) / kBlockK;
   // tokens fastest: the pairs at work share few tiles of the weights
@@ -223,7 +223,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     for (int u = pair; ok && u < p.ntiles; u += npairs) {
       const int a0 = tile_row(u), b0 = tile_col(u) + static_cast<int>(rank) * (BN / 2);
       for (int kb = 0; kb < nkb; ++kb) {
-        if (!wait_all(&empty[stage], phase ^ 1)) {
+        if (!wait(&empty[stage], phase ^ 1)) {
           ok = false;
           break;
         }
@@ -259,11 +259,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       uint32_t phase = 0, buf_phase = 0;
       bool ok = true;
       for (int u = pair; ok && u < p.ntiles; u += npairs) {
-        if (!wait_all(&tmem_empty[buf], buf_phase ^ 1)) break;
+        if (!wait(&tmem_empty[buf], buf_phase ^ 1)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * 256);
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!wait_all(&full[stage], phase)) {
+          if (!wait(&full[stage], phase)) {
             ok = false;
             break;
           }
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(Few<kTok, R>::kThreads, 2)
     bool ok = true;
     for (; it < mine; it += G::kLoaders) {
       const int stage = it % kStages;
-      if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], (it / kStages & 1) ^ 1, abort_flag, p.err))) {
+      if (!mbar_wait_warp(&empty[stage], (it / kStages & 1) ^ 1, abort_flag, p.err)) {
         ok = false;
         break;
       }
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(Few<kTok, R>::kThreads, 2)
     int acc[kTok][4] = {};
     for (uint32_t st = (share - base) & (S - 1); st < static_cast<uint32_t>(nst); st += S) {
       const uint32_t stage = (base + st) % kStages;
-      if (!mbar_wait(&full[stage], (base + st) / kStages & 1, abort_flag, p.err)) return;
+      if (!mbar_wait_warp(&full[stage], (base + st) / kStages & 1, abort_flag, p.err)) return;
       const uint32_t at = smem_u32(smem) + stage * G::kStageBytes;
       const int left = steps - static_cast<int>(st) * 8;
 #pragma unroll
@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(Few<kTok, R>::kThreads, 2)
     }
     // two buffers in turn: a warp writes one again only after a join that every
     // reader of it has reached; a single one only when all have read it
-    if (G::kBufs == 1 && tile > 0 && !mbar_wait(read, (tile - 1) & 1, abort_flag, p.err)) return;
+    if (G::kBufs == 1 && tile > 0 && !mbar_wait_warp(read, (tile - 1) & 1, abort_flag, p.err)) return;
     int* sums = reinterpret_cast<int*>(smem + G::kOffSums) + tile % G::kBufs * G::kSums;
     int* own = sums + share * kN * kM + group * 16;
     const int g = lane >> 2, t = lane & 3;
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(Few<kTok, R>::kThreads, 2)
       for (int j = 0; j < 4; ++j) own[(8 * i + 2 * t + (j & 1)) * kN + g + (j >> 1) * 8] = acc[i][j];
     __syncwarp();
     if (lane == 0) mbar_arrive(joined);
-    if (!mbar_wait(joined, tile & 1, abort_flag, p.err)) return;
+    if (!mbar_wait_warp(joined, tile & 1, abort_flag, p.err)) return;
     for (int i = threadIdx.x - 32 * G::kLoaders; i < kN * kM; i += 32 * G::kWarps) {
       const int n = u * kN + i % kN, m = i / kN;
       if (m >= p.M || n >= p.N) continue;
@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(kMidThreads)
     int kb = 0;
     for (; kb < nkb; ++kb) {
       const int s = kb % kStages;
-      if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], (kb / kStages & 1) ^ 1, abort_flag, p.err))) break;
+      if (!mbar_wait_warp(&empty[s], (kb / kStages & 1) ^ 1, abort_flag, p.err)) break;
       if (one) {
         mbar_arrive_expect_tx(&full[s], G::kStageBytes);
         uint8_t* at = smem + s * G::kStageBytes;
@@ -780,7 +780,7 @@ __global__ void __launch_bounds__(kMidThreads)
     const uint64_t ad0 = smem_desc_sw128(s0, 16, 1024), bd0 = smem_desc_sw128(s0 + G::kW, 16, 1024);
     for (int kb = 0; kb < nkb; ++kb) {
       const int s = kb % kStages;
-      if (!__all_sync(0xffffffffu, mbar_wait(&full[s], kb / kStages & 1, abort_flag, p.err))) break;
+      if (!mbar_wait_warp(&full[s], kb / kStages & 1, abort_flag, p.err)) break;
       tc_fence_after();
       const uint64_t at = static_cast<uint64_t>(s) * (G::kStageBytes >> 4);
       if (one) {
@@ -803,7 +803,7 @@ __global__ void __launch_bounds__(kMidThreads)
   bool ok = true;
   TY* y = static_cast<TY*>(p.y) + static_cast<int64_t>(t0) * p.N;
   if (warp >= 2) {
-    ok = mbar_wait(done, 0, abort_flag, p.err);
+    ok = mbar_wait_warp(done, 0, abort_flag, p.err);
     tc_fence_after();
   } else if (lane == 0) {
     mbar_drain(done, 0);  // nothing reads the ring any more
