@@ -380,12 +380,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
   pdl_wait_primary();
   pdl_launch_dependents();
 
+  // a warp's; a failed wait also stops the peer CTA's
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (mbar_wait(bar, parity, abort_flag, p.err)) return true;
+    if (mbar_wait_warp(bar, parity, abort_flag, p.err)) return true;
     st_cluster_u32(map_to_rank(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u), 1u);
     return false;
   };
-  auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };  // a warp's
   auto lead = [&](uint64_t* bar) -> uint32_t { return map_to_rank(smem_u32(bar), 0); };
 
   if (warp == kWarpLoad) {
@@ -411,7 +411,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
       // cycles that the tensor cores take for one
       auto each = [&](int n, auto load) {
         for (int kb = 0; kb < n; ++kb) {
-          if (!wait_all(&empty[stage], phase ^ 1)) {
+          if (!wait(&empty[stage], phase ^ 1)) {
             ok = false;
             return;
           }
@@ -497,14 +497,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Geo<P>::kThreads, 1)
       for (int i = 0; ok && next_tile(p, pair, npairs, i, u); ++i) {
         const Tile t = decode<P, BN>(p, u);
         if (t.nkb == 0) continue;
-        if (!wait_all(&tmem_empty[buf], buf_phase ^ 1)) break;
+        if (!wait(&tmem_empty[buf], buf_phase ^ 1)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * kTile);
         auto each = [&](auto a_mn, auto b_mn) {
           constexpr bool kAMn = decltype(a_mn)::value, kBMn = decltype(b_mn)::value;
           const uint64_t ad0 = operand_desc(s0, kAMn), bd0 = operand_desc(s0 + 2 * kBox, kBMn);
           for (int kb = 0; kb < t.nkb; ++kb) {
-            if (!wait_all(&full[stage], phase)) {
+            if (!wait(&full[stage], phase)) {
               ok = false;
               return;
             }

@@ -23,7 +23,7 @@ def test_the_warps_wait_votes():
     assert "__all_sync(0xffffffffu, mbar_wait(" in body
 
 
-@pytest.mark.parametrize("name", ["k_int8.cu"])
+@pytest.mark.parametrize("name", ["k_int8.cu", "k_xent.cu"])
 def test_waits_are_the_warps(name):
     text = code(name)
     assert re.search(r"\bmbar_wait_warp\(", text)
