@@ -28,3 +28,27 @@ def test_waits_are_the_warps(name):
     text = code(name)
     assert re.search(r"\bmbar_wait_warp\(", text)
     assert not re.findall(r"\bmbar_wait\([^\n]*", text), "a wait that each lane decides for itself"
+
+
+def test_the_layers_products_keep_their_warps_together():
+    """k_gemm.cu: one lane multiplies, in a branch of its own; every other role's lanes
+    decide together, on the wait or (loads, rebuilding) at the end of the tile."""
+    text = code("k_gemm.cu")
+    kernel = text[text.index("auto agreed = "):]
+    kernel = kernel[:kernel.index("tmem_dealloc_pair(")]
+    own = kernel.index("if (leader && lane == 0) {", kernel.index("warp == kWarpMma"))
+    end = kernel.index("mma_commit_pair(done_bar", own)
+    waits = list(re.finditer(r"(\S+ ?\S*?)\bwait\((&?\w+)", kernel))
+    assert len(waits) == 6
+    for m in waits:
+        assert own < m.start() < end or m.group(1).endswith("agreed(") or kernel[:m.end()].rstrip().endswith(
+            ("ok &= wait(&empty", "ok &= wait(&src_full")), m.group(0)
+    # a loop whose lanes may differ ends by a vote, and has no other way out
+    assert kernel.count("agreed(ok) && next_tile(") == kernel.count("ok &= wait(") == 2
+    for part in kernel.split("agreed(ok) && next_tile(")[1:]:
+        assert "break" not in part[:part.index("phase ^= 1;", part.index("ok &= wait("))]
+    # who failed loads nothing and arrives nowhere
+    assert len(re.findall(r"lane == 0 && ok\) (?:issued_parity|mbar_arrive_cluster)", kernel)) == 2
+    stage = text[text.index("void load_stage("):]
+    stage = stage[:stage.index("\ntemplate") if "\ntemplate" in stage else stage.index("\n}\n")]
+    assert "if (lane == 0 && ok) {" in stage and "if (ok) cp_async_8(" in stage and "if (ok) cp_async_mbar_arrive(" in stage
