@@ -33,6 +33,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 
@@ -1074,34 +1075,45 @@ cudaError_t forward_few(const int8_t* xq, const int8_t* wq, const FewParams& p, 
   return p.M <= 16 ? forward_few<TY, 2>(xq, wq, p, s) : forward_few<TY, 4>(xq, wq, p, s);
 }
 
+// Shared memory of which an SM holds one CTA's: what the narrow tiles' kernels may ask
+// for, as much as the question of how many clusters fit does. It is set here alone and
+// always to this, so that no host thread takes from another what it is about to use.
+constexpr int kMidLimit = 128 * 1024;
+
+template <typename TY, int NT>
+cudaError_t allow_mid() {
+  static_assert(Mid<NT>::kSmemBytes <= kMidLimit, "shared memory");
+  static bool done[64] = {};
+  return allow_smem(int8_mid_kernel<TY, NT>, kMidLimit, done);
+}
+
 // Clusters of `share` CTAs that fit at once with an SM for each CTA (a cluster lies
-// within one GPC: 15 of 8, 33 of 4).
+// within one GPC: 15 of 8, 33 of 4). An answer is kept; where the question fails, what
+// the SMs alone allow serves this call.
 int clusters_at_once(int share) {
-  static int known[64][kMidShare + 1] = {};
+  static std::atomic<int> known[64][kMidShare + 1] = {};
   int dev = 0;
   cudaGetDevice(&dev);
   const bool keep = dev >= 0 && dev < 64;
-  if (keep && known[dev][share]) return known[dev][share];
-  constexpr int kOne = 128 * 1024;  // shared memory of which an SM holds one CTA's
-  auto kernel = int8_mid_kernel<__nv_bfloat16, 64>;
+  if (keep)
+    if (const int n = known[dev][share].load(std::memory_order_relaxed)) return n;
   int clusters = 0;
-  // (each time: a launch sets the kernel's own size again)
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kOne) == cudaSuccess) {
+  if (allow_mid<__nv_bfloat16, 64>() == cudaSuccess) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(share * device_sm_count()));
     cfg.blockDim = dim3(kMidThreads);
-    cfg.dynamicSmemBytes = kOne;
+    cfg.dynamicSmemBytes = kMidLimit;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = share;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess) clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, int8_mid_kernel<__nv_bfloat16, 64>, &cfg) != cudaSuccess) clusters = 0;
   }
   cudaGetLastError();
-  if (clusters <= 0) clusters = device_sm_count() / share;
-  if (keep) known[dev][share] = clusters;
+  if (clusters <= 0) return device_sm_count() / share;
+  if (keep) known[dev][share].store(clusters, std::memory_order_relaxed);
   return clusters;
 }
 
@@ -1146,16 +1158,14 @@ cudaError_t launch_clusters(void (*kernel)(Params...), int grid, int cluster, in
 template <typename TY, int NT>
 cudaError_t launch_mid(const int8_t* xq, const int8_t* wq, MidParams p, cudaStream_t s) {
   using G = Mid<NT>;
-  auto kernel = int8_mid_kernel<TY, NT>;
-  static bool done[64] = {};
-  if (cudaError_t e = allow_smem(kernel, G::kSmemBytes, done); e != cudaSuccess) return e;
+  if (cudaError_t e = allow_mid<TY, NT>(); e != cudaSuccess) return e;
   CUtensorMap x, w;
   if (!make_map(&x, xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, p.M, p.K, kBlockK, NT) ||
       !make_map(&w, wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, p.N, p.K, kBlockK, 128))
     return cudaErrorInvalidValue;
   p.tiles_n = (p.N + 127) / 128;
   const int tiles = p.tiles_n * ((p.M + NT - 1) / NT);
-  return launch_clusters(kernel, tiles * p.share, p.share, kMidThreads, G::kSmemBytes, s, x, w, p);
+  return launch_clusters(int8_mid_kernel<TY, NT>, tiles * p.share, p.share, kMidThreads, G::kSmemBytes, s, x, w, p);
 }
 
 template <typename TY>
