@@ -425,25 +425,27 @@ __device__ __forceinline__ void load_stage(const GemmParams& p, const OpParams& 
       // the 32-byte-swizzled layout the TMA path produces; every lane's copies
       // hold the phase open until they land, lane 0 gives the one arrival
       constexpr int kChunks = (op == Op::Fwd) ? 16 : 8;  // per lane
+      if (ok) {
 #pragma unroll
-      for (int it = 0; it < kChunks; ++it) {
-        const int c = lane + 32 * it;
-        const int row = c >> 2, part = c & 3;
-        bool valid;
-        const uint8_t* src;
-        if constexpr (op == Op::Fwd) {
-          // packed rows a0..a0+127, bytes [kb*32, kb*32+32)
-          valid = (a0 + row < P.rows_a) && (r0 + part * 32 < P.red);
-          src = p.packed + static_cast<int64_t>(a0 + row) * kq + kb * 32 + part * 8;
-        } else {
-          // packed rows (n) r0..r0+63, bytes covering k in [a0, a0+128)
-          valid = (r0 + row < P.red) && (a0 + part * 32 < P.rows_a);
-          src = p.packed + static_cast<int64_t>(r0 + row) * kq + a0 / 4 + part * 8;
+        for (int it = 0; it < kChunks; ++it) {
+          const int c = lane + 32 * it;
+          const int row = c >> 2, part = c & 3;
+          bool valid;
+          const uint8_t* src;
+          if constexpr (op == Op::Fwd) {
+            // packed rows a0..a0+127, bytes [kb*32, kb*32+32)
+            valid = (a0 + row < P.rows_a) && (r0 + part * 32 < P.red);
+            src = p.packed + static_cast<int64_t>(a0 + row) * kq + kb * 32 + part * 8;
+          } else {
+            // packed rows (n) r0..r0+63, bytes covering k in [a0, a0+128)
+            valid = (r0 + row < P.red) && (a0 + part * 32 < P.rows_a);
+            src = p.packed + static_cast<int64_t>(r0 + row) * kq + a0 / 4 + part * 8;
+          }
+          const int dst = row * 32 + ((((part >> 1) ^ (row >> 2)) & 1) << 4) + ((part & 1) << 3);
+          cp_async_8(sSrc + dst, valid ? src : p.packed, valid ? 8u : 0u);
         }
-        const int dst = row * 32 + ((((part >> 1) ^ (row >> 2)) & 1) << 4) + ((part & 1) << 3);
-        if (ok) cp_async_8(sSrc + dst, valid ? src : p.packed, valid ? 8u : 0u);
+        cp_async_mbar_arrive(src_full);
       }
-      if (ok) cp_async_mbar_arrive(src_full);
       __syncwarp();
       if (lane == 0 && ok) mbar_arrive(src_full);
     }

@@ -51,4 +51,7 @@ def test_the_layers_products_keep_their_warps_together():
     assert len(re.findall(r"lane == 0 && ok\) (?:issued_parity|mbar_arrive_cluster)", kernel)) == 2
     stage = text[text.index("void load_stage("):]
     stage = stage[:stage.index("\ntemplate") if "\ntemplate" in stage else stage.index("\n}\n")]
-    assert "if (lane == 0 && ok) {" in stage and "if (ok) cp_async_8(" in stage and "if (ok) cp_async_mbar_arrive(" in stage
+    assert "if (lane == 0 && ok) {" in stage
+    copies = stage[stage.index("if (ok) {"):]
+    copies = copies[:copies.index("__syncwarp();")]
+    assert stage.count("cp_async_8(") == copies.count("cp_async_8(") == copies.count("cp_async_mbar_arrive(") == 1
