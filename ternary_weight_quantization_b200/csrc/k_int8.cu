@@ -20,13 +20,14 @@
 //   1 x 6912 x 2560          few      6.0     2.7     the start (2.2) and one HBM latency
 //   16 x 32000 x 2560, fp32  few      17.0    12.8    HBM (4.9 TB/s)
 //   64 x 32000 x 2560        mid      17.4    13.2    HBM
-//   64 x 6912 x 2560         mid      8.6     2.9     108 CTAs with 10 stages each (260 ns a stage: 4 in flight), their join
-//   64 x 2560 x 6912         mid      8.6     2.8     120 CTAs (6 per tile), 9 stages each
-//   333 x 5001 x 1040        tiles    8.3     1.4     one tile per pair: set-up, 9 stages, its end
-//   512 x 2560 x 6912        tiles    13.9    5.7     54 pairs with 54 stages each (165 ns a stage, of the loads)
-//   2048 x 2560 x 6912       tiles    26.5    22.2    tensor cores (two rounds of tiles as 1.73)
+//   64 x 6912 x 2560         mid      8.5     2.9     108 CTAs with 10 stages each (260 ns a stage: 4 in flight), their join
+//   64 x 2560 x 6912         mid      8.5     2.8     120 CTAs (6 per tile), 9 stages each
+//   333 x 5001 x 1040        tiles    8.1     1.4     one tile per pair: set-up, 9 stages, its end
+//   768 x 768 x 16384        mid      21.2    5.9     144 CTAs reading 226 MB from L2
+//   512 x 2560 x 6912        tiles    13.8    5.7     54 pairs with 54 stages each (165 ns a stage, of the loads)
+//   2048 x 2560 x 6912       tiles    26.1    22.2    tensor cores (two rounds of tiles as 1.73)
 //   2048 x 8192 x 512        tiles    12.2    5.9     the epilogue
-//   4096 x 6912 x 2560       tiles    47.9    44.4    tensor cores (5.84 rounds as 6)
+//   4096 x 6912 x 2560       tiles    47.2    44.4    tensor cores (5.84 rounds as 6)
 //   4096 x 32000 x 2560      tiles    208     205     tensor cores
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -1121,7 +1122,8 @@ int clusters_at_once(int share) {
 // the nanoseconds that follow from it: 260 per stage of a CTA, 550 + 75 per CTA for a
 // join, 1300 where the clusters do not fit one CTA to an SM (64 tokens, 17 tiles, 32
 // stages: 13.5 us alone, 9.8 over 2 CTAs, 7.9 over 4, 7.5 over 6, 8.5 over 8; 15 tiles:
-// 7.3 over 8).
+// 7.3 over 8). There is no term for what many tiles read from L2: 768 x 768 x 16384 takes
+// 21.2 us where this says 17.3 (in wide tiles 24.4, so the choice is right all the same).
 struct MidPlan {
   int share;
   int64_t ns;
