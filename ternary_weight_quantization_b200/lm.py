@@ -32,7 +32,8 @@ inputs are kept in 8 bits with ``saved8``), the SwiGLU gating
 for the backward, not in fp32) and the LM head with the cross-entropy
 (``bl_linear_xent_forward`` / ``bl_linear_xent_backward``: no logits). The head
 then takes the last norm's output and its weights in bf16, and a target outside
-the vocabulary leaves its token out of the mean.
+the vocabulary leaves its token out of the mean. (In the middle of a sequence it is
+also the next token's id, which then embeds as zeros.)
 
 With ``fused_norms`` too, what lies between two blocks' projections is one pass
 (``bl_norm_quant_forward`` / ``bl_norm_quant_backward``): the last projection's
@@ -351,7 +352,8 @@ def lm_loss(params: dict, ids: torch.Tensor, cfg, library_ops: bool = False, sav
     dh = d // H
     x_ids, y_ids = ids[:, :S], ids[:, 1:]
     embed = params["embed"]
-    one_hot = torch.nn.functional.one_hot(x_ids.reshape(-1), embed.shape[0]).to(embed.dtype)
+    # an id outside the vocabulary (a padded batch: its targets are left out) embeds as zeros
+    one_hot = (x_ids.reshape(-1, 1) == torch.arange(embed.shape[0], device=ids.device)).to(embed.dtype)
     h = (one_hot @ embed).reshape(B, S, d)
     causal = torch.ones(S, S, dtype=torch.bool, device=ids.device).tril()
     bl = BitLinearFunction.apply
