@@ -317,11 +317,16 @@ class NormHead8Function(torch.autograd.Function):
         return (*_norm_gradients(dX, None, stream, gain, rstd, ctx.x_dtype), None, dW[:V].to(ctx.w_dtype))
 
 
+def _left_out(targets, vocab):
+    """targets with those outside the vocabulary as the one that the cross-entropy ignores."""
+    return torch.where((targets >= 0) & (targets < vocab), targets, -100)
+
+
 def _mean_loss(logits, targets):
     """Mean cross-entropy of logits [M, V] at targets [M], as HeadLossFunction's."""
-    held = (targets >= 0) & (targets < logits.shape[1])
-    total = torch.nn.functional.cross_entropy(logits, torch.where(held, targets, -100), ignore_index=-100, reduction="sum")
-    return total / held.sum().clamp(min=1)
+    targets = _left_out(targets, logits.shape[1])
+    total = torch.nn.functional.cross_entropy(logits, targets, ignore_index=-100, reduction="sum")
+    return total / (targets >= 0).sum().clamp(min=1)
 
 
 def _rmsnorm(x, g, eps):
@@ -391,7 +396,7 @@ def lm_loss(params: dict, ids: torch.Tensor, cfg, library_ops: bool = False, sav
     last = norm(h, params["final_norm"])
     if library_ops:
         return HeadLossFunction.apply(last, params["head"], y_ids.reshape(-1))
-    return torch.nn.functional.cross_entropy(last @ params["head"].T, y_ids.reshape(-1))
+    return torch.nn.functional.cross_entropy(last @ params["head"].T, _left_out(y_ids.reshape(-1), params["head"].shape[0]))
 
 
 def clip_gradients(grads, max_norm: float):

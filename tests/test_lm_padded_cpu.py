@@ -28,6 +28,21 @@ def test_a_padded_batch_is_the_short_batch(monkeypatch, how, pad):
     assert all(bool(g.isfinite().all()) for g in got.values())
 
 
+@pytest.mark.parametrize("pad", [-100, -1, LM_TINY.vocab])
+def test_the_harness_leaves_padding_out_too(monkeypatch, pad):
+    """The model in plain torch around the layers, in 64 bits."""
+    from ternary_weight_quantization_b200 import lm
+    monkeypatch.setattr(lm.BitLinearFunction, "apply", staticmethod(lambda x, w: x @ w.T))
+    init, ids = plain_lm.case(LM_TINY, 2)
+    params = {n: t.double().requires_grad_(True) for n, t in init.items()}
+    padded = torch.full_like(ids, pad)
+    padded[:, :12] = ids[:, :12]
+    loss, want = lm.lm_loss(params, padded, LM_TINY), lm.lm_loss(params, ids[:, :12], LM_TINY)
+    # the same terms, in sums of at most 128 and 34
+    assert abs(float(loss.detach()) - float(want.detach())) <= (128 + 34) * 2.0 ** -52 * float(want.detach())
+    assert all(bool(g.isfinite().all()) for g in torch.autograd.grad(loss, list(params.values())))
+
+
 def test_ids_inside_embed_as_before():
     ids = torch.tensor([[0, 3, 127, 5]])
     embed = torch.randn(128, 64)
